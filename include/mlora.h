@@ -418,6 +418,102 @@ mlora_status mlora_merge(const mlora_pool* pool, int32_t adapter_id, int32_t pro
                          void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Paged 8-bit key/value cache and the attention that reads it: what a layer
+ * does with the keys and values that its (multi-LoRA) projections made.
+ *
+ * A page holds `block` consecutive tokens of one sequence, for every
+ * key/value head, in one layer.  A channel is an e4m3 code (sign, 4 exponent
+ * bits, 3 fraction bits, largest 448, no infinities); a page and head has
+ * one scale for its keys and one for its values, each a power of two between
+ * 2^-64 and 2^119, and code c stands for c * scale, which bf16 holds exactly.
+ *   k:       device uint8 [n_layers][n_blocks][kv_heads][block][dim]
+ *   v:       device uint8 [n_layers][n_blocks][kv_heads][block/16][dim][16]
+ *            (16 tokens of one channel are contiguous: an operand of the
+ *            product with the probabilities is then one 16-byte load)
+ *   k_scale, v_scale: device float [n_layers][n_blocks][kv_heads]
+ * all caller-owned and densely packed, k and v 16-byte aligned.
+ *
+ * A batch names n_seq sequences and their new rows (queries, or new keys and
+ * values): sequence i has rows row_off[i] .. row_off[i+1]-1, m of them, and
+ * kv_len[i] tokens with its new ones, so its row j stands at position
+ * kv_len[i] - m + j, and token t lies in page table[i][t / block].
+ *   table:   device int32 [n_seq][table_stride], the first `width` entries used
+ *   kv_len:  device int32 [n_seq]
+ *   row_off: device int32 [n_seq + 1], row_off[0] = 0, row_off[n_seq] = n_rows
+ * A sequence without rows (an idle slot) is passed over.  max_new is an upper
+ * bound of the rows of one sequence; it only sizes launches (n_rows is always
+ * a valid bound).
+ *
+ * What only the device knows cannot be refused without a sync: a page id
+ * outside [0, n_blocks) or past `width` is not followed (append drops its
+ * tokens, read gives NaN, attention gives NaN in the rows that see it), and
+ * rows at a negative position (kv_len < m) are dropped by append, read as
+ * NaN, and see nothing in attention.
+ * ------------------------------------------------------------------------- */
+typedef struct mlora_kv_cache {
+  int32_t n_layers; /* >= 1                                                   */
+  int32_t kv_heads; /* key/value heads, 1 .. 1024                             */
+  int32_t dim;      /* channels of a head: a multiple of 16 up to 256         */
+  int32_t block;    /* tokens of a page: 16, 32, 64, 128 or 256               */
+  int64_t n_blocks; /* pages of a layer, 1 .. 2^31 - 1                        */
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} mlora_kv_cache;
+
+typedef struct mlora_kv_batch {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* row_off;
+  int32_t n_seq;
+  int32_t width;        /* pages of a sequence at most; width * block <= 2^30 */
+  int32_t table_stride; /* entries between two sequences of table, >= width   */
+  int32_t n_rows;
+  int32_t max_new;      /* 1 .. n_rows (0 with n_rows 0)                      */
+} mlora_kv_batch;
+
+/* Quantises the batch's new keys and values into its pages of `layer`.
+ *   k, v: device bf16, channel c of head h of row r at
+ *         r * row_stride + h * head_stride + c (strides in elements, the same
+ *         for both), so a slice of a joint projection's output can be passed.
+ * A page and head takes the least scale whose 448 covers its new tokens; a
+ * page that already holds older tokens of the sequence keeps its scale if
+ * that is enough, else the older tokens are rounded to the larger one.  A
+ * page whose first token is new starts afresh whatever it held.  Infinities
+ * and NaN are stored as NaN and do not count towards the scale.  Finite
+ * values beyond 1.75 * 2^127 are stored as that.
+ * Sequences of one batch must not share pages that both write. */
+mlora_status mlora_kv_append(const mlora_kv_cache* cache, int32_t layer, const uint16_t* k, const uint16_t* v,
+                             int64_t row_stride, int64_t head_stride, const mlora_kv_batch* batch, void* stream);
+
+/* Reads the batch's rows back: k_out, v_out device bf16
+ * [n_rows][kv_heads][dim], row j of a sequence being token kv_len - m + j. */
+mlora_status mlora_kv_read(const mlora_kv_cache* cache, int32_t layer, const mlora_kv_batch* batch, uint16_t* k_out,
+                           uint16_t* v_out, void* stream);
+
+/* Attention of the batch's rows over their sequences:
+ *   out[r][h] = sum_t p_t v_t,  p = softmax over the visible t of scale * q[r][h] . k_t
+ * with the keys and values of head h * kv_heads / heads.  A row at position
+ * x sees tokens 0 .. x when `causal` is set (with window > 0 only the last
+ * `window` of them, x among them), every token of its sequence otherwise.
+ * What a row does not see never reaches it, not as NaN either; a row that
+ * sees nothing is zero.
+ *   q:    device bf16, strides in elements as for mlora_kv_append;
+ *   heads: query heads, a multiple of kv_heads, at most 1024 of them;
+ *   out:  device bf16 [n_rows][heads][dim], 16-byte aligned;
+ *   work: device scratch of mlora_kv_work_bytes() bytes, 256-byte aligned,
+ *         contents free (calls that share it must not overlap).
+ * Scores, softmax statistics and sums are fp32, probabilities enter the
+ * second product in bf16, as the values do.  Every result is reproducible
+ * bit for bit.  dim is 32, 64, 80, 96, 112, 128, 160, 192 or 256. */
+size_t mlora_kv_work_bytes(const mlora_kv_cache* cache, const mlora_kv_batch* batch, int32_t heads);
+mlora_status mlora_kv_attention(const mlora_kv_cache* cache, int32_t layer, const uint16_t* q, int64_t row_stride,
+                                int64_t head_stride, int32_t heads, const mlora_kv_batch* batch, int32_t causal,
+                                int32_t window, float scale, uint16_t* out, void* work, size_t work_bytes,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement helpers: a plain streaming copy (dst = src, `bytes` a multiple
  * of 16, both 16-byte aligned), used to calibrate achievable HBM bandwidth
  * and hardware byte counters against a kernel of known traffic.

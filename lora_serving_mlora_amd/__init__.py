@@ -11,6 +11,13 @@ Typical use::
     pool.load(adapter_id, rank, scale, down_bits, up_bits)   # host bf16 bits
     seg = build_segments(pool, row_adapter)                  # device int32 [n]
     Y = apply(pool, proj, X, W0, seg)                        # device bf16
+
+and, for the attention between a layer's projections::
+
+    cache = KVCache(n_layers, n_blocks, kv_heads, dim, block)          # paged 8-bit keys and values
+    batch = KVBatch(table, kv_len, row_off, n_rows, max_new=max_new)   # device int32 tensors
+    kv_append(cache, layer, k, v, batch)
+    O = kv_attention(cache, layer, q, batch)                           # device bf16
 """
 from __future__ import annotations
 
@@ -24,6 +31,7 @@ __all__ = [
     "MloraError", "lib", "Pool", "build_segments", "segments_header", "segments_status", "read_segments",
     "base_gemm", "shrink", "shrink_max_chunks", "expand", "fused", "shrink_rows", "gemm_lora", "new_work", "rows_t", "apply", "forward", "plan", "work_bytes",
     "forward_static", "STATIC_SCRATCH_BYTES", "merge", "hbm_copy", "hbm_read", "hbm_read_lds", "timing_arm", "timing_read", "VARIANTS", "ITEM_ROWS", "TILE_ROWS", "MAX_ROWS", "MAX_RANK", "SEG", "EXPORTS", "LIB_PATH",
+    "KVCache", "KVBatch", "kv_append", "kv_read", "kv_attention", "kv_work_bytes", "new_kv_work",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmlora.so")
@@ -46,6 +54,16 @@ class _PoolDesc(ctypes.Structure):
     _fields_ = [("din", _i32), ("dout", _i32), ("n_proj", _i32), ("max_adapters", _i32), ("max_rank", _i32),
                 ("reserved", _i32), ("n_down_pages", _i64), ("n_up_pages", _i64), ("down_pages", _c_void_p),
                 ("up_pages", _c_void_p), ("meta", _c_void_p)]
+
+
+class _KVCacheDesc(ctypes.Structure):
+    _fields_ = [("n_layers", _i32), ("kv_heads", _i32), ("dim", _i32), ("block", _i32), ("n_blocks", _i64),
+                ("k", _c_void_p), ("v", _c_void_p), ("k_scale", _c_void_p), ("v_scale", _c_void_p)]
+
+
+class _KVBatchDesc(ctypes.Structure):
+    _fields_ = [("table", _c_void_p), ("kv_len", _c_void_p), ("row_off", _c_void_p), ("n_seq", _i32), ("width", _i32),
+                ("table_stride", _i32), ("n_rows", _i32), ("max_new", _i32)]
 
 
 # name -> (restype, argtypes); every symbol include/mlora.h declares
@@ -83,6 +101,11 @@ EXPORTS = {
     "mlora_forward_static": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                             _i32, _i32, _c_void_p]),
     "mlora_merge": (ctypes.c_int, [_c_void_p, _i32, _i32, _c_void_p, _f32, _c_void_p]),
+    "mlora_kv_append": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
+    "mlora_kv_read": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "mlora_kv_work_bytes": (_sz, [_c_void_p, _c_void_p, _i32]),
+    "mlora_kv_attention": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _i64, _i64, _i32, _c_void_p, _i32, _i32, _f32,
+                                          _c_void_p, _c_void_p, _sz, _c_void_p]),
     "mlora_hbm_copy": (ctypes.c_int, [_c_void_p, _c_void_p, _sz, _c_void_p]),
     "mlora_hbm_read": (ctypes.c_int, [_c_void_p, _sz, _c_void_p, _c_void_p]),
     "mlora_hbm_read_lds": (ctypes.c_int, [_c_void_p, _sz, _c_void_p, _c_void_p]),
@@ -485,6 +508,126 @@ def merge(pool: Pool, adapter_id: int, proj: int, W0, sign: float = 1.0):
     _check(lib().mlora_merge(pool.handle, adapter_id, proj, _ptr(W0), ctypes.c_float(sign), _stream()),
            f"mlora_merge({adapter_id})")
     return W0
+
+
+class KVCache:
+    """Pages of an 8-bit key/value cache on the current device: e4m3 codes
+    with a power-of-two scale for each page, head and side (layouts and
+    limits: include/mlora.h).
+
+    storage: (k, v, k_scale, v_scale) of the documented shapes to use in
+    place of newly allocated, zeroed buffers."""
+
+    def __init__(self, n_layers: int, n_blocks: int, kv_heads: int, dim: int, block: int = 16, storage=None):
+        torch = _torch()
+        self.n_layers, self.n_blocks, self.kv_heads, self.dim, self.block = n_layers, n_blocks, kv_heads, dim, block
+        if min(n_layers, n_blocks, kv_heads, dim, block) < 1 or block % 16 != 0:
+            raise ValueError("KVCache sizes must be positive and block a multiple of 16")
+        shapes = ((n_layers, n_blocks, kv_heads, block, dim), (n_layers, n_blocks, kv_heads, block // 16, dim, 16),
+                  (n_layers, n_blocks, kv_heads), (n_layers, n_blocks, kv_heads))
+        dtypes = (torch.uint8, torch.uint8, torch.float32, torch.float32)
+        if storage is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+            storage = tuple(torch.zeros(s, dtype=t, device=dev) for s, t in zip(shapes, dtypes))
+        if len(storage) != 4:
+            raise ValueError("storage must be (k, v, k_scale, v_scale)")
+        for name, x, shape, dt in zip(("k", "v", "k_scale", "v_scale"), storage, shapes, dtypes):
+            if not isinstance(x, torch.Tensor) or x.dtype != dt or not x.is_cuda or not x.is_contiguous():
+                raise TypeError(f"storage: {name} must be a contiguous {dt} CUDA tensor")
+            if tuple(x.shape) != shape:
+                raise ValueError(f"storage: {name} has shape {tuple(x.shape)}, expected {shape}")
+        self.k, self.v, self.k_scale, self.v_scale = storage
+        self._d = _KVCacheDesc(n_layers, kv_heads, dim, block, n_blocks, *(x.data_ptr() for x in storage))
+        self._ref = ctypes.addressof(self._d)
+
+
+class KVBatch:
+    """Sequences of one batch and their new rows, all device int32: table
+    [n_seq][width] of page ids, kv_len [n_seq] tokens with the new ones,
+    row_off [n_seq + 1] offsets of each sequence's rows.  The tensors are kept,
+    not copied: a program that updates them in place (as a captured graph
+    does) keeps the object.  max_new bounds the rows of one sequence (n_rows
+    where it is not given)."""
+
+    def __init__(self, table, kv_len, row_off, n_rows: int, max_new: Optional[int] = None):
+        torch = _torch()
+        for name, x, nd in (("table", table, 2), ("kv_len", kv_len, 1), ("row_off", row_off, 1)):
+            if not isinstance(x, torch.Tensor) or x.dtype != torch.int32 or not x.is_cuda or x.dim() != nd:
+                raise TypeError(f"{name} must be an int32 CUDA tensor of {nd} dimension(s)")
+            if x.shape[-1] > 1 and x.stride(-1) != 1:
+                raise TypeError(f"{name} must be dense in its last dimension")
+        n_seq = kv_len.shape[0]
+        if table.shape[0] != n_seq or row_off.shape[0] != n_seq + 1:
+            raise ValueError(f"table must have {n_seq} rows and row_off {n_seq + 1} entries, as kv_len has {n_seq}")
+        self.table, self.kv_len, self.row_off, self.n_rows, self.n_seq = table, kv_len, row_off, n_rows, n_seq
+        self.max_new = n_rows if max_new is None else max_new
+        width = table.shape[1]
+        self._d = _KVBatchDesc(table.data_ptr(), kv_len.data_ptr(), row_off.data_ptr(), n_seq, width,
+                               table.stride(0) if n_seq > 1 else width, n_rows, self.max_new)
+        self._ref = ctypes.addressof(self._d)
+
+
+def _kv_rows(x, name: str, batch: KVBatch, heads: int, dim: int):
+    """Checks bf16 rows [n_rows][heads][dim]; (row, head) strides in elements."""
+    if x.dtype != _torch().bfloat16 or not x.is_cuda:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != batch.n_rows or shape[2] != dim or (heads and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{batch.n_rows}][{heads or 'heads'}][{dim}]")
+    rs, hs, cs = x.stride()
+    if cs != 1:
+        raise TypeError(f"{name} must be dense in its channels")
+    return rs, hs
+
+
+def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
+    """Quantises the batch's new rows, bf16 [n_rows][kv_heads][dim] (slices
+    of a joint projection's output serve as they are), into the cache."""
+    st = _kv_rows(k, "k", batch, cache.kv_heads, cache.dim)
+    if _kv_rows(v, "v", batch, cache.kv_heads, cache.dim) != st:
+        k, v = k.contiguous(), v.contiguous()
+        st = (cache.kv_heads * cache.dim, cache.dim)
+    _check(lib().mlora_kv_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), *st, batch._ref, _stream()),
+           "mlora_kv_append")
+
+
+def kv_read(cache: KVCache, layer: int, batch: KVBatch):
+    """The batch's rows of the cache as bf16: (k, v), [n_rows][kv_heads][dim]."""
+    torch = _torch()
+    k, v = (torch.empty((batch.n_rows, cache.kv_heads, cache.dim), dtype=torch.bfloat16, device=cache.k.device)
+            for _ in range(2))
+    _check(lib().mlora_kv_read(cache._ref, layer, batch._ref, k.data_ptr(), v.data_ptr(), _stream()), "mlora_kv_read")
+    return k, v
+
+
+def kv_work_bytes(cache: KVCache, batch: KVBatch, heads: int) -> int:
+    return int(lib().mlora_kv_work_bytes(cache._ref, batch._ref, heads))
+
+
+def new_kv_work(cache: KVCache, batch: KVBatch, heads: int):
+    """A work buffer for kv_attention with `heads` query heads; it serves
+    every layer, and every batch that needs no more bytes (kv_work_bytes)."""
+    torch = _torch()
+    return torch.empty(max(kv_work_bytes(cache, batch, heads), 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def kv_attention(cache: KVCache, layer: int, q, batch: KVBatch, causal: bool = True, window: int = 0,
+                 scale: Optional[float] = None, work=None, out=None):
+    """Attention of q, bf16 [n_rows][heads][dim], over the batch's sequences;
+    scale defaults to dim ** -0.5.  Returns bf16 [n_rows][heads][dim]."""
+    torch = _torch()
+    rs, hs = _kv_rows(q, "q", batch, 0, cache.dim)
+    heads = q.shape[1]
+    if out is None:
+        out = torch.empty((batch.n_rows, heads, cache.dim), dtype=torch.bfloat16, device=q.device)
+    elif tuple(_bf16_dev(out, "out").shape) != (batch.n_rows, heads, cache.dim):
+        raise ValueError(f"out must be [{batch.n_rows}][{heads}][{cache.dim}]")
+    if work is None:
+        work = new_kv_work(cache, batch, heads)
+    _check(lib().mlora_kv_attention(cache._ref, layer, q.data_ptr(), rs, hs, heads, batch._ref, causal, window,
+                                    cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), work.data_ptr(),
+                                    work.numel() * work.element_size(), _stream()), "mlora_kv_attention")
+    return out
 
 
 def hbm_copy(dst, src, nbytes: Optional[int] = None):

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "kv.h"
 
 using mlora::PoolView;
 
@@ -1157,6 +1158,111 @@ mlora_status mlora_hbm_read_lds(const void* src, size_t bytes, uint32_t* out, vo
                 "LDS-DMA read needs a non-NULL 16-byte aligned source, a multiple of 1024 bytes below 2 GiB and an "
                 "output word");
   return hip_check(mlora::launch_hbm_read_lds(src, bytes, out, as_stream(stream)), "LDS-DMA read launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------
+// paged 8-bit key/value cache
+// ----------------------------------------------------------------------------
+
+namespace {
+// Checks everything the host can see of a cache and a batch; `v` is the view
+// of `layer`.
+mlora_status kv_view(const mlora_kv_cache* c, const mlora_kv_batch* b, int32_t layer, mlora::KvView* v) {
+  if (!c || !b) return fail(MLORA_EINVAL, "cache and batch must not be NULL");
+  if (c->n_layers < 1 || c->kv_heads < 1 || c->kv_heads > 1024)
+    return fail(MLORA_EINVAL, "cache: %d layers, %d key/value heads (1 .. 1024)", c->n_layers, c->kv_heads);
+  if (c->dim < 16 || c->dim > 256 || c->dim % 16 != 0)
+    return fail(MLORA_EINVAL, "cache: dim %d is not a multiple of 16 up to 256", c->dim);
+  int lb = 4;
+  while (lb < 8 && (1 << lb) != c->block) ++lb;
+  if ((1 << lb) != c->block) return fail(MLORA_EINVAL, "cache: block %d is not 16, 32, 64, 128 or 256", c->block);
+  if (c->n_blocks < 1 || c->n_blocks > INT32_MAX)
+    return fail(MLORA_EINVAL, "cache: %lld pages", (long long)c->n_blocks);
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(MLORA_EINVAL, "cache: a buffer is NULL");
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(MLORA_EINVAL, "cache: k and v must be 16-byte aligned");
+  if (layer < 0 || layer >= c->n_layers) return fail(MLORA_EINVAL, "layer %d outside [0, %d)", layer, c->n_layers);
+  if (b->n_seq < 0 || b->n_seq > (1 << 20) || b->n_rows < 0 || b->n_rows > (1 << 24))
+    return fail(MLORA_EINVAL, "batch: %d sequences (at most 2^20), %d rows (at most 2^24)", b->n_seq, b->n_rows);
+  if (b->width < 1 || b->table_stride < b->width || (int64_t)b->width << lb > (1 << 30))
+    return fail(MLORA_EINVAL, "batch: table width %d, stride %d", b->width, b->table_stride);
+  if (b->n_rows > 0) {
+    if (b->n_seq == 0) return fail(MLORA_EINVAL, "batch: %d rows without a sequence", b->n_rows);
+    if (b->max_new < 1 || b->max_new > b->n_rows || (int64_t)b->max_new * b->n_seq < b->n_rows)
+      return fail(MLORA_EINVAL, "batch: max_new %d cannot bound %d rows of %d sequences", b->max_new, b->n_rows,
+                  b->n_seq);
+    if (!b->table || !b->kv_len || !b->row_off) return fail(MLORA_EINVAL, "batch: a buffer is NULL");
+  }
+  const size_t tok = (size_t)c->n_blocks * c->kv_heads * c->block * c->dim, sc = (size_t)c->n_blocks * c->kv_heads;
+  *v = {static_cast<uint8_t*>(c->k) + layer * tok, static_cast<uint8_t*>(c->v) + layer * tok,
+        c->k_scale + layer * sc, c->v_scale + layer * sc, b->table, b->kv_len, b->row_off, b->n_seq, b->width,
+        b->table_stride, b->n_rows, b->max_new, c->kv_heads, c->dim, lb, (int32_t)c->n_blocks};
+  return MLORA_OK;
+}
+
+mlora_status kv_strides(int64_t rs, int64_t hs) {
+  if (rs < 0 || hs < 0 || rs > INT32_MAX || hs > INT32_MAX)
+    return fail(MLORA_EINVAL, "strides %lld, %lld outside [0, 2^31)", (long long)rs, (long long)hs);
+  return MLORA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+mlora_status mlora_kv_append(const mlora_kv_cache* c, int32_t layer, const uint16_t* k, const uint16_t* v, int64_t rs,
+                             int64_t hs, const mlora_kv_batch* b, void* stream) {
+  g_err.clear();
+  mlora::KvView view;
+  mlora_status st = kv_view(c, b, layer, &view);
+  if (st == MLORA_OK) st = kv_strides(rs, hs);
+  if (st != MLORA_OK) return st;
+  if (b->n_rows == 0) return MLORA_OK;
+  if (!k || !v) return fail(MLORA_EINVAL, "k and v must not be NULL");
+  return hip_check(mlora::launch_kv_append(view, k, v, rs, hs, as_stream(stream)), "cache append launch");
+}
+
+mlora_status mlora_kv_read(const mlora_kv_cache* c, int32_t layer, const mlora_kv_batch* b, uint16_t* k, uint16_t* v,
+                           void* stream) {
+  g_err.clear();
+  mlora::KvView view;
+  mlora_status st = kv_view(c, b, layer, &view);
+  if (st != MLORA_OK) return st;
+  if (b->n_rows == 0) return MLORA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v))
+    return fail(MLORA_EINVAL, "k and v must not be NULL and be 16-byte aligned");
+  return hip_check(mlora::launch_kv_read(view, k, v, as_stream(stream)), "cache read launch");
+}
+
+size_t mlora_kv_work_bytes(const mlora_kv_cache* c, const mlora_kv_batch* b, int32_t heads) {
+  mlora::KvView view;
+  if (kv_view(c, b, 0, &view) != MLORA_OK || heads < c->kv_heads || heads > 1024 || heads % c->kv_heads != 0) return 0;
+  return mlora::kv_work_bytes(view, heads);
+}
+
+mlora_status mlora_kv_attention(const mlora_kv_cache* c, int32_t layer, const uint16_t* q, int64_t rs, int64_t hs,
+                                int32_t heads, const mlora_kv_batch* b, int32_t causal, int32_t window, float scale,
+                                uint16_t* out, void* work, size_t work_bytes, void* stream) {
+  g_err.clear();
+  mlora::KvView view;
+  mlora_status st = kv_view(c, b, layer, &view);
+  if (st == MLORA_OK) st = kv_strides(rs, hs);
+  if (st != MLORA_OK) return st;
+  if (!mlora::kv_attention_dim(c->dim))
+    return fail(MLORA_EINVAL, "attention: dim %d is not 32, 64, 80, 96, 112, 128, 160, 192 or 256", c->dim);
+  if (heads < c->kv_heads || heads > 1024 || heads % c->kv_heads != 0)
+    return fail(MLORA_EINVAL, "attention: %d query heads are not a multiple of %d up to 1024", heads, c->kv_heads);
+  if (window < 0 || (window > 0 && !causal))
+    return fail(MLORA_EINVAL, "attention: window %d%s", window, window > 0 ? " without causal" : "");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MLORA_EINVAL, "attention: scale must be finite and above 0");
+  if (b->n_rows == 0) return MLORA_OK;
+  if (!q || !out || !aligned16(out)) return fail(MLORA_EINVAL, "q and out must not be NULL, out 16-byte aligned");
+  const size_t need = mlora::kv_work_bytes(view, heads);
+  if (need > 0 && (!work || work_bytes < need))
+    return fail(MLORA_EINVAL, "work: %zu bytes given, %zu needed", work_bytes, need);
+  if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0) return fail(MLORA_EINVAL, "work must be 256-byte aligned");
+  const mlora::KvAttn a{q, rs, hs, out, scale, heads / c->kv_heads, causal != 0, window, work};
+  return hip_check(mlora::launch_kv_attention(view, a, as_stream(stream)), "attention launch");
 }
 
 }  // extern "C"

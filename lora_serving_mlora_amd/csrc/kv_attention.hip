@@ -1,0 +1,321 @@
+// Attention over the paged 8-bit key/value cache.
+//
+// For a row with query q at position x, over the tokens t that it sees:
+//   s_t = q . k_t,  p_t = 2^(s_t c - M),  o = sum_t p_t v_t / sum_t p_t,
+// c = scale * log2(e), in one pass: M is a running reference for the largest
+// s_t c, and what was summed under an older one is multiplied by the quotient.
+// The codes become bf16 in registers, times their page's scale: exact, so the
+// products lose nothing against an unquantised bf16 cache.  (The 8-bit matrix
+// instruction would take the codes as they are and run at twice the rate, but
+// it drops what lies 2^-13 below the magnitudes it sums, and the queries
+// would need two codes each.)
+#include "kv.h"
+
+namespace mlora {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr int kStep = 64;      // tokens of one step of a wave
+constexpr int kWaves = 4;
+constexpr float kSlack = 8.f;  // log2 by which a score may pass M before the sums are rescaled
+
+__device__ __forceinline__ bf16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8, uint4{a, b, c, d});
+}
+__device__ __forceinline__ bf16x8 frag_fp8(uint32_t lo, uint32_t hi, float s) {
+  return frag(kv_bf2<false>(lo, s), kv_bf2<true>(lo, s), kv_bf2<false>(hi, s), kv_bf2<true>(hi, s));
+}
+
+// over the lanes with the same l % 16
+__device__ __forceinline__ float max_rows(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_rows(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// bytes of w that are NaN codes, as 0x80 in each
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// 0x80 marks -> ones for each marked byte of the low or high pair, as packed bf16
+template <bool HI>
+__device__ __forceinline__ uint32_t ones2(uint32_t m) {
+  const uint32_t a = HI ? m >> 16 : m;
+  return (a & 0x80u ? 0x3f80u : 0u) | (a & 0x8000u ? 0x3f800000u : 0u);
+}
+
+// Rows: a (sequence, key/value head) has m * G query rows, row r being new
+// token r / G and query head h * G + r % G.
+struct Span {
+  int lo, hi;  // tokens lo <= t < hi
+};
+// What lies past the table is represented by its first token there, which has
+// no page, so that a wrong kv_len costs no more than a full table.
+__device__ __forceinline__ Span row_span(const KvView& c, const KvAttn& a, const KvSeq& s, int j) {
+  Span v{0, max(s.n, 0)};
+  if (a.causal) {
+    v.hi = max(0, s.n - s.m + j + 1);
+    if (a.window > 0) v.lo = max(0, v.hi - a.window);
+  }
+  const int end = c.width << c.lb;
+  if (v.hi > end) v = {min(v.lo, end), end + 1};
+  return v;
+}
+
+// ----------------------------------------------------------------------------
+// Few rows: 16 rows of one (sequence, key/value head), four waves that take
+// every fourth step of 64 tokens, straight from memory into registers.
+//
+// One wave's step, S^T = K Q^T and O^T = V^T P^T with 16x16x32 products: lane
+// l = 16 g + q holds in S^T's tile t, element e, the score of row q and token
+// 16 g + 4 t + e (the keys' rows are dealt to the matrix rows that way), so
+// its 16 scores are those of the 16-token block g: exactly the probabilities
+// that it has to supply to the second product, whose other operand is the
+// block's 16 bytes of a channel, one load.  Nothing passes through LDS.
+// ----------------------------------------------------------------------------
+template <int D>
+struct RowsTile {
+  static constexpr int R = (D + 63) / 64;  // 16-byte loads of a lane for a token's keys
+  static constexpr int T = D / 16;         // channel tiles of the output
+};
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, int qtiles) {
+  constexpr int R = RowsTile<D>::R, T = RowsTile<D>::T, LD = D + 4;
+  __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
+  __shared__ float sh_o[kWaves][16][LD];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int q = lane & 15, g = lane >> 4;
+  int item = blockIdx.x;
+  const int h = item % c.H;
+  item /= c.H;
+  const int qt = item % qtiles, seq = item / qtiles;
+  const KvSeq s = kv_seq(c, seq);
+  const int rows = s.m * a.G, r0 = qt * 16;
+  if (r0 >= rows) return;
+  const int r1 = min(r0 + 16, rows) - 1;
+  const int j0 = r0 / a.G, j1 = r1 / a.G;
+  const Span first = row_span(c, a, s, j0), last = row_span(c, a, s, j1);
+  const int all_lo = first.lo, all_hi = last.hi;    // seen by some row
+  const int every_lo = last.lo, every_hi = first.hi;  // seen by every row
+
+  const int r = min(r0 + q, r1), j = r / a.G;
+  const Span mine = row_span(c, a, s, j);
+  bf16x8 qf[R][2];
+  {
+    const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int u = 4 * i + g;
+      uint4 x{}, y{};
+      if (16 * u < D) {
+        if (vec) {
+          x = *reinterpret_cast<const uint4*>(p + 16 * u);
+          y = *reinterpret_cast<const uint4*>(p + 16 * u + 8);
+        } else {
+          const uint16_t* e = p + 16 * u;
+          x = uint4{e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                    e[6] | (uint32_t)e[7] << 16};
+          y = uint4{e[8] | (uint32_t)e[9] << 16, e[10] | (uint32_t)e[11] << 16, e[12] | (uint32_t)e[13] << 16,
+                    e[14] | (uint32_t)e[15] << 16};
+        }
+      }
+      qf[i][0] = __builtin_bit_cast(bf16x8, x);
+      qf[i][1] = __builtin_bit_cast(bf16x8, y);
+    }
+  }
+
+  const float cs = a.scale * 1.4426950408889634f;
+  f32x4 o[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i) o[i] = f32x4{0, 0, 0, 0};
+  float M = -kInf, L = 0.f;
+
+  const int kblk = q >> 2, B = 1 << c.lb;
+  for (int c0 = all_lo / kStep + wave; c0 * kStep < all_hi; c0 += kWaves) {
+    const int base = c0 * kStep;
+    // the pages of this lane's keys (16-token block q / 4) and values (block g)
+    const int kt = base + 16 * kblk, vt = base + 16 * g;
+    const int kid = kt < all_hi ? kv_page(c, seq, kt >> c.lb) : 0;
+    const int vid = vt < all_hi ? kv_page(c, seq, vt >> c.lb) : 0;
+    const bool bad = vid < 0;
+    const size_t kp = (size_t)max(kid, 0) * c.H + h, vp = (size_t)max(vid, 0) * c.H + h;
+    const float ks = c.k_scale[kp], vs = !bad && vt < all_hi && vt + 16 > all_lo ? c.v_scale[vp] : 1.f;
+    const uint8_t* kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
+    const uint8_t* vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
+    uint4 kw[4][R], vw[T];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        kw[t][i] = uint4{0, 0, 0, 0};
+        if (16 * (4 * i + 3) < D || 16 * (4 * i + g) < D)
+          kw[t][i] = *reinterpret_cast<const uint4*>(kptr + 4 * t * D + 16 * (4 * i + g));
+      }
+#pragma unroll
+    for (int i = 0; i < T; ++i) vw[i] = *reinterpret_cast<const uint4*>(vptr + 256 * i);
+
+    f32x4 st[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      st[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[t][i].x, kw[t][i].y, ks), qf[i][0], st[t], 0, 0, 0);
+        st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[t][i].z, kw[t][i].w, ks), qf[i][1], st[t], 0, 0, 0);
+      }
+    }
+    const int mt = base + 16 * g;  // first of this lane's 16 tokens
+    if (__ballot(bad)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (bad) st[t][e] = __builtin_nanf("");
+    }
+    const bool edge = base < every_lo || base + kStep > every_hi;
+    if (edge) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = mt + 4 * t + e;
+          if (tok < mine.lo || tok >= mine.hi) st[t][e] = -kInf;
+        }
+      // a NaN among the values must reach the rows that see it, and no other:
+      // it is taken out of the product, and the rows are found by a product of
+      // their view (ones) with the NaNs' places (ones)
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < T; ++i) any |= nan_codes(vw[i].x) | nan_codes(vw[i].y) | nan_codes(vw[i].z) | nan_codes(vw[i].w);
+      if (__ballot(any != 0)) {
+        uint32_t see[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int tok = mt + 2 * k;
+          see[k] = (tok >= mine.lo && tok < mine.hi ? 0x3f80u : 0u) |
+                   (tok + 1 >= mine.lo && tok + 1 < mine.hi ? 0x3f800000u : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&vw[i]);
+          f32x4 hit{0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t n0 = nan_codes(w[2 * u]), n1 = nan_codes(w[2 * u + 1]);
+            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                frag(ones2<false>(n0), ones2<true>(n0), ones2<false>(n1), ones2<true>(n1)),
+                frag(see[4 * u], see[4 * u + 1], see[4 * u + 2], see[4 * u + 3]), hit, 0, 0, 0);
+            w[2 * u] &= ~(n0 | (n0 - (n0 >> 7)));
+            w[2 * u + 1] &= ~(n1 | (n1 - (n1 >> 7)));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (hit[e] > 0.f) o[i][e] = __builtin_nanf("");
+        }
+      }
+    }
+    float mx = -kInf;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) mx = fmaxf(fmaxf(fmaxf(mx, st[t][0]), fmaxf(st[t][1], st[t][2])), st[t][3]);
+    mx = max_rows(mx) * cs;
+    if (__ballot(mx > M + kSlack)) {
+      const float Mn = fmaxf(M, mx), f = Mn == M ? 1.f : __builtin_amdgcn_exp2f(M - Mn);
+      M = Mn;
+      L *= f;
+#pragma unroll
+      for (int i = 0; i < T; ++i) o[i] *= f;
+    }
+    const float ref = M == -kInf ? 0.f : M;
+    uint32_t pw[8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][e], cs, -ref));
+      L += (p[0] + p[1]) + (p[2] + p[3]);
+      pw[2 * t] = pack_bf2_hw(p[0], p[1]);
+      pw[2 * t + 1] = pack_bf2_hw(p[2], p[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].x, vw[i].y, vs), frag(pw[0], pw[1], pw[2], pw[3]),
+                                                     o[i], 0, 0, 0);
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].z, vw[i].w, vs), frag(pw[4], pw[5], pw[6], pw[7]),
+                                                     o[i], 0, 0, 0);
+    }
+  }
+  L = sum_rows(L);
+
+  // join the waves
+  if (g == 0) {
+    sh_m[wave][q] = M;
+    sh_l[wave][q] = L;
+  }
+#pragma unroll
+  for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&sh_o[wave][q][16 * i + 4 * g]) = o[i];
+  __syncthreads();
+  const int Hq = c.H * a.G;
+  for (int i = tid; i < (r1 - r0 + 1) * (D / 4); i += 64 * kWaves) {
+    const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+    float top = sh_m[0][row];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][row]);
+    const float ref = top == -kInf ? 0.f : top;
+    float l = 0.f;
+    f32x4 v{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sh_m[w][row] - ref);
+      l += sh_l[w][row] * f;
+      v += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]) * f;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int rr = r0 + row;
+    uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + d;
+    *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
+  }
+}
+
+template <int D>
+hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
+  const int qtiles = ((int64_t)c.max_new * a.G + 15) / 16;
+  MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3((unsigned)(c.n_seq * qtiles * c.H)), dim3(64 * kWaves), 0, stream, c,
+               a, qtiles);
+  return launched();
+}
+
+}  // namespace
+
+bool kv_attention_dim(int dim) {
+  return dim == 32 || dim == 64 || dim == 80 || dim == 96 || dim == 112 || dim == 128 || dim == 160 || dim == 192 ||
+         dim == 256;
+}
+
+size_t kv_work_bytes(const KvView&, int) { return 0; }
+
+hipError_t launch_kv_attention(const KvView& c, const KvAttn& a, hipStream_t stream) {
+  switch (c.D) {
+    case 32: return launch_dim<32>(c, a, stream);
+    case 64: return launch_dim<64>(c, a, stream);
+    case 80: return launch_dim<80>(c, a, stream);
+    case 96: return launch_dim<96>(c, a, stream);
+    case 112: return launch_dim<112>(c, a, stream);
+    case 128: return launch_dim<128>(c, a, stream);
+    case 160: return launch_dim<160>(c, a, stream);
+    case 192: return launch_dim<192>(c, a, stream);
+    case 256: return launch_dim<256>(c, a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace mlora
