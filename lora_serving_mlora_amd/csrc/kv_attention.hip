@@ -9,7 +9,9 @@
 // instruction would take the codes as they are and run at twice the rate, but
 // it drops what lies 2^-13 below the magnitudes it sums, and the queries
 // would need two codes each.)
-#include "kv.h"
+#include <algorithm>
+
+#include "kv_sched.h"
 
 namespace mlora {
 namespace {
@@ -18,7 +20,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kInf = __builtin_huge_valf();
-constexpr int kStep = 64;      // tokens of one step of a wave
 constexpr int kWaves = 4;
 constexpr float kSlack = 8.f;  // log2 by which a score may pass M before the sums are rescaled
 
@@ -27,6 +28,18 @@ __device__ __forceinline__ bf16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint3
 }
 __device__ __forceinline__ bf16x8 frag_fp8(uint32_t lo, uint32_t hi, float s) {
   return frag(kv_bf2<false>(lo, s), kv_bf2<true>(lo, s), kv_bf2<false>(hi, s), kv_bf2<true>(hi, s));
+}
+
+// 16 bf16 at p, 16-byte aligned or not
+__device__ __forceinline__ void load16(const uint16_t* p, bool vec, uint4& x, uint4& y) {
+  if (vec) {
+    x = *reinterpret_cast<const uint4*>(p);
+    y = *reinterpret_cast<const uint4*>(p + 8);
+  } else {
+    auto two = [&](int i) { return p[i] | (uint32_t)p[i + 1] << 16; };
+    x = uint4{two(0), two(2), two(4), two(6)};
+    y = uint4{two(8), two(10), two(12), two(14)};
+  }
 }
 
 // over the lanes with the same l % 16
@@ -52,24 +65,6 @@ __device__ __forceinline__ uint32_t ones2(uint32_t m) {
   return (a & 0x80u ? 0x3f80u : 0u) | (a & 0x8000u ? 0x3f800000u : 0u);
 }
 
-// Rows: a (sequence, key/value head) has m * G query rows, row r being new
-// token r / G and query head h * G + r % G.
-struct Span {
-  int lo, hi;  // tokens lo <= t < hi
-};
-// What lies past the table is represented by its first token there, which has
-// no page, so that a wrong kv_len costs no more than a full table.
-__device__ __forceinline__ Span row_span(const KvView& c, const KvAttn& a, const KvSeq& s, int j) {
-  Span v{0, max(s.n, 0)};
-  if (a.causal) {
-    v.hi = max(0, s.n - s.m + j + 1);
-    if (a.window > 0) v.lo = max(0, v.hi - a.window);
-  }
-  const int end = c.width << c.lb;
-  if (v.hi > end) v = {min(v.lo, end), end + 1};
-  return v;
-}
-
 // ----------------------------------------------------------------------------
 // Few rows: 16 rows of one (sequence, key/value head), four waves that take
 // every fourth step of 64 tokens, straight from memory into registers.
@@ -87,210 +82,249 @@ struct RowsTile {
   static constexpr int T = D / 16;         // channel tiles of the output
 };
 
+// Loads of the next step are issued as soon as the registers they go to have
+// been read (the keys' after the first product, the values' after the second),
+// and its page ids a step before that.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, int qtiles) {
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
   constexpr int R = RowsTile<D>::R, T = RowsTile<D>::T, LD = D + 4;
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
   __shared__ float sh_o[kWaves][16][LD];
+  __shared__ SchedLds sh_sched;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int q = lane & 15, g = lane >> 4;
-  int item = blockIdx.x;
-  const int h = item % c.H;
-  item /= c.H;
-  const int qt = item % qtiles, seq = item / qtiles;
-  const KvSeq s = kv_seq(c, seq);
-  const int rows = s.m * a.G, r0 = qt * 16;
-  if (r0 >= rows) return;
-  const int r1 = min(r0 + 16, rows) - 1;
-  const int j0 = r0 / a.G, j1 = r1 / a.G;
-  const Span first = row_span(c, a, s, j0), last = row_span(c, a, s, j1);
-  const int all_lo = first.lo, all_hi = last.hi;    // seen by some row
-  const int every_lo = last.lo, every_hi = first.hi;  // seen by every row
-
-  const int r = min(r0 + q, r1), j = r / a.G;
-  const Span mine = row_span(c, a, s, j);
-  bf16x8 qf[R][2];
-  {
-    const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs;
-    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int u = 4 * i + g;
-      uint4 x{}, y{};
-      if (16 * u < D) {
-        if (vec) {
-          x = *reinterpret_cast<const uint4*>(p + 16 * u);
-          y = *reinterpret_cast<const uint4*>(p + 16 * u + 8);
-        } else {
-          const uint16_t* e = p + 16 * u;
-          x = uint4{e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
-                    e[6] | (uint32_t)e[7] << 16};
-          y = uint4{e[8] | (uint32_t)e[9] << 16, e[10] | (uint32_t)e[11] << 16, e[12] | (uint32_t)e[13] << 16,
-                    e[14] | (uint32_t)e[15] << 16};
-        }
-      }
-      qf[i][0] = __builtin_bit_cast(bf16x8, x);
-      qf[i][1] = __builtin_bit_cast(bf16x8, y);
-    }
-  }
-
+  const int q = lane & 15, g = lane >> 4, kblk = q >> 2, B = 1 << c.lb;
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
-  f32x4 o[T];
-#pragma unroll
-  for (int i = 0; i < T; ++i) o[i] = f32x4{0, 0, 0, 0};
-  float M = -kInf, L = 0.f;
 
-  const int kblk = q >> 2, B = 1 << c.lb;
-  for (int c0 = all_lo / kStep + wave; c0 * kStep < all_hi; c0 += kWaves) {
-    const int base = c0 * kStep;
-    // the pages of this lane's keys (16-token block q / 4) and values (block g)
-    const int kt = base + 16 * kblk, vt = base + 16 * g;
-    const int kid = kt < all_hi ? kv_page(c, seq, kt >> c.lb) : 0;
-    const int vid = vt < all_hi ? kv_page(c, seq, vt >> c.lb) : 0;
-    const bool bad = vid < 0;
-    const size_t kp = (size_t)max(kid, 0) * c.H + h, vp = (size_t)max(vid, 0) * c.H + h;
-    const float ks = c.k_scale[kp], vs = !bad && vt < all_hi && vt + 16 > all_lo ? c.v_scale[vp] : 1.f;
-    const uint8_t* kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
-    const uint8_t* vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
+  sched_run<16>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0, int s1,
+                                       int slot) __attribute__((always_inline)) {
+    const int r = min(t.r0 + q, t.r1), j = r / a.G;
+    const Span mine = row_span(c, a, s, j);
+    bf16x8 qf[R][2];
+    {
+      const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int u = 4 * i + g;
+        uint4 x{}, y{};
+        if (16 * u < D) load16(p + 16 * u, vec, x, y);
+        qf[i][0] = __builtin_bit_cast(bf16x8, x);
+        qf[i][1] = __builtin_bit_cast(bf16x8, y);
+      }
+    }
+    f32x4 o[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) o[i] = f32x4{0, 0, 0, 0};
+    float M = -kInf, L = 0.f;
+
+    // page ids of this lane's keys (16-token block q / 4 of a step) and values (block g)
+    int kid, vid;
+    auto ids = [&](int step) {
+      const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
+      kid = kt < t.hi ? kv_page(c, seq, kt >> c.lb) : 0;
+      vid = vt < t.hi ? kv_page(c, seq, vt >> c.lb) : 0;
+    };
+    const uint8_t *kptr, *vptr;
+    float ks, vs;
     uint4 kw[4][R], vw[T];
+    bool bad;
+    const float *ksp, *vsp;
+    bool vin;
+    auto place = [&](int step) {
+      const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
+      const size_t kp = (size_t)max(kid, 0) * c.H + h, vp = (size_t)max(vid, 0) * c.H + h;
+      kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
+      vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
+      ksp = c.k_scale + kp;
+      vsp = c.v_scale + vp;
+      bad = vid < 0;
+      vin = !bad && vt < t.hi && vt + 16 > t.lo;
+    };
+    auto load_k = [&]() {
+      ks = *ksp;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        kw[t][i] = uint4{0, 0, 0, 0};
-        if (16 * (4 * i + 3) < D || 16 * (4 * i + g) < D)
-          kw[t][i] = *reinterpret_cast<const uint4*>(kptr + 4 * t * D + 16 * (4 * i + g));
-      }
+        for (int i = 0; i < R; ++i) {
+          kw[x][i] = uint4{0, 0, 0, 0};
+          if (16 * (4 * i + 3) < D || 16 * (4 * i + g) < D)
+            kw[x][i] = *reinterpret_cast<const uint4*>(kptr + 4 * x * D + 16 * (4 * i + g));
+        }
+    };
+    auto load_v = [&]() {
+      vs = *vsp;
 #pragma unroll
-    for (int i = 0; i < T; ++i) vw[i] = *reinterpret_cast<const uint4*>(vptr + 256 * i);
+      for (int i = 0; i < T; ++i) vw[i] = *reinterpret_cast<const uint4*>(vptr + 256 * i);
+    };
 
-    f32x4 st[4];
+    int step = t.step0 + s0 + wave;
+    const int end = t.step0 + s1;
+    if (step < end) {
+      ids(step);
+      place(step);
+      load_k();
+      load_v();
+      if (step + kWaves < end) ids(step + kWaves);
+    }
+    for (; step < end; step += kWaves) {
+      const bool more = step + kWaves < end;
+      const int base = step * kKvStep;
+      const bool bad_now = bad, vin_now = vin;
+      f32x4 st[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      st[t] = f32x4{0, 0, 0, 0};
+      for (int x = 0; x < 4; ++x) {
+        st[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[t][i].x, kw[t][i].y, ks), qf[i][0], st[t], 0, 0, 0);
-        st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[t][i].z, kw[t][i].w, ks), qf[i][1], st[t], 0, 0, 0);
+        for (int i = 0; i < R; ++i) {
+          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[x][i].x, kw[x][i].y, ks), qf[i][0], st[x], 0, 0, 0);
+          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[x][i].z, kw[x][i].w, ks), qf[i][1], st[x], 0, 0, 0);
+        }
       }
-    }
-    const int mt = base + 16 * g;  // first of this lane's 16 tokens
-    if (__ballot(bad)) {
+      if (more) {
+        place(step + kWaves);
+        load_k();
+        if (step + 2 * kWaves < end) ids(step + 2 * kWaves);
+      }
+      const int mt = base + 16 * g;  // first of this lane's 16 tokens
+      if (__ballot(bad_now)) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (bad) st[t][e] = __builtin_nanf("");
-    }
-    const bool edge = base < every_lo || base + kStep > every_hi;
-    if (edge) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = mt + 4 * t + e;
-          if (tok < mine.lo || tok >= mine.hi) st[t][e] = -kInf;
-        }
-      // a NaN among the values must reach the rows that see it, and no other:
-      // it is taken out of the product, and the rows are found by a product of
-      // their view (ones) with the NaNs' places (ones)
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < T; ++i) any |= nan_codes(vw[i].x) | nan_codes(vw[i].y) | nan_codes(vw[i].z) | nan_codes(vw[i].w);
-      if (__ballot(any != 0)) {
-        uint32_t see[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int tok = mt + 2 * k;
-          see[k] = (tok >= mine.lo && tok < mine.hi ? 0x3f80u : 0u) |
-                   (tok + 1 >= mine.lo && tok + 1 < mine.hi ? 0x3f800000u : 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&vw[i]);
-          f32x4 hit{0, 0, 0, 0};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t n0 = nan_codes(w[2 * u]), n1 = nan_codes(w[2 * u + 1]);
-            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                frag(ones2<false>(n0), ones2<true>(n0), ones2<false>(n1), ones2<true>(n1)),
-                frag(see[4 * u], see[4 * u + 1], see[4 * u + 2], see[4 * u + 3]), hit, 0, 0, 0);
-            w[2 * u] &= ~(n0 | (n0 - (n0 >> 7)));
-            w[2 * u + 1] &= ~(n1 | (n1 - (n1 >> 7)));
-          }
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (hit[e] > 0.f) o[i][e] = __builtin_nanf("");
+            if (bad_now) st[x][e] = __builtin_nanf("");
+      }
+      const float vsc = vin_now ? vs : 1.f;
+      if (base < t.every_lo || base + kKvStep > t.every_hi) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = mt + 4 * x + e;
+            if (tok < mine.lo || tok >= mine.hi) st[x][e] = -kInf;
+          }
+        // a NaN among the values must reach the rows that see it, and no other:
+        // it is taken out of the product, and the rows are found by a product
+        // of their view (ones) with the NaNs' places (ones)
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+          any |= nan_codes(vw[i].x) | nan_codes(vw[i].y) | nan_codes(vw[i].z) | nan_codes(vw[i].w);
+        if (__ballot(any != 0)) {
+          uint32_t see[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int tok = mt + 2 * k;
+            see[k] = (tok >= mine.lo && tok < mine.hi ? 0x3f80u : 0u) |
+                     (tok + 1 >= mine.lo && tok + 1 < mine.hi ? 0x3f800000u : 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < T; ++i) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&vw[i]);
+            f32x4 hit{0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t n0 = nan_codes(w[2 * u]), n1 = nan_codes(w[2 * u + 1]);
+              hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  frag(ones2<false>(n0), ones2<true>(n0), ones2<false>(n1), ones2<true>(n1)),
+                  frag(see[4 * u], see[4 * u + 1], see[4 * u + 2], see[4 * u + 3]), hit, 0, 0, 0);
+              w[2 * u] &= ~(n0 | (n0 - (n0 >> 7)));
+              w[2 * u + 1] &= ~(n1 | (n1 - (n1 >> 7)));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (hit[e] > 0.f) o[i][e] = __builtin_nanf("");
+          }
         }
       }
+      float mx = -kInf;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mx = fmaxf(fmaxf(fmaxf(mx, st[x][0]), fmaxf(st[x][1], st[x][2])), st[x][3]);
+      mx = max_rows(mx) * cs;
+      if (__ballot(mx > M + kSlack)) {
+        const float Mn = fmaxf(M, mx), f = Mn == M ? 1.f : __builtin_amdgcn_exp2f(M - Mn);
+        M = Mn;
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < T; ++i) o[i] *= f;
+      }
+      const float ref = M == -kInf ? 0.f : M;
+      uint32_t pw[8];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][e], cs, -ref));
+        L += (p[0] + p[1]) + (p[2] + p[3]);
+        pw[2 * x] = pack_bf2_hw(p[0], p[1]);
+        pw[2 * x + 1] = pack_bf2_hw(p[2], p[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].x, vw[i].y, vsc), frag(pw[0], pw[1], pw[2], pw[3]),
+                                                       o[i], 0, 0, 0);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].z, vw[i].w, vsc), frag(pw[4], pw[5], pw[6], pw[7]),
+                                                       o[i], 0, 0, 0);
+      }
+      if (more) load_v();
     }
-    float mx = -kInf;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) mx = fmaxf(fmaxf(fmaxf(mx, st[t][0]), fmaxf(st[t][1], st[t][2])), st[t][3]);
-    mx = max_rows(mx) * cs;
-    if (__ballot(mx > M + kSlack)) {
-      const float Mn = fmaxf(M, mx), f = Mn == M ? 1.f : __builtin_amdgcn_exp2f(M - Mn);
-      M = Mn;
-      L *= f;
-#pragma unroll
-      for (int i = 0; i < T; ++i) o[i] *= f;
-    }
-    const float ref = M == -kInf ? 0.f : M;
-    uint32_t pw[8];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][e], cs, -ref));
-      L += (p[0] + p[1]) + (p[2] + p[3]);
-      pw[2 * t] = pack_bf2_hw(p[0], p[1]);
-      pw[2 * t + 1] = pack_bf2_hw(p[2], p[3]);
-    }
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].x, vw[i].y, vs), frag(pw[0], pw[1], pw[2], pw[3]),
-                                                     o[i], 0, 0, 0);
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].z, vw[i].w, vs), frag(pw[4], pw[5], pw[6], pw[7]),
-                                                     o[i], 0, 0, 0);
-    }
-  }
-  L = sum_rows(L);
+    L = sum_rows(L);
 
-  // join the waves
-  if (g == 0) {
-    sh_m[wave][q] = M;
-    sh_l[wave][q] = L;
-  }
-#pragma unroll
-  for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&sh_o[wave][q][16 * i + 4 * g]) = o[i];
-  __syncthreads();
-  const int Hq = c.H * a.G;
-  for (int i = tid; i < (r1 - r0 + 1) * (D / 4); i += 64 * kWaves) {
-    const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
-    float top = sh_m[0][row];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][row]);
-    const float ref = top == -kInf ? 0.f : top;
-    float l = 0.f;
-    f32x4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(sh_m[w][row] - ref);
-      l += sh_l[w][row] * f;
-      v += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]) * f;
+    // join the waves
+    if (g == 0) {
+      sh_m[wave][q] = M;
+      sh_l[wave][q] = L;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int rr = r0 + row;
-    uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + d;
-    *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
-  }
+#pragma unroll
+    for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&sh_o[wave][q][16 * i + 4 * g]) = o[i];
+    __syncthreads();
+    const int Hq = c.H * a.G;
+    for (int i = tid; i < (t.r1 - t.r0 + 1) * (D / 4); i += 64 * kWaves) {
+      const int row = i / (D / 4), ch = (i - row * (D / 4)) * 4;
+      float top = sh_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][row]);
+      const float ref = top == -kInf ? 0.f : top;
+      float l = 0.f;
+      f32x4 v{0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sh_m[w][row] - ref);
+        l += sh_l[w][row] * f;
+        v += *reinterpret_cast<const f32x4*>(&sh_o[w][row][ch]) * f;
+      }
+      if (slot >= 0) {
+        float* dst = sched_slot(a.work, slot, 16, D);
+        *reinterpret_cast<f32x4*>(dst + row * D + ch) = v;
+        if (ch == 0) dst[16 * D + row] = top, dst[16 * D + 16 + row] = l;
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int rr = t.r0 + row;
+        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + ch;
+        *reinterpret_cast<uint2*>(dst) =
+            uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
+      }
+    }
+    __syncthreads();
+  });
+}
+
+constexpr int kRowsWorkers = 512;  // two workgroups a CU
+
+// Steps of an item at most, as far as the host can tell.
+int max_steps(const KvView& c, const KvAttn& a) {
+  const int64_t cap = ((int64_t)c.width << c.lb) / kKvStep + 1;
+  return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, (a.window + c.max_new) / kKvStep + 2) : cap);
 }
 
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
-  const int qtiles = ((int64_t)c.max_new * a.G + 15) / 16;
-  MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3((unsigned)(c.n_seq * qtiles * c.H)), dim3(64 * kWaves), 0, stream, c,
-               a, qtiles);
+  const int64_t tiles = ((int64_t)c.max_new * a.G + 15) / 16, items = tiles * c.n_seq * c.H;
+  KvSched d{0, (int)tiles, 2, 8, 0, 8, 0, INT32_MAX};
+  if (items > (1 << 20) || max_steps(c, a) > 20) d.workers = kRowsWorkers;
+  MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3(d.workers ? d.workers : (unsigned)items), dim3(64 * kWaves), 0, stream,
+               c, a, d);
+  if (d.workers)
+    MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
   return launched();
 }
 
@@ -301,7 +335,9 @@ bool kv_attention_dim(int dim) {
          dim == 256;
 }
 
-size_t kv_work_bytes(const KvView&, int) { return 0; }
+size_t kv_work_bytes(const KvView& c, int heads) {
+  return c.n_rows == 0 || heads == 0 ? 0 : sched_bytes(kRowsWorkers, 16, c.D);
+}
 
 hipError_t launch_kv_attention(const KvView& c, const KvAttn& a, hipStream_t stream) {
   switch (c.D) {

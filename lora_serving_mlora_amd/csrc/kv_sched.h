@@ -1,0 +1,318 @@
+// How the attention's work is dealt to a fixed number of workgroups when the
+// lengths are only known on the device.
+//
+// An item is a tile of R rows of one (sequence, key/value head); it walks its
+// visible tokens in steps of 64.  Items lie on a line in the order (sequence,
+// head, tile), each as long as its steps plus `over` for what an item costs
+// besides; workgroup w takes the w-th of `workers` equal parts of the line, so
+// one long sequence is cut into many pieces and many short ones are packed
+// together, and no length is ever read by the host.  A cut that falls within
+// `tol` of an item's end is moved there (by both neighbours alike), which
+// keeps pieces from being tiny.  The order and the cuts depend on the batch
+// alone, so results are the same from call to call.
+//
+// A cut item's pieces go to the caller's work buffer as (O, M, L) and are
+// joined by kv_join_kernel: worker w's slot 2w holds the piece that its part
+// begins inside of, slot 2w + 1 the piece that its part ends inside of.
+#pragma once
+
+#include "kv.h"
+
+namespace mlora {
+
+constexpr int kKvStep = 64;  // tokens of a step
+
+struct KvSched {
+  int workers;             // parts, 0: workgroup i takes item i whole
+  int tiles;               // with workers 0: tiles of a (sequence, head) at most
+  int over, tol_div, mirror, min_share;
+  int min_rows, max_rows;  // sequences with other numbers of rows are left out
+};
+
+struct Span {
+  int lo, hi;  // tokens lo <= t < hi
+};
+
+// What new token j of a sequence sees.  What lies past the table is
+// represented by its first token there, which has no page, so that a wrong
+// kv_len costs no more than a full table.
+__device__ __forceinline__ Span row_span(const KvView& c, const KvAttn& a, const KvSeq& s, int j) {
+  Span v{0, max(s.n, 0)};
+  if (a.causal) {
+    v.hi = max(0, s.n - s.m + j + 1);
+    if (a.window > 0) v.lo = max(0, v.hi - a.window);
+  }
+  const int end = c.width << c.lb;
+  if (v.hi > end) v = {min(v.lo, end), end + 1};
+  return v;
+}
+
+// A tile's rows and steps.  Rows: a (sequence, key/value head) has m * G of
+// them, row r being new token r / G and query head h * G + r % G.
+template <int R>
+struct Tile {
+  int r0, r1;          // first and last row
+  int lo, hi;          // tokens seen by some row
+  int every_lo, every_hi;  // tokens seen by every row
+  int step0, steps;    // at least one step
+
+  __device__ __forceinline__ Tile(const KvView& c, const KvAttn& a, const KvSeq& s, int tile) {
+    r0 = tile * R;
+    r1 = min(r0 + R, s.m * a.G) - 1;
+    const Span x = row_span(c, a, s, r0 / a.G), y = row_span(c, a, s, r1 / a.G);
+    lo = x.lo;
+    hi = y.hi;
+    every_lo = y.lo;
+    every_hi = x.hi;
+    step0 = lo / kKvStep;
+    steps = max(1, (hi + kKvStep - 1) / kKvStep - step0);
+  }
+};
+
+__device__ __forceinline__ bool sched_takes(const KvSched& d, int rows) {
+  return rows > d.min_rows && rows <= d.max_rows;
+}
+
+// with `mirror` long and short tiles of a causal sequence alternate, so that
+// equal parts of the line hold nearly equal numbers of whole items
+__device__ __forceinline__ int sched_tile(const KvSched& d, int k, int tiles) {
+  return d.mirror ? (k & 1 ? tiles - 1 - (k >> 1) : k >> 1) : k;
+}
+
+// a place on the line: `off` into tile number k (in the line's order) of head h
+struct SchedPos {
+  int64_t p;
+  int seq, h, k, off;
+};
+
+struct SchedLds {
+  int64_t sum[4];
+  SchedPos pos[2];
+};
+
+// line length of one head of sequence i
+template <int R>
+__device__ int64_t sched_cost(const KvView& c, const KvAttn& a, const KvSched& d, int i) {
+  const KvSeq s = kv_seq(c, i);
+  const int rows = s.m * a.G;
+  if (!sched_takes(d, rows)) return 0;
+  int64_t sum = 0;
+  for (int t = 0; t * R < rows; ++t) sum += Tile<R>(c, a, s, t).steps + d.over;
+  return sum;
+}
+
+// The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p),
+// found by 256 threads that each add up a run of the sequences.
+template <int R>
+__device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, const KvSched& d, int w, SchedLds& L) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int per = (c.n_seq + 255) / 256, i0 = tid * per, i1 = min(i0 + per, c.n_seq);
+  int64_t own = 0;
+  for (int i = i0; i < i1; ++i) own += sched_cost<R>(c, a, d, i);
+  own *= c.H;
+  int64_t incl = own;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int64_t y = __shfl_up(incl, m, 64);
+    if (lane >= m) incl += y;
+  }
+  if (lane == 63) L.sum[tid >> 6] = incl;
+  __syncthreads();
+  int64_t total = 0;
+  for (int v = 0; v < 4; ++v) {
+    if (v < tid >> 6) incl += L.sum[v];
+    total += L.sum[v];
+  }
+  const int64_t share = max<int64_t>((total + d.workers - 1) / d.workers, d.min_share);
+  const int64_t tol = max<int64_t>(share / d.tol_div, d.over);
+  if (tid < 2) L.pos[tid] = {total, 0, 0, 0, 0};  // for ends past the line
+  __syncthreads();
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    const int64_t p = share * (w + b);
+    if (p < incl - own || p >= incl) continue;  // one thread at most holds the place
+    int64_t at = incl - own;
+    for (int i = i0; i < i1; ++i) {
+      const int64_t head = sched_cost<R>(c, a, d, i);
+      if (p >= at + head * c.H) {
+        at += head * c.H;
+        continue;
+      }
+      const KvSeq s = kv_seq(c, i);
+      const int tiles = (s.m * a.G + R - 1) / R;
+      SchedPos q{p, i, (int)((p - at) / head), 0, 0};
+      at += q.h * head;
+      for (;; ++q.k) {
+        const int len = Tile<R>(c, a, s, sched_tile(d, q.k, tiles)).steps + d.over;
+        if (p < at + len) {
+          q.off = (int)(p - at);
+          if (q.off <= tol) {
+            q.off = 0;
+            q.p = at;
+          } else if (at + len - p <= tol) {
+            q.p = at + len;
+            q.off = len;  // the caller goes on to the next item
+          }
+          break;
+        }
+        at += len;
+      }
+      L.pos[b] = q;
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+// words of a worker's entry in the work buffer: whether its first piece began
+// before its part (0 no, 1 and ends in it, 2 and goes on past it), and the
+// item that it begins and does not end (sequence or -1, head, tile)
+constexpr int kSchedMeta = 4;
+constexpr int kSchedMaxWorkers = 1024;
+__host__ __device__ constexpr size_t sched_slot_floats(int R, int D) { return (size_t)R * (D + 2); }
+inline size_t sched_bytes(int workers, int R, int D) {
+  return (size_t)kSchedMaxWorkers * kSchedMeta * 4 + (size_t)workers * 2 * sched_slot_floats(R, D) * 4;
+}
+__device__ __forceinline__ int* sched_meta(void* work, int w) { return static_cast<int*>(work) + w * kSchedMeta; }
+// slot: O [R][D], M [R], L [R]
+__device__ __forceinline__ float* sched_slot(void* work, int slot, int R, int D) {
+  return reinterpret_cast<float*>(static_cast<char*>(work) + (size_t)kSchedMaxWorkers * kSchedMeta * 4) +
+         (size_t)slot * sched_slot_floats(R, D);
+}
+
+// Runs body(seq, s, h, tile, t, s0, s1, slot) for every piece of worker w:
+// steps s0 <= i < s1 of the tile's, slot < 0 where the piece is the whole item.
+template <int R, class Body>
+__device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, const KvSched& d, SchedLds& L,
+                                          Body&& body) {
+  if (d.workers == 0) {
+    int item = blockIdx.x;
+    const int h = item % c.H;
+    item /= c.H;
+    const int tile = item % d.tiles, seq = item / d.tiles;
+    const KvSeq s = kv_seq(c, seq);
+    if (!sched_takes(d, s.m * a.G) || tile * R >= s.m * a.G) return;
+    const Tile<R> t(c, a, s, tile);
+    body(seq, s, h, tile, t, 0, t.steps, -1);
+    return;
+  }
+  // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
+  // turn), whose L2 then serves the tiles that share keys and values
+  const int w = (d.workers & 7) == 0 ? (blockIdx.x & 7) * (d.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  sched_part<R>(c, a, d, w, L);
+  const SchedPos b = L.pos[0];
+  const int64_t length = L.pos[1].p - b.p;
+  // the same in every lane: scalars
+  int left = __builtin_amdgcn_readfirstlane((int)min<int64_t>(length, INT32_MAX));
+  int first = 0, tail[3] = {-1, 0, 0};
+  int seq = __builtin_amdgcn_readfirstlane(b.seq), h = __builtin_amdgcn_readfirstlane(b.h);
+  int k = __builtin_amdgcn_readfirstlane(b.k), off = __builtin_amdgcn_readfirstlane(b.off);
+  while (left > 0) {
+    const KvSeq s = kv_seq(c, seq);
+    const int rows = s.m * a.G, tiles = (rows + R - 1) / R;
+    if (!sched_takes(d, rows) || h >= c.H) {
+      ++seq;
+      h = k = off = 0;
+      if (seq >= c.n_seq) break;
+      continue;
+    }
+    if (k >= tiles) {
+      k = off = 0;
+      ++h;
+      continue;
+    }
+    const int tile = sched_tile(d, k, tiles);
+    const Tile<R> t(c, a, s, tile);
+    const int len = t.steps + d.over;
+    if (off >= len) {
+      ++k;
+      off = 0;
+      continue;
+    }
+    const int take = min(left, len - off);
+    const int s0 = max(0, off - d.over), s1 = max(0, off + take - d.over);
+    const bool head = off == 0, end = off + take == len;
+    if (!head) first = end ? 1 : 2;
+    if (head && !end) tail[0] = seq, tail[1] = h, tail[2] = tile;
+    body(seq, s, h, tile, t, s0, s1, head && end ? -1 : 2 * w + (head ? 1 : 0));
+    left -= take;
+    off = 0;
+    ++k;
+  }
+  if (threadIdx.x == 0) {
+    int* m = sched_meta(a.work, w);
+    m[0] = first;
+    m[1] = tail[0];
+    m[2] = tail[1];
+    m[3] = tail[2];
+  }
+}
+
+// Joins the pieces of the item that worker blockIdx.x began and did not end:
+// o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i, the pieces in their order.
+// Eight or more pieces are read side by side (a few rows over a long axis make
+// many small pieces, and one after the other they would cost a memory latency
+// each); blockIdx.y takes a share of the rows.
+template <int R, int D>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int workers) {
+  constexpr int DL = D / 4, NG = 256 / DL;  // lanes of a row, pieces side by side
+  __shared__ __align__(16) float sh[NG][D + 4];
+  const int w = blockIdx.x, tid = threadIdx.x;
+  const int* meta = sched_meta(a.work, w);
+  const int seq = meta[1], h = meta[2], tile = meta[3];
+  if (seq < 0) return;
+  int n = 1;  // the pieces: this one and those of the workers up to the first that ends the item
+  for (int w0 = w + 1; w0 < workers; w0 += 64) {
+    const int x = w0 + (tid & 63);
+    const uint64_t on = __ballot(x < workers && sched_meta(a.work, x)[0] == 2);
+    const int run = on == ~0ull ? 64 : __builtin_ctzll(~on);
+    n += run;
+    if (run < 64) {
+      n += (w0 + run < workers);
+      break;
+    }
+  }
+  const KvSeq s = kv_seq(c, seq);
+  const int r0 = tile * R, cnt = min(R, s.m * a.G - r0), Hq = c.H * a.G;
+  const int d = 4 * (tid % DL), grp = tid / DL;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  for (int r = blockIdx.y; r < cnt; r += gridDim.y) {
+    float M = -__builtin_huge_valf(), L = 0.f;
+    f32x4 o{0, 0, 0, 0};
+    if (grp < NG)
+      for (int i = grp; i < n; i += NG) {
+        const float* slot = sched_slot(a.work, i == 0 ? 2 * w + 1 : 2 * (w + i), R, D);
+        const float m = slot[R * D + r], l = slot[R * D + R + r];
+        const f32x4 v = *reinterpret_cast<const f32x4*>(slot + r * D + d);
+        const float Mn = fmaxf(M, m), ref = Mn == -__builtin_huge_valf() ? 0.f : Mn;
+        const float f = __builtin_amdgcn_exp2f(M - ref), e = __builtin_amdgcn_exp2f(m - ref);
+        M = Mn;
+        L = L * f + l * e;
+        o = o * f + v * e;
+      }
+    __syncthreads();
+    if (grp < NG) {
+      *reinterpret_cast<f32x4*>(&sh[grp][d]) = o;
+      if (d == 0) sh[grp][D] = M, sh[grp][D + 1] = L;
+    }
+    __syncthreads();
+    if (tid < DL) {
+      float top = sh[0][D];
+      for (int i = 1; i < NG; ++i) top = fmaxf(top, sh[i][D]);
+      const float ref = top == -__builtin_huge_valf() ? 0.f : top;
+      float l = 0.f;
+      f32x4 v{0, 0, 0, 0};
+      for (int i = 0; i < NG; ++i) {
+        const float f = __builtin_amdgcn_exp2f(sh[i][D] - ref);
+        l += sh[i][D + 1] * f;
+        v += *reinterpret_cast<const f32x4*>(&sh[i][d]) * f;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int rr = r0 + r;
+      uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + d;
+      *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
+    }
+  }
+}
+
+}  // namespace mlora

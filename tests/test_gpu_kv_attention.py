@@ -55,6 +55,28 @@ def test_causal(name, heads, group, dim, block):
 
 
 @pytest.mark.parametrize("name", sorted(BATCHES))
+@pytest.mark.parametrize("heads,group,dim,block", SHAPES)
+def test_wide_tables(name, heads, group, dim, block):
+    """Tables with room for long sequences: the work is dealt in parts, and
+    cut sequences are joined."""
+    new, total = BATCHES[name]
+    total = [n + 700 * (i % 3 == 1 and m > 0) for i, (m, n) in enumerate(zip(new, total))]
+    c = Case(dim + len(name), new, total, heads, dim, block, width=8192 // block)
+    _run(c, _queries(c, group), f"wide {name} heads={heads}x{group} dim={dim} block={block}")
+
+
+def test_many_ragged_sequences():
+    rng = np.random.default_rng(2)
+    for lo, hi in ((0, 2), (0, 40)):
+        new = [int(x) for x in rng.integers(lo, hi, size=600 if hi == 2 else 40)]
+        total = [m + int(x) * (m > 0) for m, x in zip(new, rng.integers(0, 300, size=len(new)))]
+        c = Case(79, new, total, 1, 64, 16, width=512)
+        _fill_new_plain(c)
+        _run(c, _queries(c, 3), f"ragged {hi}")
+        _run(c, _queries(c, 3), f"ragged {hi}, window", window=33, max_new=c.n_rows)
+
+
+@pytest.mark.parametrize("name", sorted(BATCHES))
 @pytest.mark.parametrize("kw", [dict(causal=False), dict(window=1), dict(window=7), dict(window=64), dict(window=100),
                                 dict(window=5000), dict(scale=0.7)], ids=str)
 def test_masks(name, kw):
