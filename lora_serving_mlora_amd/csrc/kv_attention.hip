@@ -308,7 +308,345 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAtt
   });
 }
 
-constexpr int kRowsWorkers = 512;  // two workgroups a CU
+// ----------------------------------------------------------------------------
+// Many rows: 128 * NT rows of one (sequence, key/value head), 32 * NT a wave.
+// A step's 64 tokens are converted to bf16 once for the workgroup, on the way
+// from registers into LDS (two buffers, one barrier a step: the next step's
+// codes are converted and the one after's loads issued before the products),
+// and every wave runs S^T = K Q^T and O^T = V^T P^T over them with 32x32x16
+// products.  As in the few-row kernel the keys' rows are dealt to the matrix
+// rows so that a lane's 16 scores of a 32-token tile are 16 tokens in order,
+// which are its probabilities in the second product.
+// ----------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ float max_halves(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+// halves of a packed bf16 pair that are NaN: ones there, and what to keep
+__device__ __forceinline__ uint32_t nan_ones(uint32_t w) {
+  return ((w & 0x7fffu) > 0x7f80u ? 0x3f80u : 0u) | ((w & 0x7fff0000u) > 0x7f800000u ? 0x3f800000u : 0u);
+}
+__device__ __forceinline__ uint32_t nan_keep(uint32_t w) {
+  return ((w & 0x7fffu) > 0x7f80u ? 0u : 0xffffu) | ((w & 0x7fff0000u) > 0x7f800000u ? 0u : 0xffff0000u);
+}
+
+template <int D, int NT>
+struct ManyTile {
+  static constexpr int R = 128 * NT;
+  static constexpr int U = D / 8;                 // 16-byte units of a token's keys in LDS
+  static constexpr int G = U % 8 == 0 ? 8 : U % 4 == 0 ? 4 : 2;
+  static constexpr int SH = G == 8 ? 0 : G == 4 ? 1 : 2;
+  static constexpr int T = (D + 31) / 32, DV = 32 * T;
+  static constexpr int NP = (4 * D + 255) / 256;  // pieces of a thread: 16 codes of keys and of values
+  // workgroups of a CU: what registers (two waves a SIMD) and LDS allow
+  static constexpr int PER_CU = NT == 1 && D <= 128 ? 2 : 1;
+  // Units of a row change places with its number, so that the lanes of a
+  // read (8 rows, one unit) fall on different banks.
+  static __device__ __forceinline__ int k_unit(int row, int u) { return row * U + (u ^ ((row >> SH) & (G - 1))); }
+};
+
+template <int D, int NT>
+__global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
+  typedef ManyTile<D, NT> X;
+  constexpr int T = X::T, NP = X::NP, QF = D / 16;
+  __shared__ uint4 sh_k[2][64 * X::U];
+  __shared__ uint4 sh_v[2][8 * X::DV];  // [16-token block][half][channel]: 8 tokens a unit
+  __shared__ uint32_t sh_bad[2];        // a byte for each 16-token block without a page
+  __shared__ int sh_nan[2];             // step whose values hold a NaN, plus 1
+  __shared__ SchedLds sh_sched;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
+  const float cs = a.scale * 1.4426950408889634f;
+  if (tid < 2) sh_nan[tid] = 0;
+
+  sched_run<X::R>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0, int s1,
+                                         int slot) __attribute__((always_inline)) {
+    const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
+    const bool active = w0 <= t.r1;
+    Span mine[NT];
+    bf16x8 qf[NT][QF];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = min(w0 + 32 * n + q, t.r1), j = r / a.G;
+      mine[n] = row_span(c, a, s, j);
+      const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs + 8 * hf;
+#pragma unroll
+      for (int i = 0; i < QF; ++i) {
+        uint4 x{};
+        if (vec) {
+          x = *reinterpret_cast<const uint4*>(p + 16 * i);
+        } else {
+          auto two = [&](int e) { return p[16 * i + e] | (uint32_t)p[16 * i + e + 1] << 16; };
+          x = uint4{two(0), two(2), two(4), two(6)};
+        }
+        qf[n][i] = __builtin_bit_cast(bf16x8, x);
+      }
+    }
+    // what all and what some of the wave's rows see
+    const Span wa = row_span(c, a, s, min(w0, t.r1) / a.G), wb = row_span(c, a, s, min(w0 + 32 * NT - 1, t.r1) / a.G);
+
+    f32x16 o[NT][T];
+    float M[NT], L[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      M[n] = -kInf;
+      L[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[n][i][e] = 0.f;
+    }
+
+    // Piece p = tid + 256 i of a step's 4 D: block p / D, 16 bytes at
+    // (p % D) * 16 of the block's 16 D, keys and values alike.
+    int id[NP];
+    uint4 kr[NP], vr[NP];
+    float ks[NP], vs[NP];
+    bool bad[NP];
+    auto ids = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int p = tid + 256 * i, tok = step * kKvStep + 16 * (p / D);
+        id[i] = p < 4 * D && tok < t.hi ? kv_page(c, seq, tok >> c.lb) : 0;
+      }
+    };
+    auto load = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int p = tid + 256 * i, tok = step * kKvStep + 16 * (p / D);
+        if (p < 4 * D) {
+          const size_t ph = (size_t)max(id[i], 0) * c.H + h;
+          const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D + (p % D) * 16;
+          kr[i] = *reinterpret_cast<const uint4*>(c.k + at);
+          vr[i] = *reinterpret_cast<const uint4*>(c.v + at);
+          bad[i] = id[i] < 0;
+          ks[i] = c.k_scale[ph];
+          vs[i] = !bad[i] && tok < t.hi && tok + 16 > t.lo ? c.v_scale[ph] : 1.f;
+        }
+      }
+    };
+    auto store = [&](int step, int buf) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int p = tid + 256 * i, blk = p / D, at = p % D;
+        if (p < 4 * D) {
+          const int x = at / (D / 16), u = at % (D / 16);  // token of the block, unit pair
+          const int row = 32 * (blk >> 1) + 8 * (x >> 2) + 4 * (blk & 1) + (x & 3);
+          const uint4 k = kr[i], v = vr[i];
+          sh_k[buf][X::k_unit(row, 2 * u)] = uint4{kv_bf2<false>(k.x, ks[i]), kv_bf2<true>(k.x, ks[i]),
+                                                   kv_bf2<false>(k.y, ks[i]), kv_bf2<true>(k.y, ks[i])};
+          sh_k[buf][X::k_unit(row, 2 * u + 1)] = uint4{kv_bf2<false>(k.z, ks[i]), kv_bf2<true>(k.z, ks[i]),
+                                                       kv_bf2<false>(k.w, ks[i]), kv_bf2<true>(k.w, ks[i])};
+          sh_v[buf][(2 * blk) * X::DV + at] = uint4{kv_bf2<false>(v.x, vs[i]), kv_bf2<true>(v.x, vs[i]),
+                                                    kv_bf2<false>(v.y, vs[i]), kv_bf2<true>(v.y, vs[i])};
+          sh_v[buf][(2 * blk + 1) * X::DV + at] = uint4{kv_bf2<false>(v.z, vs[i]), kv_bf2<true>(v.z, vs[i]),
+                                                        kv_bf2<false>(v.w, vs[i]), kv_bf2<true>(v.w, vs[i])};
+          any |= nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+          if (at == 0) reinterpret_cast<uint8_t*>(&sh_bad[buf])[blk] = bad[i];
+        }
+      }
+      if (any) sh_nan[buf] = step + 1;
+    };
+
+    const int begin = t.step0 + s0, end = t.step0 + s1;
+    ids(begin);
+    load(begin);
+    if (begin + 1 < end) ids(begin + 1);
+    store(begin, 0);
+    if (begin + 1 < end) load(begin + 1);
+    if (begin + 2 < end) ids(begin + 2);
+    __syncthreads();
+    for (int step = begin; step < end; ++step) {
+      const int buf = (step - begin) & 1, base = step * kKvStep;
+      if (step + 1 < end) store(step + 1, buf ^ 1);
+      if (step + 2 < end) load(step + 2);
+      if (step + 3 < end) ids(step + 3);
+      if (active && base < wb.hi && base + kKvStep > wa.lo) {
+        f32x16 st[2][NT];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) st[x][n][e] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < QF; ++i) {
+            const bf16x8 kf = __builtin_bit_cast(bf16x8, sh_k[buf][X::k_unit(32 * x + q, 2 * i + hf)]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              st[x][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n][i], st[x][n], 0, 0, 0);
+          }
+        const uint32_t bads = __builtin_amdgcn_readfirstlane(sh_bad[buf]);
+        if (bads) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if ((bads >> (8 * (2 * x + hf))) & 1)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) st[x][n][e] = __builtin_nanf("");
+        }
+        const bool edge = base < wb.lo || base + kKvStep > wa.hi;
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (32 * x + e < lo || 32 * x + e >= hi) st[x][n][e] = -kInf;
+          }
+        }
+        float mx[NT];
+        bool up = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float m = fmaxf(st[0][n][0], st[1][n][0]);
+#pragma unroll
+          for (int e = 1; e < 16; ++e) m = fmaxf(fmaxf(m, st[0][n][e]), st[1][n][e]);
+          mx[n] = max_halves(m) * cs;
+          up |= mx[n] > M[n] + kSlack;
+        }
+        if (__ballot(up)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float Mn = fmaxf(M[n], mx[n]), f = Mn == M[n] ? 1.f : __builtin_amdgcn_exp2f(M[n] - Mn);
+            M[n] = Mn;
+            L[n] *= f;
+#pragma unroll
+            for (int i = 0; i < T; ++i) o[n][i] *= f;
+          }
+        }
+        uint32_t pw[NT][2][8];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float ref = M[n] == -kInf ? 0.f : M[n];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][n][e], cs, -ref));
+              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][n][e + 1], cs, -ref));
+              L[n] += p0 + p1;
+              pw[n][x][e / 2] = pack_bf2_hw(p0, p1);
+            }
+        }
+        if (edge && sh_nan[buf] == step + 1) {
+          // as in the few-row kernel: NaN values reach only the rows that see them
+#pragma unroll 1
+          for (int i = 0; i < T; ++i) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              f32x16 hit;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) hit[e] = 0.f;
+              const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const uint4 v = sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q];
+                  uint32_t see[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int e = 32 * x + 8 * u + 2 * k;
+                    see[k] = (e >= lo && e < hi ? 0x3f80u : 0u) | (e + 1 >= lo && e + 1 < hi ? 0x3f800000u : 0u);
+                  }
+                  hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                      frag(nan_ones(v.x), nan_ones(v.y), nan_ones(v.z), nan_ones(v.w)),
+                      frag(see[0], see[1], see[2], see[3]), hit, 0, 0, 0);
+                }
+#pragma unroll
+              for (int k = 0; k < T; ++k)
+                if (k == i)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    if (hit[e] > 0.f) o[n][k][e] = __builtin_nanf("");
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint4 v = sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q];
+                v = uint4{v.x & nan_keep(v.x), v.y & nan_keep(v.y), v.z & nan_keep(v.z), v.w & nan_keep(v.w)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                      __builtin_bit_cast(bf16x8, v),
+                      frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]), o[n][i], 0,
+                      0, 0);
+              }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < T; ++i) {
+                const bf16x8 vf = __builtin_bit_cast(bf16x8, sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                      vf, frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]),
+                      o[n][i], 0, 0, 0);
+              }
+        }
+      }
+      __syncthreads();
+    }
+
+    const int Hq = c.H * a.G;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float l = sum_halves(L[n]);
+      const int row = wave * 32 * NT + 32 * n + q, rr = t.r0 + row;
+      if (rr > t.r1) continue;
+      if (slot >= 0) {
+        float* dst = sched_slot(a.work, slot, X::R, D);
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int ch = 32 * i + 2 * e + 4 * hf;
+            if (ch < D)
+              *reinterpret_cast<f32x4*>(dst + row * D + ch) =
+                  f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]};
+          }
+        if (hf == 0) dst[X::R * D + row] = M[n], dst[X::R * D + X::R + row] = l;
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D;
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int ch = 32 * i + 2 * e + 4 * hf;
+            if (ch < D)
+              *reinterpret_cast<uint2*>(dst + ch) = uint2{pack_bf2_hw(o[n][i][e] * inv, o[n][i][e + 1] * inv),
+                                                          pack_bf2_hw(o[n][i][e + 2] * inv, o[n][i][e + 3] * inv)};
+          }
+      }
+    }
+  });
+}
+
+constexpr int kRowsWorkers = 512;   // few-row kernel: two workgroups a CU
+constexpr int kTileWorkers = 512;   // at most
+constexpr int kFewRows = 16;
 
 // Steps of an item at most, as far as the host can tell.
 int max_steps(const KvView& c, const KvAttn& a) {
@@ -316,15 +654,29 @@ int max_steps(const KvView& c, const KvAttn& a) {
   return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, (a.window + c.max_new) / kKvStep + 2) : cap);
 }
 
+// Sequences of at most kFewRows rows (new tokens times query heads of a
+// key/value head) take the few-row kernel, the others the many-row one; each
+// is launched unless the batch cannot hold a sequence for it.
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
-  const int64_t tiles = ((int64_t)c.max_new * a.G + 15) / 16, items = tiles * c.n_seq * c.H;
-  KvSched d{0, (int)tiles, 2, 8, 0, 8, 0, INT32_MAX};
-  if (items > (1 << 20) || max_steps(c, a) > 20) d.workers = kRowsWorkers;
-  MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3(d.workers ? d.workers : (unsigned)items), dim3(64 * kWaves), 0, stream,
-               c, a, d);
-  if (d.workers)
-    MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
+  const int64_t rows = (int64_t)c.max_new * a.G;
+  const bool many = rows > kFewRows, few = !many || c.n_rows < (int64_t)c.max_new * c.n_seq;
+  const int steps = max_steps(c, a);
+  if (few) {
+    const int64_t tiles = many ? 1 : (rows + 15) / 16, items = tiles * c.n_seq * c.H;
+    KvSched d{0, (int)tiles, 2, 8, 0, 8, 0, many ? kFewRows : INT32_MAX};
+    if (items > (1 << 20) || steps > 20) d.workers = kRowsWorkers;
+    MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3(d.workers ? d.workers : (unsigned)items), dim3(64 * kWaves), 0,
+                 stream, c, a, d);
+    if (d.workers)
+      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
+  }
+  if (many) {
+    constexpr int NT = 1, R = ManyTile<D, NT>::R;
+    KvSched d{256 * ManyTile<D, NT>::PER_CU, 0, 3, 8, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
+    MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(d.workers), dim3(256), 0, stream, c, a, d);
+    MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(d.workers, 8), dim3(256), 0, stream, c, a, d.workers);
+  }
   return launched();
 }
 
@@ -336,7 +688,9 @@ bool kv_attention_dim(int dim) {
 }
 
 size_t kv_work_bytes(const KvView& c, int heads) {
-  return c.n_rows == 0 || heads == 0 ? 0 : sched_bytes(kRowsWorkers, 16, c.D);
+  if (c.n_rows == 0) return 0;
+  const size_t few = sched_bytes(kRowsWorkers, 16, c.D);
+  return (int64_t)c.max_new * (heads / c.H) > kFewRows ? std::max(few, sched_bytes(kTileWorkers, 128, c.D)) : few;
 }
 
 hipError_t launch_kv_attention(const KvView& c, const KvAttn& a, hipStream_t stream) {
