@@ -43,6 +43,19 @@ __device__ __forceinline__ int kv_page(const KvView& c, int i, int p) {
   return (unsigned)id < (unsigned)c.n_blocks ? id : -1;
 }
 
+// the same for a place that is one for the whole wave: scalar loads (the
+// batch's tables and the scales do not change while attention runs)
+template <class T>
+__device__ __forceinline__ T kv_scalar(const T* p) {
+  typedef const T __attribute__((address_space(4))) * constant;
+  return *(constant)(uintptr_t)p;
+}
+__device__ __forceinline__ int kv_page_scalar(const KvView& c, int i, int p) {
+  int id = -1;
+  if (p >= 0 && p < c.width) id = kv_scalar(c.table + (size_t)i * c.table_stride + p);
+  return (unsigned)id < (unsigned)c.n_blocks ? id : -1;
+}
+
 typedef __bf16 kv_bf16x2 __attribute__((ext_vector_type(2)));
 
 // two e4m3 codes (the low or high half of w) times 2^e (scale's exponent), as

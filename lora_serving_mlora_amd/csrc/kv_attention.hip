@@ -17,7 +17,6 @@ namespace mlora {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kWaves = 4;
@@ -85,7 +84,7 @@ struct RowsTile {
 // Loads of the next step are issued as soon as the registers they go to have
 // been read (the keys' after the first product, the values' after the second),
 // and its page ids a step before that.
-template <int D>
+template <int D, bool WHOLE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
   constexpr int R = RowsTile<D>::R, T = RowsTile<D>::T, LD = D + 4;
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
@@ -96,8 +95,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAtt
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
 
-  sched_run<16>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0, int s1,
-                                       int slot) __attribute__((always_inline)) {
+  sched_run<16, WHOLE>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0,
+                                              int s1, int slot) __attribute__((always_inline)) {
     const int r = min(t.r0 + q, t.r1), j = r / a.G;
     const Span mine = row_span(c, a, s, j);
     bf16x8 qf[R][2];
@@ -297,11 +296,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAtt
         *reinterpret_cast<f32x4*>(dst + row * D + ch) = v;
         if (ch == 0) dst[16 * D + row] = top, dst[16 * D + 16 + row] = l;
       } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int rr = t.r0 + row;
-        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + ch;
-        *reinterpret_cast<uint2*>(dst) =
-            uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
+        write_row<D>(a, s, Hq, h, t.r0 + row, ch, v, l);
       }
     }
     __syncthreads();
@@ -328,14 +323,6 @@ __device__ __forceinline__ float sum_halves(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
-// halves of a packed bf16 pair that are NaN: ones there, and what to keep
-__device__ __forceinline__ uint32_t nan_ones(uint32_t w) {
-  return ((w & 0x7fffu) > 0x7f80u ? 0x3f80u : 0u) | ((w & 0x7fff0000u) > 0x7f800000u ? 0x3f800000u : 0u);
-}
-__device__ __forceinline__ uint32_t nan_keep(uint32_t w) {
-  return ((w & 0x7fffu) > 0x7f80u ? 0u : 0xffffu) | ((w & 0x7fff0000u) > 0x7f800000u ? 0u : 0xffff0000u);
-}
-
 template <int D, int NT>
 struct ManyTile {
   static constexpr int R = 128 * NT;
@@ -343,7 +330,7 @@ struct ManyTile {
   static constexpr int G = U % 8 == 0 ? 8 : U % 4 == 0 ? 4 : 2;
   static constexpr int SH = G == 8 ? 0 : G == 4 ? 1 : 2;
   static constexpr int T = (D + 31) / 32, DV = 32 * T;
-  static constexpr int NP = (4 * D + 255) / 256;  // pieces of a thread: 16 codes of keys and of values
+  static constexpr int NP = (D + 63) / 64;        // 16-byte pieces of a lane: a wave brings in one 16-token block
   // workgroups of a CU: what registers (two waves a SIMD) and LDS allow
   static constexpr int PER_CU = NT == 1 && D <= 128 ? 2 : 1;
   // Units of a row change places with its number, so that the lanes of a
@@ -356,9 +343,10 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
   typedef ManyTile<D, NT> X;
   constexpr int T = X::T, NP = X::NP, QF = D / 16;
   __shared__ uint4 sh_k[2][64 * X::U];
-  __shared__ uint4 sh_v[2][8 * X::DV];  // [16-token block][half][channel]: 8 tokens a unit
-  __shared__ uint32_t sh_bad[2];        // a byte for each 16-token block without a page
-  __shared__ int sh_nan[2];             // step whose values hold a NaN, plus 1
+  __shared__ uint4 sh_v[2][8 * X::DV];      // [16-token block][half][channel]: 8 tokens a unit
+  __shared__ uint32_t sh_mark[2][4 * X::DV];  // [block][channel]: a bit for each token whose value is NaN
+  __shared__ uint32_t sh_bad[2];            // a byte for each block without a page
+  __shared__ int sh_nan[2];                 // step with marks, plus 1
   __shared__ SchedLds sh_sched;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
@@ -366,8 +354,17 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
   const float cs = a.scale * 1.4426950408889634f;
   if (tid < 2) sh_nan[tid] = 0;
 
-  sched_run<X::R>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0, int s1,
-                                         int slot) __attribute__((always_inline)) {
+  // Piece i of this lane: bytes 16 (lane + 64 i) of the block's keys and of its
+  // values (both 16 D bytes); its places in LDS.
+  int koff[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int at = lane + 64 * i, x = at / (D / 16), u = at % (D / 16);  // token of the block, unit pair
+    koff[i] = X::k_unit(32 * (wave >> 1) + 8 * (x >> 2) + 4 * (wave & 1) + (x & 3), 2 * u);
+  }
+
+  sched_run<X::R, false>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0,
+                                                int s1, int slot) __attribute__((always_inline)) {
     const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
     const bool active = w0 <= t.r1;
     Span mine[NT];
@@ -404,56 +401,64 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
         for (int e = 0; e < 16; ++e) o[n][i][e] = 0.f;
     }
 
-    // Piece p = tid + 256 i of a step's 4 D: block p / D, 16 bytes at
-    // (p % D) * 16 of the block's 16 D, keys and values alike.
-    int id[NP];
-    uint4 kr[NP], vr[NP];
-    float ks[NP], vs[NP];
-    bool bad[NP];
-    auto ids = [&](int step) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = tid + 256 * i, tok = step * kKvStep + 16 * (p / D);
-        id[i] = p < 4 * D && tok < t.hi ? kv_page(c, seq, tok >> c.lb) : 0;
-      }
+    auto split = [&](int step) {  // rows differ in what they see of it
+      return step * kKvStep < t.every_lo || (step + 1) * kKvStep > t.every_hi;
     };
+    int id_next = 0;  // page of this wave's block, all scalar
+    auto ids = [&](int step) {
+      const int tok = step * kKvStep + 16 * wave;
+      id_next = tok < t.hi ? kv_page_scalar(c, seq, tok >> c.lb) : 0;
+    };
+    uint4 kr[NP], vr[NP];
+    float ks, vs;
+    bool bad;
     auto load = [&](int step) {
+      const int tok = step * kKvStep + 16 * wave;
+      const size_t ph = (size_t)max(id_next, 0) * c.H + h;
+      const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D;
+      const uint4 *kp = reinterpret_cast<const uint4*>(c.k + at), *vp = reinterpret_cast<const uint4*>(c.v + at);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = tid + 256 * i, tok = step * kKvStep + 16 * (p / D);
-        if (p < 4 * D) {
-          const size_t ph = (size_t)max(id[i], 0) * c.H + h;
-          const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D + (p % D) * 16;
-          kr[i] = *reinterpret_cast<const uint4*>(c.k + at);
-          vr[i] = *reinterpret_cast<const uint4*>(c.v + at);
-          bad[i] = id[i] < 0;
-          ks[i] = c.k_scale[ph];
-          vs[i] = !bad[i] && tok < t.hi && tok + 16 > t.lo ? c.v_scale[ph] : 1.f;
-        }
-      }
+      for (int i = 0; i < NP; ++i)
+        if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
+      bad = id_next < 0;
+      ks = kv_scalar(c.k_scale + ph);
+      vs = !bad && tok < t.hi && tok + 16 > t.lo ? kv_scalar(c.v_scale + ph) : 1.f;
     };
     auto store = [&](int step, int buf) {
-      uint32_t any = 0;
+      if (split(step)) {
+        // A NaN among the values must reach the rows that see it, and no
+        // other: it is taken out here, and its place marked for the rows.
+        uint32_t any = 0;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = tid + 256 * i, blk = p / D, at = p % D;
-        if (p < 4 * D) {
-          const int x = at / (D / 16), u = at % (D / 16);  // token of the block, unit pair
-          const int row = 32 * (blk >> 1) + 8 * (x >> 2) + 4 * (blk & 1) + (x & 3);
-          const uint4 k = kr[i], v = vr[i];
-          sh_k[buf][X::k_unit(row, 2 * u)] = uint4{kv_bf2<false>(k.x, ks[i]), kv_bf2<true>(k.x, ks[i]),
-                                                   kv_bf2<false>(k.y, ks[i]), kv_bf2<true>(k.y, ks[i])};
-          sh_k[buf][X::k_unit(row, 2 * u + 1)] = uint4{kv_bf2<false>(k.z, ks[i]), kv_bf2<true>(k.z, ks[i]),
-                                                       kv_bf2<false>(k.w, ks[i]), kv_bf2<true>(k.w, ks[i])};
-          sh_v[buf][(2 * blk) * X::DV + at] = uint4{kv_bf2<false>(v.x, vs[i]), kv_bf2<true>(v.x, vs[i]),
-                                                    kv_bf2<false>(v.y, vs[i]), kv_bf2<true>(v.y, vs[i])};
-          sh_v[buf][(2 * blk + 1) * X::DV + at] = uint4{kv_bf2<false>(v.z, vs[i]), kv_bf2<true>(v.z, vs[i]),
-                                                        kv_bf2<false>(v.w, vs[i]), kv_bf2<true>(v.w, vs[i])};
-          any |= nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
-          if (at == 0) reinterpret_cast<uint8_t*>(&sh_bad[buf])[blk] = bad[i];
-        }
+        for (int i = 0; i < NP; ++i)
+          if (64 * i + 63 < D || lane + 64 * i < D) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&vr[i]);
+            uint32_t mark = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t n = nan_codes(w[k]);
+              w[k] &= ~(n | (n - (n >> 7)));
+              mark |= ((n >> 7 & 1) | (n >> 14 & 2) | (n >> 21 & 4) | (n >> 28 & 8)) << (4 * k);
+            }
+            sh_mark[buf][wave * X::DV + lane + 64 * i] = mark;
+            any |= mark;
+          }
+        if (any) sh_nan[buf] = step + 1;
       }
-      if (any) sh_nan[buf] = step + 1;
+      if (lane == 0) reinterpret_cast<uint8_t*>(&sh_bad[buf])[wave] = bad;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (64 * i + 63 < D || lane + 64 * i < D) {
+          const uint4 k = kr[i], v = vr[i];
+          sh_k[buf][koff[i]] =
+              uint4{kv_bf2<false>(k.x, ks), kv_bf2<true>(k.x, ks), kv_bf2<false>(k.y, ks), kv_bf2<true>(k.y, ks)};
+          sh_k[buf][koff[i] ^ 1] =
+              uint4{kv_bf2<false>(k.z, ks), kv_bf2<true>(k.z, ks), kv_bf2<false>(k.w, ks), kv_bf2<true>(k.w, ks)};
+          uint4* dst = &sh_v[buf][2 * wave * X::DV + lane + 64 * i];
+          dst[0] = uint4{kv_bf2<false>(v.x, vs), kv_bf2<true>(v.x, vs), kv_bf2<false>(v.y, vs), kv_bf2<true>(v.y, vs)};
+          dst[X::DV] =
+              uint4{kv_bf2<false>(v.z, vs), kv_bf2<true>(v.z, vs), kv_bf2<false>(v.w, vs), kv_bf2<true>(v.w, vs)};
+        }
     };
 
     const int begin = t.step0 + s0, end = t.step0 + s1;
@@ -487,25 +492,53 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
               st[x][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n][i], st[x][n], 0, 0, 0);
           }
         const uint32_t bads = __builtin_amdgcn_readfirstlane(sh_bad[buf]);
-        if (bads) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if ((bads >> (8 * (2 * x + hf))) & 1)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) st[x][n][e] = __builtin_nanf("");
-        }
-        const bool edge = base < wb.lo || base + kKvStep > wa.hi;
-        if (edge) {
+        if (bads != 0 || base < wb.lo || base + kKvStep > wa.hi) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+              const bool none = (bads >> (8 * (2 * x + hf))) & 1;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (none) st[x][n][e] = __builtin_nanf("");
+                if (32 * x + e < lo || 32 * x + e >= hi) st[x][n][e] = -kInf;
+              }
+            }
+          }
+        }
+        if (split(step) && sh_nan[buf] == step + 1) {
+          // the rows that see a marked value: a product of their view (ones)
+          // with the marks (ones)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+              f32x16 hit;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) hit[e] = 0.f;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int ch = 32 * i + q;
+                const uint32_t mark = ch < D ? sh_mark[buf][(2 * x + hf) * X::DV + ch] : 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  uint32_t see[4], at[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int b = 8 * u + 2 * k, e = 32 * x + b;
+                    see[k] = (e >= lo && e < hi ? 0x3f80u : 0u) | (e + 1 >= lo && e + 1 < hi ? 0x3f800000u : 0u);
+                    at[k] = (mark >> b & 1 ? 0x3f80u : 0u) | (mark >> (b + 1) & 1 ? 0x3f800000u : 0u);
+                  }
+                  hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(at[0], at[1], at[2], at[3]),
+                                                                frag(see[0], see[1], see[2], see[3]), hit, 0, 0, 0);
+                }
+              }
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (32 * x + e < lo || 32 * x + e >= hi) st[x][n][e] = -kInf;
+                if (hit[e] > 0.f) o[n][i][e] = __builtin_nanf("");
+            }
           }
         }
         float mx[NT];
@@ -542,69 +575,19 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
               pw[n][x][e / 2] = pack_bf2_hw(p0, p1);
             }
         }
-        if (edge && sh_nan[buf] == step + 1) {
-          // as in the few-row kernel: NaN values reach only the rows that see them
-#pragma unroll 1
-          for (int i = 0; i < T; ++i) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              f32x16 hit;
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) hit[e] = 0.f;
-              const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+            for (int i = 0; i < T; ++i) {
+              const bf16x8 vf = __builtin_bit_cast(bf16x8, sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const uint4 v = sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q];
-                  uint32_t see[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int e = 32 * x + 8 * u + 2 * k;
-                    see[k] = (e >= lo && e < hi ? 0x3f80u : 0u) | (e + 1 >= lo && e + 1 < hi ? 0x3f800000u : 0u);
-                  }
-                  hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                      frag(nan_ones(v.x), nan_ones(v.y), nan_ones(v.z), nan_ones(v.w)),
-                      frag(see[0], see[1], see[2], see[3]), hit, 0, 0, 0);
-                }
-#pragma unroll
-              for (int k = 0; k < T; ++k)
-                if (k == i)
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    if (hit[e] > 0.f) o[n][k][e] = __builtin_nanf("");
+              for (int n = 0; n < NT; ++n)
+                o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    vf, frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]), o[n][i],
+                    0, 0, 0);
             }
-          }
-#pragma unroll
-          for (int i = 0; i < T; ++i)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint4 v = sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q];
-                v = uint4{v.x & nan_keep(v.x), v.y & nan_keep(v.y), v.z & nan_keep(v.z), v.w & nan_keep(v.w)};
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                      __builtin_bit_cast(bf16x8, v),
-                      frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]), o[n][i], 0,
-                      0, 0);
-              }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int i = 0; i < T; ++i) {
-                const bf16x8 vf = __builtin_bit_cast(bf16x8, sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                      vf, frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]),
-                      o[n][i], 0, 0, 0);
-              }
-        }
       }
       __syncthreads();
     }
@@ -628,16 +611,13 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
           }
         if (hf == 0) dst[X::R * D + row] = M[n], dst[X::R * D + X::R + row] = l;
       } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D;
 #pragma unroll
         for (int i = 0; i < T; ++i)
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const int ch = 32 * i + 2 * e + 4 * hf;
             if (ch < D)
-              *reinterpret_cast<uint2*>(dst + ch) = uint2{pack_bf2_hw(o[n][i][e] * inv, o[n][i][e + 1] * inv),
-                                                          pack_bf2_hw(o[n][i][e + 2] * inv, o[n][i][e + 3] * inv)};
+              write_row<D>(a, s, Hq, h, rr, ch, f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]}, l);
           }
       }
     }
@@ -666,10 +646,12 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
     const int64_t tiles = many ? 1 : (rows + 15) / 16, items = tiles * c.n_seq * c.H;
     KvSched d{0, (int)tiles, 2, 8, 0, 8, 0, many ? kFewRows : INT32_MAX};
     if (items > (1 << 20) || steps > 20) d.workers = kRowsWorkers;
-    MLORA_LAUNCH("kv_rows", kv_rows_kernel<D>, dim3(d.workers ? d.workers : (unsigned)items), dim3(64 * kWaves), 0,
-                 stream, c, a, d);
-    if (d.workers)
+    if (d.workers) {
+      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(d.workers), dim3(64 * kWaves), 0, stream, c, a, d);
       MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
+    } else {
+      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)items), dim3(64 * kWaves), 0, stream, c, a, d);
+    }
   }
   if (many) {
     constexpr int NT = 1, R = ManyTile<D, NT>::R;

@@ -23,8 +23,8 @@ namespace mlora {
 constexpr int kKvStep = 64;  // tokens of a step
 
 struct KvSched {
-  int workers;             // parts, 0: workgroup i takes item i whole
-  int tiles;               // with workers 0: tiles of a (sequence, head) at most
+  int workers;             // parts
+  int tiles;               // where workgroup i takes item i whole: tiles of a (sequence, head) at most
   int over, tol_div, mirror, min_share;
   int min_rows, max_rows;  // sequences with other numbers of rows are left out
 };
@@ -182,10 +182,11 @@ __device__ __forceinline__ float* sched_slot(void* work, int slot, int R, int D)
 
 // Runs body(seq, s, h, tile, t, s0, s1, slot) for every piece of worker w:
 // steps s0 <= i < s1 of the tile's, slot < 0 where the piece is the whole item.
-template <int R, class Body>
+// WHOLE: no parts, workgroup i takes item i.
+template <int R, bool WHOLE, class Body>
 __device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, const KvSched& d, SchedLds& L,
                                           Body&& body) {
-  if (d.workers == 0) {
+  if constexpr (WHOLE) {
     int item = blockIdx.x;
     const int h = item % c.H;
     item /= c.H;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, cons
     const Tile<R> t(c, a, s, tile);
     body(seq, s, h, tile, t, 0, t.steps, -1);
     return;
-  }
+  } else {
   // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
   // turn), whose L2 then serves the tiles that share keys and values
   const int w = (d.workers & 7) == 0 ? (blockIdx.x & 7) * (d.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
@@ -246,13 +247,24 @@ __device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, cons
     m[2] = tail[1];
     m[3] = tail[2];
   }
+  }
+}
+
+// four channels of row rr of a (sequence, head): o / l, zero where it saw nothing
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+template <int D>
+__device__ __forceinline__ void write_row(const KvAttn& a, const KvSeq& s, int Hq, int h, int rr, int ch, f32x4 o,
+                                          float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + ch;
+  *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(o[0] * inv, o[1] * inv), pack_bf2_hw(o[2] * inv, o[3] * inv)};
 }
 
 // Joins the pieces of the item that worker blockIdx.x began and did not end:
 // o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i, the pieces in their order.
-// Eight or more pieces are read side by side (a few rows over a long axis make
-// many small pieces, and one after the other they would cost a memory latency
-// each); blockIdx.y takes a share of the rows.
+// Many pieces (a few rows over a long axis) are read side by side, as one after
+// the other they would cost a memory latency each; with few, the rows are.
+// blockIdx.y takes a share of the rows.
 template <int R, int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int workers) {
   constexpr int DL = D / 4, NG = 256 / DL;  // lanes of a row, pieces side by side
@@ -275,7 +287,36 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int wo
   const KvSeq s = kv_seq(c, seq);
   const int r0 = tile * R, cnt = min(R, s.m * a.G - r0), Hq = c.H * a.G;
   const int d = 4 * (tid % DL), grp = tid / DL;
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  if (n <= 4) {
+    for (int x = blockIdx.y * 256 + tid; x < cnt * DL; x += gridDim.y * 256) {
+      const int r = x / DL, ch = 4 * (x % DL);
+      float m[4], l[4], top = -__builtin_huge_valf();
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = -__builtin_huge_valf();
+        l[i] = 0.f;
+        v[i] = f32x4{0, 0, 0, 0};
+        if (i < n) {
+          const float* slot = sched_slot(a.work, i == 0 ? 2 * w + 1 : 2 * (w + i), R, D);
+          m[i] = slot[R * D + r], l[i] = slot[R * D + R + r];
+          v[i] = *reinterpret_cast<const f32x4*>(slot + r * D + ch);
+        }
+        top = fmaxf(top, m[i]);
+      }
+      const float ref = top == -__builtin_huge_valf() ? 0.f : top;
+      float L = 0.f;
+      f32x4 o{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
+        L += l[i] * f;
+        o += v[i] * f;
+      }
+      write_row<D>(a, s, Hq, h, r0 + r, ch, o, L);
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < cnt; r += gridDim.y) {
     float M = -__builtin_huge_valf(), L = 0.f;
     f32x4 o{0, 0, 0, 0};
@@ -307,10 +348,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int wo
         l += sh[i][D + 1] * f;
         v += *reinterpret_cast<const f32x4*>(&sh[i][d]) * f;
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int rr = r0 + r;
-      uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + d;
-      *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(v[0] * inv, v[1] * inv), pack_bf2_hw(v[2] * inv, v[3] * inv)};
+      write_row<D>(a, s, Hq, h, r0 + r, d, v, l);
     }
   }
 }
