@@ -537,6 +537,7 @@ class KVCache:
             if tuple(x.shape) != shape:
                 raise ValueError(f"storage: {name} has shape {tuple(x.shape)}, expected {shape}")
         self.k, self.v, self.k_scale, self.v_scale = storage
+        self.device_index = self.k.device.index
         self._d = _KVCacheDesc(n_layers, kv_heads, dim, block, n_blocks, *(x.data_ptr() for x in storage))
         self._ref = ctypes.addressof(self._d)
 
@@ -568,16 +569,21 @@ class KVBatch:
 
 
 def _kv_rows(x, name: str, batch: KVBatch, heads: int, dim: int):
-    """Checks bf16 rows [n_rows][heads][dim]; (row, head) strides in elements."""
-    if x.dtype != _torch().bfloat16 or not x.is_cuda:
+    """Checks bf16 rows [n_rows][heads][dim]; strides in elements."""
+    if x.dtype is not _torch().bfloat16 or not x.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
     shape = x.shape
     if len(shape) != 3 or shape[0] != batch.n_rows or shape[2] != dim or (heads and shape[1] != heads):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [{batch.n_rows}][{heads or 'heads'}][{dim}]")
-    rs, hs, cs = x.stride()
-    if cs != 1:
+    st = x.stride()
+    if st[2] != 1:
         raise TypeError(f"{name} must be dense in its channels")
-    return rs, hs
+    return st
+
+
+def _kv_stream(cache: KVCache) -> int:
+    # the handle alone: building a Stream object costs as much as a small launch
+    return _torch()._C._cuda_getCurrentRawStream(cache.device_index)
 
 
 def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
@@ -586,17 +592,22 @@ def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
     st = _kv_rows(k, "k", batch, cache.kv_heads, cache.dim)
     if _kv_rows(v, "v", batch, cache.kv_heads, cache.dim) != st:
         k, v = k.contiguous(), v.contiguous()
-        st = (cache.kv_heads * cache.dim, cache.dim)
-    _check(lib().mlora_kv_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), *st, batch._ref, _stream()),
-           "mlora_kv_append")
+        st = k.stride()
+    status = lib().mlora_kv_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), st[0], st[1], batch._ref,
+                                   _kv_stream(cache))
+    if status != OK:
+        raise MloraError(status, "mlora_kv_append")
 
 
 def kv_read(cache: KVCache, layer: int, batch: KVBatch):
     """The batch's rows of the cache as bf16: (k, v), [n_rows][kv_heads][dim]."""
     torch = _torch()
-    k, v = (torch.empty((batch.n_rows, cache.kv_heads, cache.dim), dtype=torch.bfloat16, device=cache.k.device)
-            for _ in range(2))
-    _check(lib().mlora_kv_read(cache._ref, layer, batch._ref, k.data_ptr(), v.data_ptr(), _stream()), "mlora_kv_read")
+    shape, dev = (batch.n_rows, cache.kv_heads, cache.dim), cache.k.device
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    status = lib().mlora_kv_read(cache._ref, layer, batch._ref, k.data_ptr(), v.data_ptr(), _kv_stream(cache))
+    if status != OK:
+        raise MloraError(status, "mlora_kv_read")
     return k, v
 
 
@@ -616,17 +627,19 @@ def kv_attention(cache: KVCache, layer: int, q, batch: KVBatch, causal: bool = T
     """Attention of q, bf16 [n_rows][heads][dim], over the batch's sequences;
     scale defaults to dim ** -0.5.  Returns bf16 [n_rows][heads][dim]."""
     torch = _torch()
-    rs, hs = _kv_rows(q, "q", batch, 0, cache.dim)
-    heads = q.shape[1]
+    rs, hs, _ = _kv_rows(q, "q", batch, 0, cache.dim)
+    shape = (batch.n_rows, q.shape[1], cache.dim)
     if out is None:
-        out = torch.empty((batch.n_rows, heads, cache.dim), dtype=torch.bfloat16, device=q.device)
-    elif tuple(_bf16_dev(out, "out").shape) != (batch.n_rows, heads, cache.dim):
-        raise ValueError(f"out must be [{batch.n_rows}][{heads}][{cache.dim}]")
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
+    elif tuple(_bf16_dev(out, "out").shape) != shape:
+        raise ValueError(f"out must be {list(shape)}")
     if work is None:
-        work = new_kv_work(cache, batch, heads)
-    _check(lib().mlora_kv_attention(cache._ref, layer, q.data_ptr(), rs, hs, heads, batch._ref, causal, window,
-                                    cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), work.data_ptr(),
-                                    work.numel() * work.element_size(), _stream()), "mlora_kv_attention")
+        work = new_kv_work(cache, batch, shape[1])
+    status = lib().mlora_kv_attention(cache._ref, layer, q.data_ptr(), rs, hs, shape[1], batch._ref, causal, window,
+                                      cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), work.data_ptr(),
+                                      work.nbytes, _kv_stream(cache))
+    if status != OK:
+        raise MloraError(status, "mlora_kv_attention")
     return out
 
 

@@ -26,13 +26,29 @@ struct KvView {
 struct KvSeq {
   int32_t row0, m, n;  // first row, rows, tokens with the new ones
 };
+__device__ __forceinline__ int kv_clamp(int n) { return min(max(n, -(1 << 30)), 1 << 30); }
 __device__ __forceinline__ KvSeq kv_seq(const KvView& c, int i) {
   KvSeq s;
   const int a = c.row_off[i], b = c.row_off[i + 1];
-  s.n = min(c.kv_len[i], 1 << 30);
-  s.row0 = a < 0 ? 0 : (a > c.n_rows ? c.n_rows : a);
-  const int e = b < s.row0 ? s.row0 : (b > c.n_rows ? c.n_rows : b);
-  s.m = e - s.row0;
+  s.n = kv_clamp(c.kv_len[i]);
+  s.row0 = min(max(a, 0), c.n_rows);
+  s.m = min(max(b, s.row0), c.n_rows) - s.row0;
+  return s;
+}
+
+// a place that is the same for the whole wave: a scalar load (the batch's
+// tables, and while attention runs the scales, do not change)
+template <class T>
+__device__ __forceinline__ T kv_scalar(const T* p) {
+  typedef const T __attribute__((address_space(4))) * constant;
+  return *(constant)(uintptr_t)p;
+}
+__device__ __forceinline__ KvSeq kv_seq_scalar(const KvView& c, int i) {
+  KvSeq s;
+  const int a = kv_scalar(c.row_off + i), b = kv_scalar(c.row_off + i + 1);
+  s.n = kv_clamp(kv_scalar(c.kv_len + i));
+  s.row0 = min(max(a, 0), c.n_rows);
+  s.m = min(max(b, s.row0), c.n_rows) - s.row0;
   return s;
 }
 
@@ -43,13 +59,6 @@ __device__ __forceinline__ int kv_page(const KvView& c, int i, int p) {
   return (unsigned)id < (unsigned)c.n_blocks ? id : -1;
 }
 
-// the same for a place that is one for the whole wave: scalar loads (the
-// batch's tables and the scales do not change while attention runs)
-template <class T>
-__device__ __forceinline__ T kv_scalar(const T* p) {
-  typedef const T __attribute__((address_space(4))) * constant;
-  return *(constant)(uintptr_t)p;
-}
 __device__ __forceinline__ int kv_page_scalar(const KvView& c, int i, int p) {
   int id = -1;
   if (p >= 0 && p < c.width) id = kv_scalar(c.table + (size_t)i * c.table_stride + p);

@@ -323,18 +323,20 @@ __device__ __forceinline__ float sum_halves(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
+constexpr int kAhead = 4;  // reads of an operand from LDS ahead of its product
+
 template <int D, int NT>
 struct ManyTile {
   static constexpr int R = 128 * NT;
   static constexpr int U = D / 8;                 // 16-byte units of a token's keys in LDS
-  static constexpr int G = U % 8 == 0 ? 8 : U % 4 == 0 ? 4 : 2;
-  static constexpr int SH = G == 8 ? 0 : G == 4 ? 1 : 2;
+  static constexpr int G = U % 16 == 0 ? 16 : U % 8 == 0 ? 8 : U % 4 == 0 ? 4 : 2;
+  static constexpr int SH = G == 16 ? 0 : G == 8 ? 1 : G == 4 ? 2 : 3;
   static constexpr int T = (D + 31) / 32, DV = 32 * T;
   static constexpr int NP = (D + 63) / 64;        // 16-byte pieces of a lane: a wave brings in one 16-token block
   // workgroups of a CU: what registers (two waves a SIMD) and LDS allow
   static constexpr int PER_CU = NT == 1 && D <= 128 ? 2 : 1;
-  // Units of a row change places with its number, so that the lanes of a
-  // read (8 rows, one unit) fall on different banks.
+  // Units of a row change places with its number, so that 16 lanes of a
+  // read (16 rows, one unit) fall on different banks.
   static __device__ __forceinline__ int k_unit(int row, int u) { return row * U + (u ^ ((row >> SH) & (G - 1))); }
 };
 
@@ -482,15 +484,25 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 16; ++e) st[x][n][e] = 0.f;
+        // Two chains of products.  Reads from LDS run kAhead products ahead of
+        // their use and the order is fixed (left alone, the compiler puts each
+        // read right before its product, which then waits for it).
+        {
+          uint4 kf[kAhead];
+          auto read = [&](int g) { kf[g % kAhead] = sh_k[buf][X::k_unit(32 * (g & 1) + q, 2 * (g >> 1) + hf)]; };
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int g = 0; g < kAhead; ++g) read(g);
 #pragma unroll
-          for (int i = 0; i < QF; ++i) {
-            const bf16x8 kf = __builtin_bit_cast(bf16x8, sh_k[buf][X::k_unit(32 * x + q, 2 * i + hf)]);
+          for (int g = 0; g < 2 * QF; ++g) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              st[x][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n][i], st[x][n], 0, 0, 0);
+              st[g & 1][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g % kAhead]),
+                                                                     qf[n][g >> 1], st[g & 1][n], 0, 0, 0);
+            if (g + kAhead < 2 * QF) read(g + kAhead);
           }
+          __builtin_amdgcn_sched_barrier(0);
+        }
         const uint32_t bads = __builtin_amdgcn_readfirstlane(sh_bad[buf]);
         if (bads != 0 || base < wb.lo || base + kKvStep > wa.hi) {
 #pragma unroll
@@ -561,33 +573,50 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
             for (int i = 0; i < T; ++i) o[n][i] *= f;
           }
         }
-        uint32_t pw[NT][2][8];
+        // Group c of 8 tokens: its probabilities, then its products, beside which
+        // the next group's probabilities are made, and the reads as above.
+        {
+          float ref[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float ref = M[n] == -kInf ? 0.f : M[n];
+          for (int n = 0; n < NT; ++n) ref[n] = M[n] == -kInf ? 0.f : M[n];
+          uint32_t pw[NT][2][4];  // groups c and c + 1
+          auto prob = [&](int c, int e) {  // tokens 2 e and 2 e + 1 of group c
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][n][e], cs, -ref));
-              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][n][e + 1], cs, -ref));
+            for (int n = 0; n < NT; ++n) {
+              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c >> 1][n][8 * (c & 1) + 2 * e], cs, -ref[n]));
+              const float p1 =
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(st[c >> 1][n][8 * (c & 1) + 2 * e + 1], cs, -ref[n]));
               L[n] += p0 + p1;
-              pw[n][x][e / 2] = pack_bf2_hw(p0, p1);
+              pw[n][c & 1][e] = pack_bf2_hw(p0, p1);
             }
-        }
+          };
+          uint4 vf[kAhead];
+          auto read = [&](int g) {
+            const int c = g / T, i = g % T;
+            vf[g % kAhead] = sh_v[buf][(2 * (2 * (c >> 1) + hf) + (c & 1)) * X::DV + 32 * i + q];
+          };
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int g = 0; g < kAhead; ++g) read(g);
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int e = 0; e < 4; ++e) prob(0, e);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < T; ++i) {
-              const bf16x8 vf = __builtin_bit_cast(bf16x8, sh_v[buf][(2 * (2 * x + hf) + u) * X::DV + 32 * i + q]);
+              const int g = c * T + i;
+              __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
                 o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    vf, frag(pw[n][x][4 * u], pw[n][x][4 * u + 1], pw[n][x][4 * u + 2], pw[n][x][4 * u + 3]), o[n][i],
-                    0, 0, 0);
+                    __builtin_bit_cast(bf16x8, vf[g % kAhead]),
+                    frag(pw[n][c & 1][0], pw[n][c & 1][1], pw[n][c & 1][2], pw[n][c & 1][3]), o[n][i], 0, 0, 0);
+              if (g + kAhead < 4 * T) read(g + kAhead);
+              if (c < 3)
+#pragma unroll
+                for (int e = 4 * i / T; e < 4 * (i + 1) / T; ++e) prob(c + 1, e);
             }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
       __syncthreads();
     }
