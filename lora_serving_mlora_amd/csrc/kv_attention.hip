@@ -406,25 +406,31 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
     auto split = [&](int step) {  // rows differ in what they see of it
       return step * kKvStep < t.every_lo || (step + 1) * kKvStep > t.every_hi;
     };
-    int id_next = 0;  // page of this wave's block, all scalar
+    // Page and scales of this wave's block, one for all its lanes, come by
+    // vector loads all the same: a scalar load in flight would have every read
+    // from LDS wait for it (they share a counter, and it returns in no order).
+    int id_next = 0;
     auto ids = [&](int step) {
-      const int tok = step * kKvStep + 16 * wave;
-      id_next = tok < t.hi ? kv_page_scalar(c, seq, tok >> c.lb) : 0;
+      const int tok = step * kKvStep + 16 * wave, p = tok >> c.lb;
+      id_next = tok < t.hi ? -1 : 0;
+      if (tok < t.hi && p < c.width) id_next = c.table[(size_t)seq * c.table_stride + p];
     };
     uint4 kr[NP], vr[NP];
     float ks, vs;
-    bool bad;
+    bool bad, vin;
     auto load = [&](int step) {
       const int tok = step * kKvStep + 16 * wave;
-      const size_t ph = (size_t)max(id_next, 0) * c.H + h;
+      const int id = __builtin_amdgcn_readfirstlane(id_next);
+      bad = (unsigned)id >= (unsigned)c.n_blocks;
+      vin = !bad && tok < t.hi && tok + 16 > t.lo;
+      const size_t ph = (size_t)(bad ? 0 : id) * c.H + h;
       const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D;
       const uint4 *kp = reinterpret_cast<const uint4*>(c.k + at), *vp = reinterpret_cast<const uint4*>(c.v + at);
+      ks = c.k_scale[ph];
+      vs = c.v_scale[ph];
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
-      bad = id_next < 0;
-      ks = kv_scalar(c.k_scale + ph);
-      vs = !bad && tok < t.hi && tok + 16 > t.lo ? kv_scalar(c.v_scale + ph) : 1.f;
     };
     auto store = [&](int step, int buf) {
       if (split(step)) {
@@ -448,6 +454,7 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
         if (any) sh_nan[buf] = step + 1;
       }
       if (lane == 0) reinterpret_cast<uint8_t*>(&sh_bad[buf])[wave] = bad;
+      const float vsc = vin ? vs : 1.f;
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         if (64 * i + 63 < D || lane + 64 * i < D) {
@@ -457,9 +464,9 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
           sh_k[buf][koff[i] ^ 1] =
               uint4{kv_bf2<false>(k.z, ks), kv_bf2<true>(k.z, ks), kv_bf2<false>(k.w, ks), kv_bf2<true>(k.w, ks)};
           uint4* dst = &sh_v[buf][2 * wave * X::DV + lane + 64 * i];
-          dst[0] = uint4{kv_bf2<false>(v.x, vs), kv_bf2<true>(v.x, vs), kv_bf2<false>(v.y, vs), kv_bf2<true>(v.y, vs)};
+          dst[0] = uint4{kv_bf2<false>(v.x, vsc), kv_bf2<true>(v.x, vsc), kv_bf2<false>(v.y, vsc), kv_bf2<true>(v.y, vsc)};
           dst[X::DV] =
-              uint4{kv_bf2<false>(v.z, vs), kv_bf2<true>(v.z, vs), kv_bf2<false>(v.w, vs), kv_bf2<true>(v.w, vs)};
+              uint4{kv_bf2<false>(v.z, vsc), kv_bf2<true>(v.z, vsc), kv_bf2<false>(v.w, vsc), kv_bf2<true>(v.w, vsc)};
         }
     };
 
@@ -673,7 +680,7 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   const int steps = max_steps(c, a);
   if (few) {
     const int64_t tiles = many ? 1 : (rows + 15) / 16, items = tiles * c.n_seq * c.H;
-    KvSched d{0, (int)tiles, 2, 8, 0, 8, 0, many ? kFewRows : INT32_MAX};
+    KvSched d{0, (int)tiles, 2, 1 << 30, 0, 8, 0, many ? kFewRows : INT32_MAX};
     if (items > (1 << 20) || steps > 20) d.workers = kRowsWorkers;
     if (d.workers) {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(d.workers), dim3(64 * kWaves), 0, stream, c, a, d);
@@ -684,7 +691,7 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   }
   if (many) {
     constexpr int NT = 1, R = ManyTile<D, NT>::R;
-    KvSched d{256 * ManyTile<D, NT>::PER_CU, 0, 3, 8, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
+    KvSched d{256 * ManyTile<D, NT>::PER_CU, 0, 3, 6, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
     MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(d.workers), dim3(256), 0, stream, c, a, d);
     MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(d.workers, 8), dim3(256), 0, stream, c, a, d.workers);
   }

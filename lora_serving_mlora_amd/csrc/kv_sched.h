@@ -6,9 +6,9 @@
 // head, tile), each as long as its steps plus `over` for what an item costs
 // besides; workgroup w takes the w-th of `workers` equal parts of the line, so
 // one long sequence is cut into many pieces and many short ones are packed
-// together, and no length is ever read by the host.  A cut that falls within
-// `tol` of an item's end is moved there (by both neighbours alike), which
-// keeps pieces from being tiny.  The order and the cuts depend on the batch
+// together, and no length is ever read by the host.  A cut that falls close to
+// an item's end is moved there (by both neighbours alike), which keeps pieces
+// from being tiny.  The order and the cuts depend on the batch
 // alone, so results are the same from call to call.
 //
 // A cut item's pieces go to the caller's work buffer as (O, M, L) and are
@@ -25,7 +25,7 @@ constexpr int kKvStep = 64;  // tokens of a step
 struct KvSched {
   int workers;             // parts
   int tiles;               // where workgroup i takes item i whole: tiles of a (sequence, head) at most
-  int over, tol_div, mirror, min_share;
+  int over, tol_max, mirror, min_share;
   int min_rows, max_rows;  // sequences with other numbers of rows are left out
 };
 
@@ -85,9 +85,14 @@ struct SchedPos {
   int seq, h, k, off;
 };
 
+constexpr int kSchedSeqs = 256;  // sequences whose tiles are dealt with side by side
 struct SchedLds {
   int64_t sum[4];
+  int64_t cost[kSchedSeqs];  // line length of one head
+  int64_t at[2];             // start of the head that holds the place
   SchedPos pos[2];
+  int m[kSchedSeqs], n[kSchedSeqs];
+  int before[kSchedSeqs + 1];  // tiles of the sequences before
 };
 
 // line length of one head of sequence i
@@ -101,63 +106,119 @@ __device__ int64_t sched_cost(const KvView& c, const KvAttn& a, const KvSched& d
   return sum;
 }
 
-// The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p),
-// found by 256 threads that each add up a run of the sequences.
-template <int R>
-__device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, const KvSched& d, int w, SchedLds& L) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int per = (c.n_seq + 255) / 256, i0 = tid * per, i1 = min(i0 + per, c.n_seq);
-  int64_t own = 0;
-  for (int i = i0; i < i1; ++i) own += sched_cost<R>(c, a, d, i);
-  own *= c.H;
-  int64_t incl = own;
+template <class T>
+__device__ __forceinline__ T wave_scan(T x) {  // inclusive
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const int64_t y = __shfl_up(incl, m, 64);
-    if (lane >= m) incl += y;
+    const T y = __shfl_up(x, m, 64);
+    if (lane >= m) x += y;
   }
-  if (lane == 63) L.sum[tid >> 6] = incl;
+  return x;
+}
+
+// The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p).
+// Everything that depends on the number of tiles is done by all 256 threads
+// side by side: one thread that went through the tiles of a long prompt alone
+// took longer than the products of a short one.
+template <int R>
+__device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, const KvSched& d, int w, SchedLds& L) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool small = c.n_seq <= kSchedSeqs;
+  const int per = (c.n_seq + 255) / 256, i0 = tid * per, i1 = min(i0 + per, c.n_seq);
+  int64_t own = 0;
+  if (small) {
+    int tiles = 0;
+    if (tid < c.n_seq) {
+      const KvSeq s = kv_seq(c, tid);
+      const int rows = s.m * a.G;
+      if (sched_takes(d, rows)) tiles = (rows + R - 1) / R;
+      L.m[tid] = s.m;
+      L.n[tid] = s.n;
+    }
+    L.cost[tid] = 0;
+    int incl = wave_scan(tiles);
+    if (lane == 63) L.sum[wave] = incl;
+    __syncthreads();
+    for (int v = 0; v < wave; ++v) incl += (int)L.sum[v];
+    L.before[tid + 1] = incl;
+    if (tid == 0) L.before[0] = 0;
+    __syncthreads();
+    const int all = L.before[kSchedSeqs];
+    for (int f = tid; f < all; f += 256) {
+      int i = 0;  // the last sequence that begins at or before tile f
+#pragma unroll
+      for (int x = kSchedSeqs / 2; x > 0; x >>= 1)
+        if (L.before[i + x] <= f) i += x;
+      const KvSeq s{0, L.m[i], L.n[i]};
+      atomicAdd(reinterpret_cast<unsigned long long*>(&L.cost[i]),
+                (unsigned long long)(Tile<R>(c, a, s, f - L.before[i]).steps + d.over));
+    }
+    __syncthreads();
+    own = L.cost[tid];
+  } else {
+    for (int i = i0; i < i1; ++i) own += sched_cost<R>(c, a, d, i);
+  }
+  own *= c.H;
+  int64_t incl = wave_scan(own);
+  if (lane == 63) L.sum[wave] = incl;
   __syncthreads();
   int64_t total = 0;
   for (int v = 0; v < 4; ++v) {
-    if (v < tid >> 6) incl += L.sum[v];
+    if (v < wave) incl += L.sum[v];
     total += L.sum[v];
   }
   const int64_t share = max<int64_t>((total + d.workers - 1) / d.workers, d.min_share);
-  const int64_t tol = max<int64_t>(share / d.tol_div, d.over);
-  if (tid < 2) L.pos[tid] = {total, 0, 0, 0, 0};  // for ends past the line
+  const int64_t tol = min<int64_t>(max<int64_t>(share / 8, d.over), d.tol_max);
+  if (tid < 2) L.pos[tid] = {total, -1, 0, 0, 0};  // for ends past the line
   __syncthreads();
+  // the sequence and head that hold each place (one thread at most holds it)
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
     const int64_t p = share * (w + b);
-    if (p < incl - own || p >= incl) continue;  // one thread at most holds the place
+    if (p < incl - own || p >= incl) continue;
     int64_t at = incl - own;
     for (int i = i0; i < i1; ++i) {
-      const int64_t head = sched_cost<R>(c, a, d, i);
+      const int64_t head = small ? L.cost[tid] : sched_cost<R>(c, a, d, i);
       if (p >= at + head * c.H) {
         at += head * c.H;
         continue;
       }
-      const KvSeq s = kv_seq(c, i);
-      const int tiles = (s.m * a.G + R - 1) / R;
-      SchedPos q{p, i, (int)((p - at) / head), 0, 0};
-      at += q.h * head;
-      for (;; ++q.k) {
-        const int len = Tile<R>(c, a, s, sched_tile(d, q.k, tiles)).steps + d.over;
-        if (p < at + len) {
-          q.off = (int)(p - at);
-          if (q.off <= tol) {
-            q.off = 0;
-            q.p = at;
-          } else if (at + len - p <= tol) {
-            q.p = at + len;
-            q.off = len;  // the caller goes on to the next item
-          }
-          break;
-        }
-        at += len;
+      const int h = (int)((p - at) / head);
+      L.pos[b] = {p, i, h, 0, 0};
+      L.at[b] = at + h * head;
+      break;
+    }
+  }
+  __syncthreads();
+  // its tile, by a wave for each place
+  if (wave < 2 && L.pos[wave].seq >= 0) {
+    SchedPos q = L.pos[wave];
+    const KvSeq s = kv_seq(c, q.seq);
+    const int tiles = (s.m * a.G + R - 1) / R;
+    int64_t at = L.at[wave];
+    for (int k0 = 0; k0 < tiles; k0 += 64) {
+      const int k = k0 + lane;
+      const int len = k < tiles ? Tile<R>(c, a, s, sched_tile(d, k, tiles)).steps + d.over : 0;
+      const int64_t end = at + wave_scan(len);
+      const uint64_t past = __ballot(q.p < end);
+      if (past == 0) {
+        at = __shfl(end, 63, 64);
+        continue;
       }
-      L.pos[b] = q;
+      if (lane == __builtin_ctzll(past)) {
+        const int64_t begin = end - len;
+        q.k = k;
+        q.off = (int)(q.p - begin);
+        if (q.off <= tol) {
+          q.off = 0;
+          q.p = begin;
+        } else if (end - q.p <= tol) {
+          q.p = end;
+          q.off = len;  // the caller goes on to the next item
+        }
+        L.pos[wave] = q;
+      }
       break;
     }
   }
@@ -212,9 +273,16 @@ __device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, cons
     const KvSeq s = kv_seq(c, seq);
     const int rows = s.m * a.G, tiles = (rows + R - 1) / R;
     if (!sched_takes(d, rows) || h >= c.H) {
-      ++seq;
+      // on to the next sequence that has tiles, 64 looked at together
       h = k = off = 0;
-      if (seq >= c.n_seq) break;
+      uint64_t has = 0;
+      for (++seq; seq < c.n_seq; seq += 64) {
+        const int i = seq + (int)(threadIdx.x & 63);
+        has = __ballot(i < c.n_seq && sched_takes(d, kv_seq(c, min(i, c.n_seq - 1)).m * a.G));
+        if (has) break;
+      }
+      if (!has) break;
+      seq += __builtin_ctzll(has);
       continue;
     }
     if (k >= tiles) {
