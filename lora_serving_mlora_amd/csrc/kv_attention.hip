@@ -84,18 +84,22 @@ struct RowsTile {
 // Loads of the next step are issued as soon as the registers they go to have
 // been read (the keys' after the first product, the values' after the second),
 // and its page ids a step before that.
+template <int D>
+struct RowsLds {
+  float m[kWaves][16], l[kWaves][16];
+  float o[kWaves][16][D + 4];
+  SchedLds sched;
+};
+
 template <int D, bool WHOLE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
-  constexpr int R = RowsTile<D>::R, T = RowsTile<D>::T, LD = D + 4;
-  __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
-  __shared__ float sh_o[kWaves][16][LD];
-  __shared__ SchedLds sh_sched;
+__device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, const KvSched& d, RowsLds<D>& lds) {
+  constexpr int R = RowsTile<D>::R, T = RowsTile<D>::T;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 15, g = lane >> 4, kblk = q >> 2, B = 1 << c.lb;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
 
-  sched_run<16, WHOLE>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0,
+  sched_run<16, WHOLE>(c, a, d, lds.sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0,
                                               int s1, int slot) __attribute__((always_inline)) {
     const int r = min(t.r0 + q, t.r1), j = r / a.G;
     const Span mine = row_span(c, a, s, j);
@@ -270,26 +274,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAtt
 
     // join the waves
     if (g == 0) {
-      sh_m[wave][q] = M;
-      sh_l[wave][q] = L;
+      lds.m[wave][q] = M;
+      lds.l[wave][q] = L;
     }
 #pragma unroll
-    for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&sh_o[wave][q][16 * i + 4 * g]) = o[i];
+    for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&lds.o[wave][q][16 * i + 4 * g]) = o[i];
     __syncthreads();
     const int Hq = c.H * a.G;
     for (int i = tid; i < (t.r1 - t.r0 + 1) * (D / 4); i += 64 * kWaves) {
       const int row = i / (D / 4), ch = (i - row * (D / 4)) * 4;
-      float top = sh_m[0][row];
+      float top = lds.m[0][row];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][row]);
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds.m[w][row]);
       const float ref = top == -kInf ? 0.f : top;
       float l = 0.f;
       f32x4 v{0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sh_m[w][row] - ref);
-        l += sh_l[w][row] * f;
-        v += *reinterpret_cast<const f32x4*>(&sh_o[w][row][ch]) * f;
+        const float f = __builtin_amdgcn_exp2f(lds.m[w][row] - ref);
+        l += lds.l[w][row] * f;
+        v += *reinterpret_cast<const f32x4*>(&lds.o[w][row][ch]) * f;
       }
       if (slot >= 0) {
         float* dst = sched_slot(a.work, slot, 16, D);
@@ -323,7 +327,7 @@ __device__ __forceinline__ float sum_halves(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
-constexpr int kAhead = 4;  // reads of an operand from LDS ahead of its product
+constexpr int kAhead = 8;  // reads of an operand from LDS ahead of its product
 
 template <int D, int NT>
 struct ManyTile {
@@ -341,20 +345,25 @@ struct ManyTile {
 };
 
 template <int D, int NT>
-__global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
+struct TileLds {
+  typedef ManyTile<D, NT> X;
+  uint4 k[2][64 * X::U];
+  uint4 v[2][8 * X::DV];        // [16-token block][half][channel]: 8 tokens a unit
+  uint32_t mark[2][4 * X::DV];  // [block][channel]: a bit for each token whose value is NaN
+  uint32_t bad[2];              // a byte for each block without a page
+  int nan[2];                   // step with marks, plus 1
+  SchedLds sched;
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, const KvSched& d, TileLds<D, NT>& lds) {
   typedef ManyTile<D, NT> X;
   constexpr int T = X::T, NP = X::NP, QF = D / 16;
-  __shared__ uint4 sh_k[2][64 * X::U];
-  __shared__ uint4 sh_v[2][8 * X::DV];      // [16-token block][half][channel]: 8 tokens a unit
-  __shared__ uint32_t sh_mark[2][4 * X::DV];  // [block][channel]: a bit for each token whose value is NaN
-  __shared__ uint32_t sh_bad[2];            // a byte for each block without a page
-  __shared__ int sh_nan[2];                 // step with marks, plus 1
-  __shared__ SchedLds sh_sched;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
-  if (tid < 2) sh_nan[tid] = 0;
+  if (tid < 2) lds.nan[tid] = 0;
 
   // Piece i of this lane: bytes 16 (lane + 64 i) of the block's keys and of its
   // values (both 16 D bytes); its places in LDS.
@@ -365,7 +374,7 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
     koff[i] = X::k_unit(32 * (wave >> 1) + 8 * (x >> 2) + 4 * (wave & 1) + (x & 3), 2 * u);
   }
 
-  sched_run<X::R, false>(c, a, d, sh_sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0,
+  sched_run<X::R, false>(c, a, d, lds.sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0,
                                                 int s1, int slot) __attribute__((always_inline)) {
     const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
     const bool active = w0 <= t.r1;
@@ -432,7 +441,7 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
       for (int i = 0; i < NP; ++i)
         if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
     };
-    auto store = [&](int step, int buf) {
+    auto mark = [&](int step, int buf) {
       if (split(step)) {
         // A NaN among the values must reach the rows that see it, and no
         // other: it is taken out here, and its place marked for the rows.
@@ -441,50 +450,57 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
         for (int i = 0; i < NP; ++i)
           if (64 * i + 63 < D || lane + 64 * i < D) {
             uint32_t* w = reinterpret_cast<uint32_t*>(&vr[i]);
-            uint32_t mark = 0;
+            uint32_t at = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t n = nan_codes(w[k]);
               w[k] &= ~(n | (n - (n >> 7)));
-              mark |= ((n >> 7 & 1) | (n >> 14 & 2) | (n >> 21 & 4) | (n >> 28 & 8)) << (4 * k);
+              at |= ((n >> 7 & 1) | (n >> 14 & 2) | (n >> 21 & 4) | (n >> 28 & 8)) << (4 * k);
             }
-            sh_mark[buf][wave * X::DV + lane + 64 * i] = mark;
-            any |= mark;
+            lds.mark[buf][wave * X::DV + lane + 64 * i] = at;
+            any |= at;
           }
-        if (any) sh_nan[buf] = step + 1;
+        if (any) lds.nan[buf] = step + 1;
       }
-      if (lane == 0) reinterpret_cast<uint8_t*>(&sh_bad[buf])[wave] = bad;
-      const float vsc = vin ? vs : 1.f;
+      if (lane == 0) reinterpret_cast<uint8_t*>(&lds.bad[buf])[wave] = bad;
+    };
+    // half a piece from its codes into LDS: j / 4 is the piece, j % 4 which of
+    // the keys' and the values' halves
+    auto store = [&](int j, int buf) {
+      const int i = j / 4, half = j & 1;
+      if (64 * i + 63 < D || lane + 64 * i < D) {
+        const uint4 w = j & 2 ? vr[i] : kr[i];
+        const uint32_t x = half ? w.z : w.x, y = half ? w.w : w.y;
+        const float f = j & 2 ? (vin ? vs : 1.f) : ks;
+        const uint4 z{kv_bf2<false>(x, f), kv_bf2<true>(x, f), kv_bf2<false>(y, f), kv_bf2<true>(y, f)};
+        if (j & 2)
+          lds.v[buf][(2 * wave + half) * X::DV + lane + 64 * i] = z;
+        else
+          lds.k[buf][koff[i] ^ half] = z;
+      }
+    };
+    auto store_all = [&](int buf) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        if (64 * i + 63 < D || lane + 64 * i < D) {
-          const uint4 k = kr[i], v = vr[i];
-          sh_k[buf][koff[i]] =
-              uint4{kv_bf2<false>(k.x, ks), kv_bf2<true>(k.x, ks), kv_bf2<false>(k.y, ks), kv_bf2<true>(k.y, ks)};
-          sh_k[buf][koff[i] ^ 1] =
-              uint4{kv_bf2<false>(k.z, ks), kv_bf2<true>(k.z, ks), kv_bf2<false>(k.w, ks), kv_bf2<true>(k.w, ks)};
-          uint4* dst = &sh_v[buf][2 * wave * X::DV + lane + 64 * i];
-          dst[0] = uint4{kv_bf2<false>(v.x, vsc), kv_bf2<true>(v.x, vsc), kv_bf2<false>(v.y, vsc), kv_bf2<true>(v.y, vsc)};
-          dst[X::DV] =
-              uint4{kv_bf2<false>(v.z, vsc), kv_bf2<true>(v.z, vsc), kv_bf2<false>(v.w, vsc), kv_bf2<true>(v.w, vsc)};
-        }
+      for (int j = 0; j < 4 * NP; ++j) store(j, buf);
     };
 
     const int begin = t.step0 + s0, end = t.step0 + s1;
     ids(begin);
     load(begin);
     if (begin + 1 < end) ids(begin + 1);
-    store(begin, 0);
+    mark(begin, 0);
+    store_all(0);
     if (begin + 1 < end) load(begin + 1);
     if (begin + 2 < end) ids(begin + 2);
     __syncthreads();
     for (int step = begin; step < end; ++step) {
       const int buf = (step - begin) & 1, base = step * kKvStep;
-      if (step + 1 < end) store(step + 1, buf ^ 1);
-      if (step + 2 < end) load(step + 2);
-      if (step + 3 < end) ids(step + 3);
-      if (active && base < wb.hi && base + kKvStep > wa.lo) {
-        f32x16 st[2][NT];
+      const bool run = active && base < wb.hi && base + kKvStep > wa.lo;
+      f32x16 st[2][NT];
+      // The next step's codes go into the other buffer beside the products
+      // (after the last step the old ones do, which nobody reads).
+      if (step + 1 < end) mark(step + 1, buf ^ 1);
+      if (run) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -496,9 +512,9 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
         // read right before its product, which then waits for it).
         {
           uint4 kf[kAhead];
-          auto read = [&](int g) { kf[g % kAhead] = sh_k[buf][X::k_unit(32 * (g & 1) + q, 2 * (g >> 1) + hf)]; };
+          auto read = [&](int g) { kf[g % kAhead] = lds.k[buf][X::k_unit(32 * (g & 1) + q, 2 * (g >> 1) + hf)]; };
 #pragma unroll
-          for (int g = 0; g < kAhead; ++g) read(g);
+          for (int g = 0; g < kAhead && g < 2 * QF; ++g) read(g);
 #pragma unroll
           for (int g = 0; g < 2 * QF; ++g) {
             __builtin_amdgcn_sched_barrier(0);
@@ -507,10 +523,18 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
               st[g & 1][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g % kAhead]),
                                                                      qf[n][g >> 1], st[g & 1][n], 0, 0, 0);
             if (g + kAhead < 2 * QF) read(g + kAhead);
+#pragma unroll
+            for (int j = 4 * NP * g / (2 * QF); j < 4 * NP * (g + 1) / (2 * QF); ++j) store(j, buf ^ 1);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        const uint32_t bads = __builtin_amdgcn_readfirstlane(sh_bad[buf]);
+      } else {
+        store_all(buf ^ 1);
+      }
+      if (step + 2 < end) load(step + 2);
+      if (step + 3 < end) ids(step + 3);
+      if (run) {
+        const uint32_t bads = __builtin_amdgcn_readfirstlane(lds.bad[buf]);
         if (bads != 0 || base < wb.lo || base + kKvStep > wa.hi) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -526,7 +550,7 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
             }
           }
         }
-        if (split(step) && sh_nan[buf] == step + 1) {
+        if (split(step) && lds.nan[buf] == step + 1) {
           // the rows that see a marked value: a product of their view (ones)
           // with the marks (ones)
 #pragma unroll
@@ -540,7 +564,7 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const int ch = 32 * i + q;
-                const uint32_t mark = ch < D ? sh_mark[buf][(2 * x + hf) * X::DV + ch] : 0;
+                const uint32_t mark = ch < D ? lds.mark[buf][(2 * x + hf) * X::DV + ch] : 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                   uint32_t see[4], at[4];
@@ -600,10 +624,10 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
           uint4 vf[kAhead];
           auto read = [&](int g) {
             const int c = g / T, i = g % T;
-            vf[g % kAhead] = sh_v[buf][(2 * (2 * (c >> 1) + hf) + (c & 1)) * X::DV + 32 * i + q];
+            vf[g % kAhead] = lds.v[buf][(2 * (2 * (c >> 1) + hf) + (c & 1)) * X::DV + 32 * i + q];
           };
 #pragma unroll
-          for (int g = 0; g < kAhead; ++g) read(g);
+          for (int g = 0; g < kAhead && g < 4 * T; ++g) read(g);
 #pragma unroll
           for (int e = 0; e < 4; ++e) prob(0, e);
 #pragma unroll
@@ -660,6 +684,31 @@ __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel
   });
 }
 
+template <int D, bool WHOLE>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
+  __shared__ RowsLds<D> lds;
+  rows_part<D, WHOLE>(c, a, d, lds);
+}
+
+template <int D, int NT>
+__global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
+  __shared__ TileLds<D, NT> lds;
+  tile_part<D, NT>(c, a, d, lds);
+}
+
+template <int R, int D>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int workers) {
+  join_part<R, D>(c, a, workers, blockIdx.x);
+}
+template <int R, int D>
+__global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, int workers, KvAttn few_a,
+                                                           int few_workers) {
+  if ((int)blockIdx.x < workers)
+    join_part<R, D>(c, a, workers, blockIdx.x);
+  else
+    join_part<16, D>(c, few_a, few_workers, blockIdx.x - workers);
+}
+
 constexpr int kRowsWorkers = 512;   // few-row kernel: two workgroups a CU
 constexpr int kTileWorkers = 512;   // at most
 constexpr int kFewRows = 16;
@@ -670,31 +719,40 @@ int max_steps(const KvView& c, const KvAttn& a) {
   return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, (a.window + c.max_new) / kKvStep + 2) : cap);
 }
 
+size_t tile_bytes(int D) { return (sched_bytes(kTileWorkers, 128, D) + 255) / 256 * 256; }
+
 // Sequences of at most kFewRows rows (new tokens times query heads of a
-// key/value head) take the few-row kernel, the others the many-row one; each
+// key/value head) take the few-row form, the others the many-row one; each
 // is launched unless the batch cannot hold a sequence for it.
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   const int64_t rows = (int64_t)c.max_new * a.G;
   const bool many = rows > kFewRows, few = !many || c.n_rows < (int64_t)c.max_new * c.n_seq;
-  const int steps = max_steps(c, a);
-  if (few) {
-    const int64_t tiles = many ? 1 : (rows + 15) / 16, items = tiles * c.n_seq * c.H;
-    KvSched d{0, (int)tiles, 2, 1 << 30, 0, 8, 0, many ? kFewRows : INT32_MAX};
-    if (items > (1 << 20) || steps > 20) d.workers = kRowsWorkers;
-    if (d.workers) {
+  if (!many) {
+    const int64_t items = (int64_t)c.n_seq * c.H;
+    KvSched d{kRowsWorkers, 1, 2, 6, 0, 8, 0, INT32_MAX};
+    if (items > (1 << 20) || max_steps(c, a) > 20) {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(d.workers), dim3(64 * kWaves), 0, stream, c, a, d);
       MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
     } else {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)items), dim3(64 * kWaves), 0, stream, c, a, d);
     }
+    return launched();
   }
-  if (many) {
-    constexpr int NT = 1, R = ManyTile<D, NT>::R;
-    KvSched d{256 * ManyTile<D, NT>::PER_CU, 0, 3, 6, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
-    MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(d.workers), dim3(256), 0, stream, c, a, d);
-    MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(d.workers, 8), dim3(256), 0, stream, c, a, d.workers);
-  }
+  constexpr int NT = 1, R = ManyTile<D, NT>::R, workers = 256 * ManyTile<D, NT>::PER_CU;
+  const KvSched d{workers, 0, 3, 6, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
+  KvAttn few_a = a;
+  few_a.work = static_cast<char*>(a.work) + tile_bytes(D);
+  const KvSched few_d{kRowsWorkers, 0, 2, 6, 0, 8, 0, kFewRows};
+  if (few)
+    MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(kRowsWorkers), dim3(64 * kWaves), 0, stream, c, few_a,
+                 few_d);
+  MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(workers), dim3(256), 0, stream, c, a, d);
+  if (few)
+    MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(workers + kRowsWorkers, 8), dim3(256), 0, stream, c, a,
+                 workers, few_a, kRowsWorkers);
+  else
+    MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(workers, 8), dim3(256), 0, stream, c, a, workers);
   return launched();
 }
 
@@ -708,7 +766,7 @@ bool kv_attention_dim(int dim) {
 size_t kv_work_bytes(const KvView& c, int heads) {
   if (c.n_rows == 0) return 0;
   const size_t few = sched_bytes(kRowsWorkers, 16, c.D);
-  return (int64_t)c.max_new * (heads / c.H) > kFewRows ? std::max(few, sched_bytes(kTileWorkers, 128, c.D)) : few;
+  return (int64_t)c.max_new * (heads / c.H) > kFewRows ? tile_bytes(c.D) + few : few;
 }
 
 hipError_t launch_kv_attention(const KvView& c, const KvAttn& a, hipStream_t stream) {

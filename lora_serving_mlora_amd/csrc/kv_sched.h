@@ -12,7 +12,7 @@
 // alone, so results are the same from call to call.
 //
 // A cut item's pieces go to the caller's work buffer as (O, M, L) and are
-// joined by kv_join_kernel: worker w's slot 2w holds the piece that its part
+// joined by join_part: worker w's slot 2w holds the piece that its part
 // begins inside of, slot 2w + 1 the piece that its part ends inside of.
 #pragma once
 
@@ -328,16 +328,16 @@ __device__ __forceinline__ void write_row(const KvAttn& a, const KvSeq& s, int H
   *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(o[0] * inv, o[1] * inv), pack_bf2_hw(o[2] * inv, o[3] * inv)};
 }
 
-// Joins the pieces of the item that worker blockIdx.x began and did not end:
+// Joins the pieces of the item that worker w began and did not end:
 // o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) L_i, the pieces in their order.
 // Many pieces (a few rows over a long axis) are read side by side, as one after
 // the other they would cost a memory latency each; with few, the rows are.
 // blockIdx.y takes a share of the rows.
 template <int R, int D>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvView c, KvAttn a, int workers) {
+__device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int workers, int w) {
   constexpr int DL = D / 4, NG = 256 / DL;  // lanes of a row, pieces side by side
   __shared__ __align__(16) float sh[NG][D + 4];
-  const int w = blockIdx.x, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const int* meta = sched_meta(a.work, w);
   const int seq = meta[1], h = meta[2], tile = meta[3];
   if (seq < 0) return;
