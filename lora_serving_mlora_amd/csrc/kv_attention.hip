@@ -120,12 +120,18 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
     for (int i = 0; i < T; ++i) o[i] = f32x4{0, 0, 0, 0};
     float M = -kInf, L = 0.f;
 
-    // page ids of this lane's keys (16-token block q / 4 of a step) and values (block g)
+    // page ids of this lane's keys (16-token block q / 4 of a step) and values
+    // (block g), looked at when they are used: a look here would wait for them,
+    // and so for all loads before them
     int kid, vid;
+    const int* pages = c.table + (size_t)seq * c.table_stride;
     auto ids = [&](int step) {
-      const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
-      kid = kt < t.hi ? kv_page(c, seq, kt >> c.lb) : 0;
-      vid = vt < t.hi ? kv_page(c, seq, vt >> c.lb) : 0;
+      kid = pages[min((step * kKvStep + 16 * kblk) >> c.lb, c.width - 1)];
+      vid = pages[min((step * kKvStep + 16 * g) >> c.lb, c.width - 1)];
+    };
+    auto page_at = [&](int id, int tok) {  // -1 where there is none, any for what nobody sees
+      if (tok >= t.hi) return 0;
+      return (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks ? id : -1;
     };
     const uint8_t *kptr, *vptr;
     float ks, vs;
@@ -135,12 +141,13 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
     bool vin;
     auto place = [&](int step) {
       const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
-      const size_t kp = (size_t)max(kid, 0) * c.H + h, vp = (size_t)max(vid, 0) * c.H + h;
+      const int kpage = page_at(kid, kt), vpage = page_at(vid, vt);
+      const size_t kp = (size_t)max(kpage, 0) * c.H + h, vp = (size_t)max(vpage, 0) * c.H + h;
       kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
       vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
       ksp = c.k_scale + kp;
       vsp = c.v_scale + vp;
-      bad = vid < 0;
+      bad = vpage < 0;
       vin = !bad && vt < t.hi && vt + 16 > t.lo;
     };
     auto load_k = [&]() {
@@ -418,11 +425,10 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     // Page and scales of this wave's block, one for all its lanes, come by
     // vector loads all the same: a scalar load in flight would have every read
     // from LDS wait for it (they share a counter, and it returns in no order).
-    int id_next = 0;
+    int id_next;
+    const int* pages = c.table + (size_t)seq * c.table_stride;
     auto ids = [&](int step) {
-      const int tok = step * kKvStep + 16 * wave, p = tok >> c.lb;
-      id_next = tok < t.hi ? -1 : 0;
-      if (tok < t.hi && p < c.width) id_next = c.table[(size_t)seq * c.table_stride + p];
+      id_next = pages[min((step * kKvStep + 16 * wave) >> c.lb, c.width - 1)];
     };
     uint4 kr[NP], vr[NP];
     float ks, vs;
@@ -430,9 +436,10 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     auto load = [&](int step) {
       const int tok = step * kKvStep + 16 * wave;
       const int id = __builtin_amdgcn_readfirstlane(id_next);
-      bad = (unsigned)id >= (unsigned)c.n_blocks;
-      vin = !bad && tok < t.hi && tok + 16 > t.lo;
-      const size_t ph = (size_t)(bad ? 0 : id) * c.H + h;
+      const bool there = (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks, seen = tok < t.hi;
+      bad = seen && !there;
+      vin = seen && there && tok + 16 > t.lo;
+      const size_t ph = (size_t)(seen && there ? id : 0) * c.H + h;
       const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D;
       const uint4 *kp = reinterpret_cast<const uint4*>(c.k + at), *vp = reinterpret_cast<const uint4*>(c.v + at);
       ks = c.k_scale[ph];
