@@ -99,84 +99,99 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
 
-  sched_run<16, WHOLE>(c, a, d, lds.sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<16>& t, int s0,
-                                              int s1, int slot) __attribute__((always_inline)) {
-    const int r = min(t.r0 + q, t.r1), j = r / a.G;
-    const Span mine = row_span(c, a, s, j);
-    bf16x8 qf[R][2];
-    {
-      const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs;
+  typedef Piece<16> P;
+  bf16x8 qf[R][2];
+  auto load_q = [&](const P& p) {
+    const int r = min(p.t.r0 + q, p.t.r1), j = r / a.G;
+    const uint16_t* src = a.q + (size_t)(p.s.row0 + j) * a.rs + (size_t)(p.h * a.G + r % a.G) * a.hs;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int u = 4 * i + g;
+      uint4 x{}, y{};
+      if (16 * u < D) load16(src + 16 * u, vec, x, y);
+      qf[i][0] = __builtin_bit_cast(bf16x8, x);
+      qf[i][1] = __builtin_bit_cast(bf16x8, y);
+    }
+  };
+  // page ids of this lane's keys (16-token block q / 4 of a step) and values
+  // (block g), looked at when they are used: a look here would wait for them,
+  // and so for all loads before them
+  int kid = 0, vid = 0;
+  auto ids = [&](const P& p, int step, int& key, int& value) {
+    const int* pages = c.table + (size_t)p.seq * c.table_stride;
+    key = pages[min((step * kKvStep + 16 * kblk) >> c.lb, c.width - 1)];
+    value = pages[min((step * kKvStep + 16 * g) >> c.lb, c.width - 1)];
+  };
+  const uint8_t *kptr, *vptr;
+  float ks, vs;
+  uint4 kw[4][R], vw[T];
+  bool bad, vin;
+  const float *ksp, *vsp;
+  auto place = [&](const P& p, int step) {
+    const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
+    auto page_at = [&](int id, int tok) {  // -1 where there is none, any for what nobody sees
+      if (tok >= p.t.hi) return 0;
+      return (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks ? id : -1;
+    };
+    const int kpage = page_at(kid, kt), vpage = page_at(vid, vt);
+    const size_t kp = (size_t)max(kpage, 0) * c.H + p.h, vp = (size_t)max(vpage, 0) * c.H + p.h;
+    kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
+    vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
+    ksp = c.k_scale + kp;
+    vsp = c.v_scale + vp;
+    bad = vpage < 0;
+    vin = !bad && vt < p.t.hi && vt + 16 > p.t.lo;
+  };
+  auto load_k = [&]() {
+    ks = *ksp;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int u = 4 * i + g;
-        uint4 x{}, y{};
-        if (16 * u < D) load16(p + 16 * u, vec, x, y);
-        qf[i][0] = __builtin_bit_cast(bf16x8, x);
-        qf[i][1] = __builtin_bit_cast(bf16x8, y);
+        kw[x][i] = uint4{0, 0, 0, 0};
+        if (16 * (4 * i + 3) < D || 16 * (4 * i + g) < D)
+          kw[x][i] = *reinterpret_cast<const uint4*>(kptr + 4 * x * D + 16 * (4 * i + g));
       }
+  };
+  auto load_v = [&]() {
+    vs = *vsp;
+#pragma unroll
+    for (int i = 0; i < T; ++i) vw[i] = *reinterpret_cast<const uint4*>(vptr + 256 * i);
+  };
+  // the loads of a piece's first step, whose ids are here
+  auto start = [&](const P& p) {
+    const int step = p.t.step0 + p.s0 + wave, end = p.t.step0 + p.s1;
+    if (step < end) {
+      place(p, step);
+      load_k();
+      load_v();
+      ids(p, step + kWaves, kid, vid);
     }
+    load_q(p);
+  };
+
+  Pieces<16, WHOLE> pieces(c, a, d, lds.sched);
+  P p, next;
+  bool have = pieces.next(p);
+  if (have) {
+    ids(p, p.t.step0 + p.s0 + wave, kid, vid);
+    start(p);
+  }
+  while (have) {
+    const Tile<16>& t = p.t;
+    const KvSeq& s = p.s;
+    const int h = p.h, slot = p.slot;
+    const bool have_next = pieces.next(next);
+    int next_kid = 0, next_vid = 0;
+    if (have_next) ids(next, next.t.step0 + next.s0 + wave, next_kid, next_vid);
+    const Span mine = row_span(c, a, s, min(t.r0 + q, t.r1) / a.G);
     f32x4 o[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) o[i] = f32x4{0, 0, 0, 0};
     float M = -kInf, L = 0.f;
 
-    // page ids of this lane's keys (16-token block q / 4 of a step) and values
-    // (block g), looked at when they are used: a look here would wait for them,
-    // and so for all loads before them
-    int kid, vid;
-    const int* pages = c.table + (size_t)seq * c.table_stride;
-    auto ids = [&](int step) {
-      kid = pages[min((step * kKvStep + 16 * kblk) >> c.lb, c.width - 1)];
-      vid = pages[min((step * kKvStep + 16 * g) >> c.lb, c.width - 1)];
-    };
-    auto page_at = [&](int id, int tok) {  // -1 where there is none, any for what nobody sees
-      if (tok >= t.hi) return 0;
-      return (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks ? id : -1;
-    };
-    const uint8_t *kptr, *vptr;
-    float ks, vs;
-    uint4 kw[4][R], vw[T];
-    bool bad;
-    const float *ksp, *vsp;
-    bool vin;
-    auto place = [&](int step) {
-      const int kt = step * kKvStep + 16 * kblk, vt = step * kKvStep + 16 * g;
-      const int kpage = page_at(kid, kt), vpage = page_at(vid, vt);
-      const size_t kp = (size_t)max(kpage, 0) * c.H + h, vp = (size_t)max(vpage, 0) * c.H + h;
-      kptr = c.k + ((kp << c.lb) + (kt & (B - 1)) + (q & 3)) * D;
-      vptr = c.v + ((vp << c.lb) + (vt & (B - 1))) * D + q * 16;
-      ksp = c.k_scale + kp;
-      vsp = c.v_scale + vp;
-      bad = vpage < 0;
-      vin = !bad && vt < t.hi && vt + 16 > t.lo;
-    };
-    auto load_k = [&]() {
-      ks = *ksp;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          kw[x][i] = uint4{0, 0, 0, 0};
-          if (16 * (4 * i + 3) < D || 16 * (4 * i + g) < D)
-            kw[x][i] = *reinterpret_cast<const uint4*>(kptr + 4 * x * D + 16 * (4 * i + g));
-        }
-    };
-    auto load_v = [&]() {
-      vs = *vsp;
-#pragma unroll
-      for (int i = 0; i < T; ++i) vw[i] = *reinterpret_cast<const uint4*>(vptr + 256 * i);
-    };
-
-    int step = t.step0 + s0 + wave;
-    const int end = t.step0 + s1;
-    if (step < end) {
-      ids(step);
-      place(step);
-      load_k();
-      load_v();
-      if (step + kWaves < end) ids(step + kWaves);
-    }
-    for (; step < end; step += kWaves) {
+    const int end = t.step0 + p.s1;
+    for (int step = t.step0 + p.s0 + wave; step < end; step += kWaves) {
       const bool more = step + kWaves < end;
       const int base = step * kKvStep;
       const bool bad_now = bad, vin_now = vin;
@@ -191,9 +206,9 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
         }
       }
       if (more) {
-        place(step + kWaves);
+        place(p, step + kWaves);
         load_k();
-        if (step + 2 * kWaves < end) ids(step + 2 * kWaves);
+        ids(p, step + 2 * kWaves, kid, vid);
       }
       const int mt = base + 16 * g;  // first of this lane's 16 tokens
       if (__ballot(bad_now)) {
@@ -286,6 +301,11 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
     }
 #pragma unroll
     for (int i = 0; i < T; ++i) *reinterpret_cast<f32x4*>(&lds.o[wave][q][16 * i + 4 * g]) = o[i];
+    // the next piece's first loads are under way while this one is written
+    if (have_next) {
+      kid = next_kid, vid = next_vid;
+      start(next);
+    }
     __syncthreads();
     const int Hq = c.H * a.G;
     for (int i = tid; i < (t.r1 - t.r0 + 1) * (D / 4); i += 64 * kWaves) {
@@ -311,7 +331,10 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
       }
     }
     __syncthreads();
-  });
+    p = next;
+    have = have_next;
+  }
+  pieces.finish();
 }
 
 // ----------------------------------------------------------------------------
@@ -381,29 +404,71 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     koff[i] = X::k_unit(32 * (wave >> 1) + 8 * (x >> 2) + 4 * (wave & 1) + (x & 3), 2 * u);
   }
 
-  sched_run<X::R, false>(c, a, d, lds.sched, [&](int seq, const KvSeq& s, int h, int tile, const Tile<X::R>& t, int s0,
-                                                int s1, int slot) __attribute__((always_inline)) {
-    const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
-    const bool active = w0 <= t.r1;
-    Span mine[NT];
-    bf16x8 qf[NT][QF];
+  typedef Piece<X::R> P;
+  bf16x8 qf[NT][QF];
+  auto load_q = [&](const P& p) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = min(w0 + 32 * n + q, t.r1), j = r / a.G;
-      mine[n] = row_span(c, a, s, j);
-      const uint16_t* p = a.q + (size_t)(s.row0 + j) * a.rs + (size_t)(h * a.G + r % a.G) * a.hs + 8 * hf;
+      const int r = min(p.t.r0 + wave * 32 * NT + 32 * n + q, p.t.r1), j = r / a.G;
+      const uint16_t* src = a.q + (size_t)(p.s.row0 + j) * a.rs + (size_t)(p.h * a.G + r % a.G) * a.hs + 8 * hf;
 #pragma unroll
       for (int i = 0; i < QF; ++i) {
         uint4 x{};
         if (vec) {
-          x = *reinterpret_cast<const uint4*>(p + 16 * i);
+          x = *reinterpret_cast<const uint4*>(src + 16 * i);
         } else {
-          auto two = [&](int e) { return p[16 * i + e] | (uint32_t)p[16 * i + e + 1] << 16; };
+          auto two = [&](int e) { return src[16 * i + e] | (uint32_t)src[16 * i + e + 1] << 16; };
           x = uint4{two(0), two(2), two(4), two(6)};
         }
         qf[n][i] = __builtin_bit_cast(bf16x8, x);
       }
     }
+  };
+  // Page and scales of this wave's block, one for all its lanes, come by
+  // vector loads all the same: a scalar load in flight would have every read
+  // from LDS wait for it (they share a counter, and it returns in no order).
+  int id_next = 0;
+  auto ids = [&](const P& p, int step, int& id) {
+    id = c.table[(size_t)p.seq * c.table_stride + min((step * kKvStep + 16 * wave) >> c.lb, c.width - 1)];
+  };
+  uint4 kr[NP], vr[NP];
+  float ks, vs;
+  bool bad, vin;
+  auto load = [&](const P& p, int step) {
+    const int tok = step * kKvStep + 16 * wave;
+    const int id = __builtin_amdgcn_readfirstlane(id_next);
+    const bool there = (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks, seen = tok < p.t.hi;
+    bad = seen && !there;
+    vin = seen && there && tok + 16 > p.t.lo;
+    const size_t ph = (size_t)(seen && there ? id : 0) * c.H + p.h;
+    const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D;
+    const uint4 *kp = reinterpret_cast<const uint4*>(c.k + at), *vp = reinterpret_cast<const uint4*>(c.v + at);
+    ks = c.k_scale[ph];
+    vs = c.v_scale[ph];
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
+  };
+  Pieces<X::R, false> pieces(c, a, d, lds.sched);
+  P p, next;
+  bool have = pieces.next(p);
+  if (have) {
+    ids(p, p.t.step0 + p.s0, id_next);
+    load(p, p.t.step0 + p.s0);
+    load_q(p);
+  }
+  while (have) {
+    const Tile<X::R>& t = p.t;
+    const KvSeq& s = p.s;
+    const int h = p.h, slot = p.slot;
+    const bool have_next = pieces.next(next);
+    int next_id = 0;
+    if (have_next) ids(next, next.t.step0 + next.s0, next_id);
+    const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
+    const bool active = w0 <= t.r1;
+    Span mine[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mine[n] = row_span(c, a, s, min(w0 + 32 * n + q, t.r1) / a.G);
     // what all and what some of the wave's rows see
     const Span wa = row_span(c, a, s, min(w0, t.r1) / a.G), wb = row_span(c, a, s, min(w0 + 32 * NT - 1, t.r1) / a.G);
 
@@ -421,32 +486,6 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
 
     auto split = [&](int step) {  // rows differ in what they see of it
       return step * kKvStep < t.every_lo || (step + 1) * kKvStep > t.every_hi;
-    };
-    // Page and scales of this wave's block, one for all its lanes, come by
-    // vector loads all the same: a scalar load in flight would have every read
-    // from LDS wait for it (they share a counter, and it returns in no order).
-    int id_next;
-    const int* pages = c.table + (size_t)seq * c.table_stride;
-    auto ids = [&](int step) {
-      id_next = pages[min((step * kKvStep + 16 * wave) >> c.lb, c.width - 1)];
-    };
-    uint4 kr[NP], vr[NP];
-    float ks, vs;
-    bool bad, vin;
-    auto load = [&](int step) {
-      const int tok = step * kKvStep + 16 * wave;
-      const int id = __builtin_amdgcn_readfirstlane(id_next);
-      const bool there = (tok >> c.lb) < c.width && (unsigned)id < (unsigned)c.n_blocks, seen = tok < t.hi;
-      bad = seen && !there;
-      vin = seen && there && tok + 16 > t.lo;
-      const size_t ph = (size_t)(seen && there ? id : 0) * c.H + h;
-      const size_t at = ((ph << c.lb) + (tok & (B - 1))) * D;
-      const uint4 *kp = reinterpret_cast<const uint4*>(c.k + at), *vp = reinterpret_cast<const uint4*>(c.v + at);
-      ks = c.k_scale[ph];
-      vs = c.v_scale[ph];
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-        if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
     };
     auto mark = [&](int step, int buf) {
       if (split(step)) {
@@ -491,14 +530,14 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
       for (int j = 0; j < 4 * NP; ++j) store(j, buf);
     };
 
-    const int begin = t.step0 + s0, end = t.step0 + s1;
-    ids(begin);
-    load(begin);
-    if (begin + 1 < end) ids(begin + 1);
+    // a step's loads are issued one step before it goes into LDS, its page id
+    // one before that
+    const int begin = t.step0 + p.s0, end = t.step0 + p.s1;
+    ids(p, begin + 1, id_next);
     mark(begin, 0);
     store_all(0);
-    if (begin + 1 < end) load(begin + 1);
-    if (begin + 2 < end) ids(begin + 2);
+    if (begin + 1 < end) load(p, begin + 1);
+    ids(p, begin + 2, id_next);
     __syncthreads();
     for (int step = begin; step < end; ++step) {
       const int buf = (step - begin) & 1, base = step * kKvStep;
@@ -538,8 +577,8 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
       } else {
         store_all(buf ^ 1);
       }
-      if (step + 2 < end) load(step + 2);
-      if (step + 3 < end) ids(step + 3);
+      if (step + 2 < end) load(p, step + 2);
+      ids(p, step + 3, id_next);
       if (run) {
         const uint32_t bads = __builtin_amdgcn_readfirstlane(lds.bad[buf]);
         if (bads != 0 || base < wb.lo || base + kKvStep > wa.hi) {
@@ -659,6 +698,12 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
       __syncthreads();
     }
 
+    // the next piece's first loads are under way while this one is written
+    if (have_next) {
+      id_next = next_id;
+      load(next, next.t.step0 + next.s0);
+      load_q(next);
+    }
     const int Hq = c.H * a.G;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -688,7 +733,10 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
           }
       }
     }
-  });
+    p = next;
+    have = have_next;
+  }
+  pieces.finish();
 }
 
 template <int D, bool WHOLE>

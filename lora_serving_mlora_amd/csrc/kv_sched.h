@@ -56,6 +56,7 @@ struct Tile {
   int every_lo, every_hi;  // tokens seen by every row
   int step0, steps;    // at least one step
 
+  Tile() = default;
   __device__ __forceinline__ Tile(const KvView& c, const KvAttn& a, const KvSeq& s, int tile) {
     r0 = tile * R;
     r1 = min(r0 + R, s.m * a.G) - 1;
@@ -241,82 +242,121 @@ __device__ __forceinline__ float* sched_slot(void* work, int slot, int R, int D)
          (size_t)slot * sched_slot_floats(R, D);
 }
 
-// Runs body(seq, s, h, tile, t, s0, s1, slot) for every piece of worker w:
-// steps s0 <= i < s1 of the tile's, slot < 0 where the piece is the whole item.
+// steps s0 <= i < s1 of a tile's, slot < 0 where that is the whole item
+template <int R>
+struct Piece {
+  KvSeq s;
+  Tile<R> t;
+  int seq, h, tile, s0, s1, slot;
+};
+
+// The pieces of this workgroup's part, in their order; the same in every lane.
 // WHOLE: no parts, workgroup i takes item i.
-template <int R, bool WHOLE, class Body>
-__device__ __forceinline__ void sched_run(const KvView& c, const KvAttn& a, const KvSched& d, SchedLds& L,
-                                          Body&& body) {
-  if constexpr (WHOLE) {
-    int item = blockIdx.x;
-    const int h = item % c.H;
-    item /= c.H;
-    const int tile = item % d.tiles, seq = item / d.tiles;
-    const KvSeq s = kv_seq(c, seq);
-    if (!sched_takes(d, s.m * a.G) || tile * R >= s.m * a.G) return;
-    const Tile<R> t(c, a, s, tile);
-    body(seq, s, h, tile, t, 0, t.steps, -1);
-    return;
-  } else {
-  // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
-  // turn), whose L2 then serves the tiles that share keys and values
-  const int w = (d.workers & 7) == 0 ? (blockIdx.x & 7) * (d.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-  sched_part<R>(c, a, d, w, L);
-  const SchedPos b = L.pos[0];
-  const int64_t length = L.pos[1].p - b.p;
-  // the same in every lane: scalars
-  int left = __builtin_amdgcn_readfirstlane((int)min<int64_t>(length, INT32_MAX));
-  int first = 0, tail[3] = {-1, 0, 0};
-  int seq = __builtin_amdgcn_readfirstlane(b.seq), h = __builtin_amdgcn_readfirstlane(b.h);
-  int k = __builtin_amdgcn_readfirstlane(b.k), off = __builtin_amdgcn_readfirstlane(b.off);
-  while (left > 0) {
-    const KvSeq s = kv_seq(c, seq);
-    const int rows = s.m * a.G, tiles = (rows + R - 1) / R;
-    if (!sched_takes(d, rows) || h >= c.H) {
-      // on to the next sequence that has tiles, 64 looked at together
-      h = k = off = 0;
-      uint64_t has = 0;
-      for (++seq; seq < c.n_seq; seq += 64) {
-        const int i = seq + (int)(threadIdx.x & 63);
-        has = __ballot(i < c.n_seq && sched_takes(d, kv_seq(c, min(i, c.n_seq - 1)).m * a.G));
-        if (has) break;
+template <int R, bool WHOLE>
+struct Pieces {
+  const KvView& c;
+  const KvAttn& a;
+  const KvSched& d;
+  int w, left, first, tail[3], seq, h, k, off;
+  KvSeq s;
+
+  __device__ __forceinline__ Pieces(const KvView& c_, const KvAttn& a_, const KvSched& d_, SchedLds& L)
+      : c(c_), a(a_), d(d_), w(blockIdx.x), left(1), first(0), tail{-1, 0, 0}, h(0), k(0), off(0) {
+    if constexpr (!WHOLE) {
+      // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
+      // turn), whose L2 then serves the tiles that share keys and values
+      if ((d.workers & 7) == 0) w = (blockIdx.x & 7) * (d.workers >> 3) + (blockIdx.x >> 3);
+      sched_part<R>(c, a, d, w, L);
+      const SchedPos b = L.pos[0];
+      const int64_t length = L.pos[1].p - b.p;
+      left = __builtin_amdgcn_readfirstlane((int)min<int64_t>(length, INT32_MAX));
+      seq = __builtin_amdgcn_readfirstlane(b.seq), h = __builtin_amdgcn_readfirstlane(b.h);
+      k = __builtin_amdgcn_readfirstlane(b.k), off = __builtin_amdgcn_readfirstlane(b.off);
+      if (left > 0) load();
+    }
+  }
+  __device__ __forceinline__ void load() {
+    const KvSeq x = kv_seq(c, seq);
+    s.row0 = __builtin_amdgcn_readfirstlane(x.row0);
+    s.m = __builtin_amdgcn_readfirstlane(x.m);
+    s.n = __builtin_amdgcn_readfirstlane(x.n);
+  }
+
+  __device__ __forceinline__ bool next(Piece<R>& p) {
+    if constexpr (WHOLE) {
+      if (left == 0) return false;
+      left = 0;
+      int item = blockIdx.x;
+      h = item % c.H;
+      item /= c.H;
+      k = item % d.tiles, seq = item / d.tiles;
+      load();
+      if (!sched_takes(d, s.m * a.G) || k * R >= s.m * a.G) return false;
+      p.t = Tile<R>(c, a, s, k);
+      p.s = s, p.seq = seq, p.h = h, p.tile = k, p.s0 = 0, p.s1 = p.t.steps, p.slot = -1;
+      return true;
+    } else {
+      while (left > 0) {
+        const int rows = s.m * a.G, tiles = (rows + R - 1) / R;
+        if (!sched_takes(d, rows) || h >= c.H) {
+          // on to the next sequence that has tiles, 64 looked at together
+          h = k = off = 0;
+          uint64_t has = 0;
+          for (++seq; seq < c.n_seq; seq += 64) {
+            const int i = seq + (int)(threadIdx.x & 63);
+            has = __ballot(i < c.n_seq && sched_takes(d, kv_seq(c, min(i, c.n_seq - 1)).m * a.G));
+            if (has) break;
+          }
+          if (!has) {
+            left = 0;
+            break;
+          }
+          seq += __builtin_ctzll(has);
+          load();
+          continue;
+        }
+        if (k >= tiles) {
+          k = off = 0;
+          ++h;
+          continue;
+        }
+        p.tile = sched_tile(d, k, tiles);
+        p.t = Tile<R>(c, a, s, p.tile);
+        const int len = p.t.steps + d.over;
+        if (off >= len) {
+          ++k;
+          off = 0;
+          continue;
+        }
+        const int take = min(left, len - off);
+        const bool head = off == 0, end = off + take == len;
+        if (!head) first = end ? 1 : 2;
+        if (head && !end) tail[0] = seq, tail[1] = h, tail[2] = p.tile;
+        p.s = s, p.seq = seq, p.h = h;
+        p.s0 = max(0, off - d.over), p.s1 = max(0, off + take - d.over);
+        p.slot = head && end ? -1 : 2 * w + (head ? 1 : 0);
+        left -= take;
+        off = 0;
+        ++k;
+        return true;
       }
-      if (!has) break;
-      seq += __builtin_ctzll(has);
-      continue;
+      return false;
     }
-    if (k >= tiles) {
-      k = off = 0;
-      ++h;
-      continue;
+  }
+
+  // after the last piece: what the join has to know
+  __device__ __forceinline__ void finish() {
+    if constexpr (!WHOLE) {
+      if (threadIdx.x == 0) {
+        int* m = sched_meta(a.work, w);
+        m[0] = first;
+        m[1] = tail[0];
+        m[2] = tail[1];
+        m[3] = tail[2];
+      }
     }
-    const int tile = sched_tile(d, k, tiles);
-    const Tile<R> t(c, a, s, tile);
-    const int len = t.steps + d.over;
-    if (off >= len) {
-      ++k;
-      off = 0;
-      continue;
-    }
-    const int take = min(left, len - off);
-    const int s0 = max(0, off - d.over), s1 = max(0, off + take - d.over);
-    const bool head = off == 0, end = off + take == len;
-    if (!head) first = end ? 1 : 2;
-    if (head && !end) tail[0] = seq, tail[1] = h, tail[2] = tile;
-    body(seq, s, h, tile, t, s0, s1, head && end ? -1 : 2 * w + (head ? 1 : 0));
-    left -= take;
-    off = 0;
-    ++k;
   }
-  if (threadIdx.x == 0) {
-    int* m = sched_meta(a.work, w);
-    m[0] = first;
-    m[1] = tail[0];
-    m[2] = tail[1];
-    m[3] = tail[2];
-  }
-  }
-}
+};
 
 // four channels of row rr of a (sequence, head): o / l, zero where it saw nothing
 typedef float f32x4 __attribute__((ext_vector_type(4)));
