@@ -766,6 +766,7 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
 
 constexpr int kRowsWorkers = 512;   // few-row kernel: two workgroups a CU
 constexpr int kTileWorkers = 512;   // at most
+constexpr int kSkew = 24;
 constexpr int kFewRows = 16;
 
 // Steps of an item at most, as far as the host can tell.
@@ -785,20 +786,22 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   const bool many = rows > kFewRows, few = !many || c.n_rows < (int64_t)c.max_new * c.n_seq;
   if (!many) {
     const int64_t items = (int64_t)c.n_seq * c.H;
-    KvSched d{kRowsWorkers, 1, 2, 6, 0, 8, 0, INT32_MAX};
+    KvSched d{9, kSkew, 1, 2, 6, 0, 8, 0, INT32_MAX};
     if (items > (1 << 20) || max_steps(c, a) > 20) {
-      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(d.workers), dim3(64 * kWaves), 0, stream, c, a, d);
-      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(d.workers, 4), dim3(256), 0, stream, c, a, d.workers);
+      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(kRowsWorkers), dim3(64 * kWaves), 0, stream, c, a, d);
+      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(kRowsWorkers, 4), dim3(256), 0, stream, c, a,
+                   kRowsWorkers);
     } else {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)items), dim3(64 * kWaves), 0, stream, c, a, d);
     }
     return launched();
   }
   constexpr int NT = 1, R = ManyTile<D, NT>::R, workers = 256 * ManyTile<D, NT>::PER_CU;
-  const KvSched d{workers, 0, 3, 6, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
+  const KvSched d{workers == 512 ? 9 : 8, workers == 512 ? kSkew : 0, 0, 3, 6, a.causal, 4, few ? kFewRows : 0,
+                  INT32_MAX};
   KvAttn few_a = a;
   few_a.work = static_cast<char*>(a.work) + tile_bytes(D);
-  const KvSched few_d{kRowsWorkers, 0, 2, 6, 0, 8, 0, kFewRows};
+  const KvSched few_d{9, kSkew, 0, 2, 6, 0, 8, 0, kFewRows};
   if (few)
     MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(kRowsWorkers), dim3(64 * kWaves), 0, stream, c, few_a,
                  few_d);

@@ -4,7 +4,7 @@
 // An item is a tile of R rows of one (sequence, key/value head); it walks its
 // visible tokens in steps of 64.  Items lie on a line in the order (sequence,
 // head, tile), each as long as its steps plus `over` for what an item costs
-// besides; workgroup w takes the w-th of `workers` equal parts of the line, so
+// besides; workgroup w takes the w-th of 2^lw (nearly) equal parts of the line, so
 // one long sequence is cut into many pieces and many short ones are packed
 // together, and no length is ever read by the host.  A cut that falls close to
 // an item's end is moved there (by both neighbours alike), which keeps pieces
@@ -23,7 +23,8 @@ namespace mlora {
 constexpr int kKvStep = 64;  // tokens of a step
 
 struct KvSched {
-  int workers;             // parts
+  int lw;                  // log2 of the workgroups: parts of the line
+  int skew;                // 256ths that the parts of the second half take less, see sched_place
   int tiles;               // where workgroup i takes item i whole: tiles of a (sequence, head) at most
   int over, tol_max, mirror, min_share;
   int min_rows, max_rows;  // sequences with other numbers of rows are left out
@@ -118,6 +119,15 @@ __device__ __forceinline__ T wave_scan(T x) {  // inclusive
   return x;
 }
 
+// Where worker w's part begins.  The workgroups of an XCD take neighbouring
+// parts; those launched later share their CU with one launched earlier, whose
+// waves are served first where both could issue, so each of them takes `skew`
+// less and the earlier ones that much more, for both to end together.
+__device__ __forceinline__ int64_t sched_place(const KvSched& d, int64_t share, int w) {
+  const int per = (1 << d.lw) >> 3, l = w % per, more = l < per / 2 ? l : per - l;
+  return share * w + (share * more * d.skew >> 8);
+}
+
 // The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p).
 // Everything that depends on the number of tiles is done by all 256 threads
 // side by side: one thread that went through the tiles of a long prompt alone
@@ -169,14 +179,14 @@ __device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, con
     if (v < wave) incl += L.sum[v];
     total += L.sum[v];
   }
-  const int64_t share = max<int64_t>((total + d.workers - 1) / d.workers, d.min_share);
+  const int64_t share = max<int64_t>((total + (1 << d.lw) - 1) >> d.lw, d.min_share);
   const int64_t tol = min<int64_t>(max<int64_t>(share / 8, d.over), d.tol_max);
   if (tid < 2) L.pos[tid] = {total, -1, 0, 0, 0};  // for ends past the line
   __syncthreads();
   // the sequence and head that hold each place (one thread at most holds it)
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
-    const int64_t p = share * (w + b);
+    const int64_t p = sched_place(d, share, w + b);
     if (p < incl - own || p >= incl) continue;
     int64_t at = incl - own;
     for (int i = i0; i < i1; ++i) {
@@ -185,7 +195,8 @@ __device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, con
         at += head * c.H;
         continue;
       }
-      const int h = (int)((p - at) / head);
+      // (a division in 64 bits takes half a microsecond)
+      const int h = p - at <= INT32_MAX ? (int)((uint32_t)(p - at) / (uint32_t)head) : (int)((p - at) / head);
       L.pos[b] = {p, i, h, 0, 0};
       L.at[b] = at + h * head;
       break;
@@ -265,7 +276,7 @@ struct Pieces {
     if constexpr (!WHOLE) {
       // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
       // turn), whose L2 then serves the tiles that share keys and values
-      if ((d.workers & 7) == 0) w = (blockIdx.x & 7) * (d.workers >> 3) + (blockIdx.x >> 3);
+      w = ((blockIdx.x & 7) << (d.lw - 3)) + (blockIdx.x >> 3);
       sched_part<R>(c, a, d, w, L);
       const SchedPos b = L.pos[0];
       const int64_t length = L.pos[1].p - b.p;
@@ -373,6 +384,7 @@ __device__ __forceinline__ void write_row(const KvAttn& a, const KvSeq& s, int H
 // Many pieces (a few rows over a long axis) are read side by side, as one after
 // the other they would cost a memory latency each; with few, the rows are.
 // blockIdx.y takes a share of the rows.
+constexpr int kJoinFew = 8;
 template <int R, int D>
 __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int workers, int w) {
   constexpr int DL = D / 4, NG = 256 / DL;  // lanes of a row, pieces side by side
@@ -395,13 +407,13 @@ __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int 
   const KvSeq s = kv_seq(c, seq);
   const int r0 = tile * R, cnt = min(R, s.m * a.G - r0), Hq = c.H * a.G;
   const int d = 4 * (tid % DL), grp = tid / DL;
-  if (n <= 4) {
+  if (n <= kJoinFew) {
     for (int x = blockIdx.y * 256 + tid; x < cnt * DL; x += gridDim.y * 256) {
       const int r = x / DL, ch = 4 * (x % DL);
-      float m[4], l[4], top = -__builtin_huge_valf();
-      f32x4 v[4];
+      float m[kJoinFew], l[kJoinFew], top = -__builtin_huge_valf();
+      f32x4 v[kJoinFew];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kJoinFew; ++i) {
         m[i] = -__builtin_huge_valf();
         l[i] = 0.f;
         v[i] = f32x4{0, 0, 0, 0};
@@ -416,7 +428,7 @@ __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int 
       float L = 0.f;
       f32x4 o{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kJoinFew; ++i) {
         const float f = __builtin_amdgcn_exp2f(m[i] - ref);
         L += l[i] * f;
         o += v[i] * f;
