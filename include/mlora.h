@@ -498,9 +498,10 @@ mlora_status mlora_kv_read(const mlora_kv_cache* cache, int32_t layer, const mlo
  * x sees tokens 0 .. x when `causal` is set (with window > 0 only the last
  * `window` of them, x among them), every token of its sequence otherwise.
  * What a row does not see never reaches it, not as NaN either; a row that
- * sees nothing is zero.
+ * sees nothing is zero, one whose scores are all -infinity NaN.
  *   q:    device bf16, strides in elements as for mlora_kv_append;
- *   heads: query heads, a multiple of kv_heads, at most 1024 of them;
+ *   heads: query heads, a multiple of kv_heads, at most 1024 of them
+ *         (n_rows * heads / kv_heads at most 2^28);
  *   out:  device bf16 [n_rows][heads][dim], 16-byte aligned;
  *   work: device scratch of mlora_kv_work_bytes() bytes, 256-byte aligned,
  *         contents free (calls that share it must not overlap).

@@ -1252,6 +1252,9 @@ mlora_status mlora_kv_attention(const mlora_kv_cache* c, int32_t layer, const ui
     return fail(MLORA_EINVAL, "attention: dim %d is not 32, 64, 80, 96, 112, 128, 160, 192 or 256", c->dim);
   if (heads < c->kv_heads || heads > 1024 || heads % c->kv_heads != 0)
     return fail(MLORA_EINVAL, "attention: %d query heads are not a multiple of %d up to 1024", heads, c->kv_heads);
+  if ((int64_t)b->n_rows * (heads / c->kv_heads) > 1 << 28)
+    return fail(MLORA_EINVAL, "attention: %d rows of %d query heads a key/value head (together at most 2^28)", b->n_rows,
+                heads / c->kv_heads);
   if (window < 0 || (window > 0 && !causal))
     return fail(MLORA_EINVAL, "attention: window %d%s", window, window > 0 ? " without causal" : "");
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MLORA_EINVAL, "attention: scale must be finite and above 0");

@@ -327,7 +327,7 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
         *reinterpret_cast<f32x4*>(dst + row * D + ch) = v;
         if (ch == 0) dst[16 * D + row] = top, dst[16 * D + 16 + row] = l;
       } else {
-        write_row<D>(a, s, Hq, h, t.r0 + row, ch, v, l);
+        write_row<D>(a, s, Hq, h, t.r0 + row, ch, v, l, row_sees(c, a, s, t.r0 + row));
       }
     }
     __syncthreads();
@@ -729,7 +729,8 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
           for (int e = 0; e < 16; e += 4) {
             const int ch = 32 * i + 2 * e + 4 * hf;
             if (ch < D)
-              write_row<D>(a, s, Hq, h, rr, ch, f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]}, l);
+              write_row<D>(a, s, Hq, h, rr, ch, f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]}, l,
+                           mine[n].hi > mine[n].lo);
           }
       }
     }

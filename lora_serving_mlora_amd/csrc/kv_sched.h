@@ -369,12 +369,17 @@ struct Pieces {
   }
 };
 
-// four channels of row rr of a (sequence, head): o / l, zero where it saw nothing
+// four channels of row rr of a (sequence, head): o / l, zero where the row
+// sees nothing (l may also be 0 because every score is -infinity: NaN)
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bool row_sees(const KvView& c, const KvAttn& a, const KvSeq& s, int rr) {
+  const Span x = row_span(c, a, s, rr / a.G);
+  return x.hi > x.lo;
+}
 template <int D>
 __device__ __forceinline__ void write_row(const KvAttn& a, const KvSeq& s, int Hq, int h, int rr, int ch, f32x4 o,
-                                          float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+                                          float l, bool sees) {
+  const float inv = sees ? 1.f / l : 0.f;
   uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + ch;
   *reinterpret_cast<uint2*>(dst) = uint2{pack_bf2_hw(o[0] * inv, o[1] * inv), pack_bf2_hw(o[2] * inv, o[3] * inv)};
 }
@@ -433,7 +438,7 @@ __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int 
         L += l[i] * f;
         o += v[i] * f;
       }
-      write_row<D>(a, s, Hq, h, r0 + r, ch, o, L);
+      write_row<D>(a, s, Hq, h, r0 + r, ch, o, L, row_sees(c, a, s, r0 + r));
     }
     return;
   }
@@ -468,7 +473,7 @@ __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int 
         l += sh[i][D + 1] * f;
         v += *reinterpret_cast<const f32x4*>(&sh[i][d]) * f;
       }
-      write_row<D>(a, s, Hq, h, r0 + r, d, v, l);
+      write_row<D>(a, s, Hq, h, r0 + r, d, v, l, row_sees(c, a, s, r0 + r));
     }
   }
 }

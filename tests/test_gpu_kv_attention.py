@@ -203,6 +203,44 @@ def test_queries_that_are_not_finite():
     _check(got, ref, bound, "NaN queries")
 
 
+@pytest.mark.parametrize("new,total", [([1, 1], [1, 700]), ([40], [40])])
+def test_rows_whose_every_score_is_minus_infinity(new, total):
+    """They see tokens, so they are NaN (0 / 0), not the zero of a row that
+    sees none; rows of other queries are as ever."""
+    c = Case(80, new, total, 1, 64, 16)
+    x = np.abs(c.row(c.n_rows))
+    K.append(c.cache, x, x, c.batch)
+    lut = K.code_values()
+    c.cache["k"] = np.where(np.isnan(lut[c.cache["k"]]), c.cache["k"], c.cache["k"] & 0x7f).astype(np.uint8)
+    torch = torch_cuda()
+    c.cache["k"][c.cache["k"] == 0] = 1  # no zero among the keys (0 times infinity)
+    for n in ("k", "v", "k_scale", "v_scale"):
+        getattr(c.dev, n)[c.layer].copy_(torch.from_numpy(c.cache[n]))
+    q = _queries(c, 4)
+    ref, bound = K.attention(c.cache, q, c.batch)
+    q[0, 1], q[-1, 3] = -np.inf, -np.inf
+    ref[0, 1], ref[-1, 3] = np.nan, np.nan
+    say(f"kv attention scores of minus infinity {new}")
+    got = c.M.kv_attention(c.dev, 0, dev_rows(q), c.dev_batch())
+    _check(got, ref, bound, "minus infinity")
+
+
+@pytest.mark.parametrize("order", ["prompts first", "prompts last", "between"])
+def test_few_and_many_rows_in_one_batch(order):
+    """Sequences of both kinds, among them idle ones, in more sequences than a
+    workgroup deals with side by side as well."""
+    rng = np.random.default_rng(5)
+    for n_single in (20, 300):
+        prompts = [(33, 200), (70, 70), (5, 900)]
+        singles = [(1, int(x)) if x % 7 else (0, 0) for x in rng.integers(1, 120, size=n_single)]
+        half = n_single // 2
+        seqs = {"prompts first": prompts + singles, "prompts last": singles + prompts,
+                "between": prompts[:1] + singles[:half] + prompts[1:2] + singles[half:] + prompts[2:]}[order]
+        c = Case(81, [m for m, _ in seqs], [n for _, n in seqs], 1, 64, 16)
+        _fill_new_plain(c)
+        _run(c, _queries(c, 4), f"{order}, {n_single} singles")
+
+
 def test_large_scores():
     """Scores in the thousands, rising and falling along the sequence, and
     pages whose scales lie 2^30 apart."""

@@ -112,6 +112,45 @@ def test_pages_that_do_not_exist_and_negative_positions():
     _read_equal(d)
 
 
+def test_lengths_at_the_ends_of_their_type():
+    """Nothing is written for them, and their rows are NaN."""
+    torch = torch_cuda()
+    c = Case(14, [2, 1, 1], [2, 1, 1], 1, 64, 16)
+    before = [c.dev.k.clone(), c.dev.v.clone()]
+    c.kv_len[0], c.kv_len[1], c.kv_len[2] = -2 ** 31, 2 ** 31 - 1, -1
+    x = dev_rows(c.row(4))
+    say("kv append and read, extreme lengths")
+    c.M.kv_append(c.dev, 0, x, x, c.dev_batch())
+    assert torch.equal(c.dev.k, before[0]) and torch.equal(c.dev.v, before[1])
+    for y in c.M.kv_read(c.dev, 0, c.dev_batch()):
+        assert torch.isnan(y).all()
+    one = c.M.KVBatch(c.dev_batch().table[1:2].contiguous(), torch.tensor([-2 ** 31], dtype=torch.int32, device="cuda"),
+                      torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1)
+    c.M.kv_append(c.dev, 0, x[:1], x[:1], one)
+    for y in c.M.kv_read(c.dev, 0, one):
+        assert torch.isnan(y).all()
+
+
+@pytest.mark.parametrize("block,dim", [(32, 96), (64, 128), (128, 192), (256, 256)])
+def test_pages_of_many_blocks(block, dim):
+    """A page written by several waves, in chunks that end anywhere in it, with
+    scales that grow and values that are not finite in any of its blocks."""
+    c = Case(15, [1, 1], [1, 1], 2, dim, block, width=3, extra=8)
+    c.table[:] = [[0, 1, 2], [3, 4, 5]]
+    rng = np.random.default_rng(6)
+    c.kv_len[:] = 0
+    for step, (m0, m1) in enumerate([(17, 1), (1, 40), (30, 100), (0, 15), (100, 1), (1, 16)]):
+        c.kv_len += np.array([m0, m1], np.int32)
+        c.row_off = np.array([0, m0, m0 + m1], np.int32)
+        c.n_rows, c.max_new = m0 + m1, max(m0, m1)
+        k, v = c.row(c.n_rows) * 2.0 ** (step % 3 * 3), c.row(c.n_rows) * 2.0 ** (step % 2 * 4)
+        k[rng.integers(c.n_rows), 1, 3], v[rng.integers(c.n_rows), 0, 5] = np.inf, np.nan
+        say(f"kv append, blocks of a page, {block} {dim} step {step}")
+        _append(c, k, v)
+        assert c.pages_equal() == "", f"step {step}"
+        _read_equal(c)
+
+
 def test_untouched_pages_keep_their_bytes():
     torch = torch_cuda()
     c = Case(11, [1, 1], [18, 40], 2, 64, 16)

@@ -64,3 +64,12 @@ def test_nothing_to_do():
     assert L.mlora_kv_append(c, 0, None, None, 128, 64, b, None) == M.OK
     assert L.mlora_kv_read(c, 0, b, None, None, None) == M.OK
     assert L.mlora_kv_attention(c, 0, None, 128, 64, 2, b, 1, 0, 0.125, None, None, 0, None) == M.OK
+
+
+def test_rows_past_what_the_kernels_count():
+    """2^24 rows of 32 query heads to a key/value head: refused, not wrapped."""
+    L = M.lib()
+    for rows, heads in ((1 << 24, 64), ((1 << 23) + 1, 64)):
+        c, b = _descs(n_rows=rows, max_new=rows)
+        assert L.mlora_kv_attention(c, 0, 4096, 128, 64, heads, b, 1, 0, 0.125, 4096, 4096, 1 << 60, None) == M.EINVAL
+        assert b"2^28" in L.mlora_last_error()
