@@ -79,6 +79,10 @@ template <int D>
 struct RowsTile {
   static constexpr int R = (D + 63) / 64;  // 16-byte loads of a lane for a token's keys
   static constexpr int T = D / 16;         // channel tiles of the output
+  // workgroups of a CU: at 256 channels the registers of two would not hold the
+  // output (64 sequences of 500 .. 4000 tokens: 93 us with two, 64 us with one;
+  // at 192 channels 46 and 49 us)
+  static constexpr int PER_CU = D > 192 ? 1 : 2;
 };
 
 // Loads of the next step are issued as soon as the registers they go to have
@@ -709,7 +713,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     for (int n = 0; n < NT; ++n) {
       const float l = sum_halves(L[n]);
       const int row = wave * 32 * NT + 32 * n + q, rr = t.r0 + row;
-      if (rr > t.r1) continue;
+      if (rr > t.r1) continue;  // (both lanes of a row)
       if (slot >= 0) {
         float* dst = sched_slot(a.work, slot, X::R, D);
 #pragma unroll
@@ -723,15 +727,26 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
           }
         if (hf == 0) dst[X::R * D + row] = M[n], dst[X::R * D + X::R + row] = l;
       } else {
+        // The two halves of the wave hold four channels in turn; they change
+        // places so that a lane has eight in a row: half as many stores.
+        const float inv = mine[n].hi > mine[n].lo ? 1.f / l : 0.f;
+        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + 8 * hf;
 #pragma unroll
         for (int i = 0; i < T; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const int ch = 32 * i + 2 * e + 4 * hf;
-            if (ch < D)
-              write_row<D>(a, s, Hq, h, rr, ch, f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]}, l,
-                           mine[n].hi > mine[n].lo);
-          }
+          for (int e = 0; e < 16; e += 8)
+            if (32 * i + 2 * e < D) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const auto z = __builtin_amdgcn_permlane32_swap(
+                    pack_bf2_hw(o[n][i][e + 2 * k] * inv, o[n][i][e + 2 * k + 1] * inv),
+                    pack_bf2_hw(o[n][i][e + 4 + 2 * k] * inv, o[n][i][e + 5 + 2 * k] * inv), false, false);
+                x[k] = z[0];
+                x[2 + k] = z[1];
+              }
+              *reinterpret_cast<uint4*>(dst + 32 * i + 2 * e) = uint4{x[0], x[1], x[2], x[3]};
+            }
       }
     }
     p = next;
@@ -741,7 +756,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
 }
 
 template <int D, bool WHOLE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
+__global__ __launch_bounds__(64 * kWaves, RowsTile<D>::PER_CU) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
   __shared__ RowsLds<D> lds;
   rows_part<D, WHOLE>(c, a, d, lds);
 }
@@ -765,8 +780,7 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
     join_part<16, D>(c, few_a, few_workers, blockIdx.x - workers);
 }
 
-constexpr int kRowsWorkers = 512;   // few-row kernel: two workgroups a CU
-constexpr int kTileWorkers = 512;   // at most
+constexpr int kRowsWorkers = 512, kTileWorkers = 512;  // at most
 constexpr int kSkew = 24;
 constexpr int kFewRows = 16;
 
@@ -784,14 +798,22 @@ size_t tile_bytes(int D) { return (sched_bytes(kTileWorkers, 128, D) + 255) / 25
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   const int64_t rows = (int64_t)c.max_new * a.G;
-  const bool many = rows > kFewRows, few = !many || c.n_rows < (int64_t)c.max_new * c.n_seq;
+  const bool many = rows > kFewRows;
+  // Whether sequences of few rows are left to the few-row form.  In a batch of
+  // few sequences with more rows than that on average (prompts, drafts) the
+  // many-row form takes them along, which saves a launch that may find nothing:
+  // 8 prompts 70 -> 65 us, 2 prompts with 6 single rows 81 -> 72 us, a chunk
+  // of 1024 with 8 single rows 144 -> 139 us.
+  const bool few = !many || (c.n_rows < (int64_t)c.max_new * c.n_seq &&
+                             (c.n_seq > 16 || (int64_t)c.n_rows * a.G < kFewRows * (int64_t)c.n_seq));
+  constexpr int rw = 256 * RowsTile<D>::PER_CU;
+  static_assert(rw <= kRowsWorkers);
   if (!many) {
     const int64_t items = (int64_t)c.n_seq * c.H;
-    KvSched d{9, kSkew, 1, 2, 6, 0, 8, 0, INT32_MAX};
+    const KvSched d{rw == 512 ? 9 : 8, rw == 512 ? kSkew : 0, 1, 2, 6, 0, 8, 0, INT32_MAX};
     if (items > (1 << 20) || max_steps(c, a) > 20) {
-      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(kRowsWorkers), dim3(64 * kWaves), 0, stream, c, a, d);
-      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(kRowsWorkers, 4), dim3(256), 0, stream, c, a,
-                   kRowsWorkers);
+      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, a, d);
+      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(rw, 4), dim3(256), 0, stream, c, a, rw);
     } else {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)items), dim3(64 * kWaves), 0, stream, c, a, d);
     }
@@ -802,14 +824,14 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
                   INT32_MAX};
   KvAttn few_a = a;
   few_a.work = static_cast<char*>(a.work) + tile_bytes(D);
-  const KvSched few_d{9, kSkew, 0, 2, 6, 0, 8, 0, kFewRows};
+  const KvSched few_d{rw == 512 ? 9 : 8, rw == 512 ? kSkew : 0, 0, 2, 6, 0, 8, 0, kFewRows};
   if (few)
-    MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(kRowsWorkers), dim3(64 * kWaves), 0, stream, c, few_a,
+    MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, few_a,
                  few_d);
   MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(workers), dim3(256), 0, stream, c, a, d);
   if (few)
-    MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(workers + kRowsWorkers, 8), dim3(256), 0, stream, c, a,
-                 workers, few_a, kRowsWorkers);
+    MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(workers + rw, 8), dim3(256), 0, stream, c, a,
+                 workers, few_a, rw);
   else
     MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(workers, 8), dim3(256), 0, stream, c, a, workers);
   return launched();
