@@ -389,7 +389,7 @@ struct TileLds {
   SchedLds sched;
 };
 
-template <int D, int NT>
+template <int D, int NT, bool WHOLE>
 __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, const KvSched& d, TileLds<D, NT>& lds) {
   typedef ManyTile<D, NT> X;
   constexpr int T = X::T, NP = X::NP, QF = D / 16;
@@ -453,7 +453,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     for (int i = 0; i < NP; ++i)
       if (64 * i + 63 < D || lane + 64 * i < D) kr[i] = kp[lane + 64 * i], vr[i] = vp[lane + 64 * i];
   };
-  Pieces<X::R, false> pieces(c, a, d, lds.sched);
+  Pieces<X::R, WHOLE> pieces(c, a, d, lds.sched);
   P p, next;
   bool have = pieces.next(p);
   if (have) {
@@ -761,10 +761,10 @@ __global__ __launch_bounds__(64 * kWaves, RowsTile<D>::PER_CU) void kv_rows_kern
   rows_part<D, WHOLE>(c, a, d, lds);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool WHOLE>
 __global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
   __shared__ TileLds<D, NT> lds;
-  tile_part<D, NT>(c, a, d, lds);
+  tile_part<D, NT, WHOLE>(c, a, d, lds);
 }
 
 template <int R, int D>
@@ -783,6 +783,7 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
 constexpr int kRowsWorkers = 512, kTileWorkers = 512;  // at most
 constexpr int kSkew = 24;
 constexpr int kFewRows = 16;
+constexpr int kWholeSteps = 20;
 
 // Steps of an item at most, as far as the host can tell.
 int max_steps(const KvView& c, const KvAttn& a) {
@@ -797,7 +798,10 @@ size_t tile_bytes(int D) { return (sched_bytes(kTileWorkers, 128, D) + 255) / 25
 // is launched unless the batch cannot hold a sequence for it.
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
-  const int64_t rows = (int64_t)c.max_new * a.G;
+  constexpr int NT = 1, R = ManyTile<D, NT>::R;
+  constexpr int rw = 256 * RowsTile<D>::PER_CU, tw = 256 * ManyTile<D, NT>::PER_CU;
+  static_assert(rw <= kRowsWorkers && tw <= kTileWorkers);
+  const int64_t rows = (int64_t)c.max_new * a.G, heads = (int64_t)c.n_seq * c.H;
   const bool many = rows > kFewRows;
   // Whether sequences of few rows are left to the few-row form.  In a batch of
   // few sequences with more rows than that on average (prompts, drafts) the
@@ -806,34 +810,29 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   // of 1024 with 8 single rows 144 -> 139 us.
   const bool few = !many || (c.n_rows < (int64_t)c.max_new * c.n_seq &&
                              (c.n_seq > 16 || (int64_t)c.n_rows * a.G < kFewRows * (int64_t)c.n_seq));
-  constexpr int rw = 256 * RowsTile<D>::PER_CU;
-  static_assert(rw <= kRowsWorkers);
-  if (!many) {
-    const int64_t items = (int64_t)c.n_seq * c.H;
-    const KvSched d{rw == 512 ? 9 : 8, rw == 512 ? kSkew : 0, 1, 2, 6, 0, 8, 0, INT32_MAX};
-    if (items > (1 << 20) || max_steps(c, a) > 20) {
-      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, a, d);
-      MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(rw, 4), dim3(256), 0, stream, c, a, rw);
-    } else {
-      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)items), dim3(64 * kWaves), 0, stream, c, a, d);
-    }
+  const int64_t few_tiles = (std::min<int64_t>(rows, kFewRows) + 15) / 16, tiles = (rows + R - 1) / R;
+  KvSched fd{rw == 512 ? 9 : 8, rw == 512 ? kSkew : 0, (int)few_tiles, 2, 6, 0, 8, 0, many ? kFewRows : INT32_MAX};
+  KvSched td{tw == 512 ? 9 : 8, tw == 512 ? kSkew : 0, (int)tiles, 3, 6, a.causal, 4, few ? kFewRows : 0, INT32_MAX};
+
+  if (max_steps(c, a) <= kWholeSteps && std::max(few_tiles, many ? tiles : 0) * heads <= 1 << 20) {
+    if (few)
+      MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)(few_tiles * heads)), dim3(64 * kWaves), 0,
+                   stream, c, a, fd);
+    if (many)
+      MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT, true>), dim3((unsigned)(tiles * heads)), dim3(256), 0, stream, c,
+                   a, td);
     return launched();
   }
-  constexpr int NT = 1, R = ManyTile<D, NT>::R, workers = 256 * ManyTile<D, NT>::PER_CU;
-  const KvSched d{workers == 512 ? 9 : 8, workers == 512 ? kSkew : 0, 0, 3, 6, a.causal, 4, few ? kFewRows : 0,
-                  INT32_MAX};
-  KvAttn few_a = a;
-  few_a.work = static_cast<char*>(a.work) + tile_bytes(D);
-  const KvSched few_d{rw == 512 ? 9 : 8, rw == 512 ? kSkew : 0, 0, 2, 6, 0, 8, 0, kFewRows};
-  if (few)
-    MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, few_a,
-                 few_d);
-  MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT>), dim3(workers), dim3(256), 0, stream, c, a, d);
-  if (few)
-    MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(workers + rw, 8), dim3(256), 0, stream, c, a,
-                 workers, few_a, rw);
+  KvAttn fa = a;
+  if (many) fa.work = static_cast<char*>(a.work) + tile_bytes(D);
+  if (few) MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, fa, fd);
+  if (many) MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT, false>), dim3(tw), dim3(256), 0, stream, c, a, td);
+  if (few && many)
+    MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(tw + rw, 8), dim3(256), 0, stream, c, a, tw, fa, rw);
+  else if (many)
+    MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(tw, 8), dim3(256), 0, stream, c, a, tw);
   else
-    MLORA_LAUNCH("kv_join", (kv_join_kernel<R, D>), dim3(workers, 8), dim3(256), 0, stream, c, a, workers);
+    MLORA_LAUNCH("kv_join", (kv_join_kernel<16, D>), dim3(rw, 4), dim3(256), 0, stream, c, a, rw);
   return launched();
 }
 

@@ -297,10 +297,12 @@ struct Pieces {
     if constexpr (WHOLE) {
       if (left == 0) return false;
       left = 0;
+      // the last tiles, which see most, first; a head's stay on one XCD where
+      // there are 8 heads
       int item = blockIdx.x;
       h = item % c.H;
       item /= c.H;
-      k = item % d.tiles, seq = item / d.tiles;
+      seq = item % c.n_seq, k = d.tiles - 1 - item / c.n_seq;
       load();
       if (!sched_takes(d, s.m * a.G) || k * R >= s.m * a.G) return false;
       p.t = Tile<R>(c, a, s, k);
@@ -412,31 +414,36 @@ __device__ __forceinline__ void join_part(const KvView& c, const KvAttn& a, int 
   const KvSeq s = kv_seq(c, seq);
   const int r0 = tile * R, cnt = min(R, s.m * a.G - r0), Hq = c.H * a.G;
   const int d = 4 * (tid % DL), grp = tid / DL;
-  if (n <= kJoinFew) {
+  if (R > 16 || n <= kJoinFew) {
     for (int x = blockIdx.y * 256 + tid; x < cnt * DL; x += gridDim.y * 256) {
       const int r = x / DL, ch = 4 * (x % DL);
-      float m[kJoinFew], l[kJoinFew], top = -__builtin_huge_valf();
-      f32x4 v[kJoinFew];
-#pragma unroll
-      for (int i = 0; i < kJoinFew; ++i) {
-        m[i] = -__builtin_huge_valf();
-        l[i] = 0.f;
-        v[i] = f32x4{0, 0, 0, 0};
-        if (i < n) {
-          const float* slot = sched_slot(a.work, i == 0 ? 2 * w + 1 : 2 * (w + i), R, D);
-          m[i] = slot[R * D + r], l[i] = slot[R * D + R + r];
-          v[i] = *reinterpret_cast<const f32x4*>(slot + r * D + ch);
-        }
-        top = fmaxf(top, m[i]);
-      }
-      const float ref = top == -__builtin_huge_valf() ? 0.f : top;
-      float L = 0.f;
+      float M = -__builtin_huge_valf(), L = 0.f;
       f32x4 o{0, 0, 0, 0};
+      for (int i0 = 0; i0 < n; i0 += kJoinFew) {
+        float m[kJoinFew], l[kJoinFew], top = M;
+        f32x4 v[kJoinFew];
 #pragma unroll
-      for (int i = 0; i < kJoinFew; ++i) {
-        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
-        L += l[i] * f;
-        o += v[i] * f;
+        for (int i = 0; i < kJoinFew; ++i) {
+          m[i] = -__builtin_huge_valf();
+          l[i] = 0.f;
+          v[i] = f32x4{0, 0, 0, 0};
+          if (i0 + i < n) {
+            const float* slot = sched_slot(a.work, i0 + i == 0 ? 2 * w + 1 : 2 * (w + i0 + i), R, D);
+            m[i] = slot[R * D + r], l[i] = slot[R * D + R + r];
+            v[i] = *reinterpret_cast<const f32x4*>(slot + r * D + ch);
+          }
+          top = fmaxf(top, m[i]);
+        }
+        const float ref = top == -__builtin_huge_valf() ? 0.f : top, f0 = __builtin_amdgcn_exp2f(M - ref);
+        M = top;
+        L *= f0;
+        o *= f0;
+#pragma unroll
+        for (int i = 0; i < kJoinFew; ++i) {
+          const float f = __builtin_amdgcn_exp2f(m[i] - ref);
+          L += l[i] * f;
+          o += v[i] * f;
+        }
       }
       write_row<D>(a, s, Hq, h, r0 + r, ch, o, L, row_sees(c, a, s, r0 + r));
     }
