@@ -74,6 +74,12 @@ __device__ __forceinline__ uint32_t ones2(uint32_t m) {
 // its 16 scores are those of the 16-token block g: exactly the probabilities
 // that it has to supply to the second product, whose other operand is the
 // block's 16 bytes of a channel, one load.  Nothing passes through LDS.
+//
+// Bound by reading the cache: 256 requests of 1000 .. 8100 tokens (8 heads of
+// 128 channels, 2.4 GB) take 418 us, 5.7 TB/s, where a plain read of 1 GiB
+// reaches 6.0; 32 requests of 100 .. 4000 tokens 32 us (3.9 TB/s): the parts
+// are found, the first loads arrive, the waves and the pieces are joined, about
+// 10 us that no other load hides.
 // ----------------------------------------------------------------------------
 template <int D>
 struct RowsTile {
@@ -87,7 +93,8 @@ struct RowsTile {
 
 // Loads of the next step are issued as soon as the registers they go to have
 // been read (the keys' after the first product, the values' after the second),
-// and its page ids a step before that.
+// and its page ids a step before that.  An id looked at where it was loaded had
+// the wave wait for all loads before it: 256 requests 431 us, not 420.
 template <int D>
 struct RowsLds {
   float m[kWaves][16], l[kWaves][16];
@@ -350,6 +357,13 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
 // products.  As in the few-row kernel the keys' rows are dealt to the matrix
 // rows so that a lane's 16 scores of a 32-token tile are 16 tokens in order,
 // which are its probabilities in the second product.
+//
+// A chunk of 2048 tokens over 16301 cached ones (32 query heads on 8, 128
+// channels, 581 GFLOP) takes 605 us, 960 TFLOP/s, where a library product of
+// 8192^3 reaches 1200; the clock is down to 2.1 GHz by then (matrix pipes busy
+// for 40 % of its cycles), so what makes the loop denser gives little time.
+// 64 rows a wave halve the reads from LDS, but take all registers of a SIMD
+// for one wave: 894 us when 32 rows took 736.
 // ----------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -780,9 +794,17 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
     join_part<16, D>(c, few_a, few_workers, blockIdx.x - workers);
 }
 
-constexpr int kRowsWorkers = 512, kTileWorkers = 512;  // at most
+constexpr int rows_workers(int D) { return D > 192 ? 256 : 512; }
+constexpr int tile_workers(int D) { return D > 128 ? 256 : 512; }
+// A chunk of 2048 tokens: workgroups 0 .. 255 end at 627 us and the others at
+// 768 us with equal parts; at 24 / 256 both ends meet (620 -> 604 us).
 constexpr int kSkew = 24;
+// 32 sequences of 20 rows: 51 us in the many-row form, 53 us as two 16-row tiles.
 constexpr int kFewRows = 16;
+// Up to this many steps an item goes to a workgroup whole: no parts to find, no
+// pieces to join, and the hardware deals the items.  8 prompts of 240 .. 890
+// tokens: 64 us in parts, 48 us whole; over a hundred batches of all kinds the
+// time over the floor is 2.19 / 2.18 / 2.48 times at 12 / 20 / 32 steps.
 constexpr int kWholeSteps = 20;
 
 // Steps of an item at most, as far as the host can tell.
@@ -791,7 +813,7 @@ int max_steps(const KvView& c, const KvAttn& a) {
   return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, (a.window + c.max_new) / kKvStep + 2) : cap);
 }
 
-size_t tile_bytes(int D) { return (sched_bytes(kTileWorkers, 128, D) + 255) / 256 * 256; }
+size_t tile_bytes(int D) { return (sched_bytes(tile_workers(D), 128, D) + 255) / 256 * 256; }
 
 // Sequences of at most kFewRows rows (new tokens times query heads of a
 // key/value head) take the few-row form, the others the many-row one; each
@@ -799,8 +821,8 @@ size_t tile_bytes(int D) { return (sched_bytes(kTileWorkers, 128, D) + 255) / 25
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   constexpr int NT = 1, R = ManyTile<D, NT>::R;
-  constexpr int rw = 256 * RowsTile<D>::PER_CU, tw = 256 * ManyTile<D, NT>::PER_CU;
-  static_assert(rw <= kRowsWorkers && tw <= kTileWorkers);
+  constexpr int rw = rows_workers(D), tw = tile_workers(D);
+  static_assert(rw == 256 * RowsTile<D>::PER_CU && tw == 256 * ManyTile<D, NT>::PER_CU);
   const int64_t rows = (int64_t)c.max_new * a.G, heads = (int64_t)c.n_seq * c.H;
   const bool many = rows > kFewRows;
   // Whether sequences of few rows are left to the few-row form.  In a batch of
@@ -845,7 +867,7 @@ bool kv_attention_dim(int dim) {
 
 size_t kv_work_bytes(const KvView& c, int heads) {
   if (c.n_rows == 0) return 0;
-  const size_t few = sched_bytes(kRowsWorkers, 16, c.D);
+  const size_t few = sched_bytes(rows_workers(c.D), 16, c.D);
   return (int64_t)c.max_new * (heads / c.H) > kFewRows ? tile_bytes(c.D) + few : few;
 }
 

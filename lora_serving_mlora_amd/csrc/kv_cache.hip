@@ -1,14 +1,21 @@
 // Writing new tokens into the paged 8-bit key/value cache, and reading them
 // back.  Both are bound by memory traffic (2 bytes a channel on the bf16
 // side, 1 on the cache's) and, for a decode step, by the latency of a launch
-// with a few dependent loads (row_off -> table -> page).
+// with a few dependent loads (row_off -> table -> page):
+//   one new token of 256 requests (8 heads of 128 channels) written in 4.6 us,
+//   the 2200 tokens of the pages read back in 8.3 us;
+//   4238 tokens of 8 prompts written in 12 us (26 MB);
+//   32768 tokens read back in 44 us from memory (201 MB, 4.6 TB/s; a plain copy
+//   reaches 5.1) and 31 us from the last-level cache;
+//   64 histories of 1 .. 1500 tokens, 80 channels, in 18 us (5.0 TB/s).
 //
-// One workgroup owns one page of one head, keys or values, so a page's scale
-// is found and used without another launch, and no two workgroups write one
-// page.  The sequence and page of a workgroup come from its index in closed
-// form: sequence i's pages start at item row_off[i] / B + 2 i, which leaves it
-// at least as many items as m rows touch pages, so the grid is known on the
-// host although the lengths are not, and no prefix sum is needed.
+// A page of one head, keys or values, is written by the waves of one
+// workgroup, so its scale is found and used without another launch, and no two
+// workgroups write one page.  The sequence and page of a workgroup come from
+// its index in closed form: sequence i's pages start at item row_off[i] / B +
+// 2 i, which leaves it at least as many items as m rows touch pages, so the
+// grid is known on the host although the lengths are not, and no prefix sum is
+// needed.
 #include <algorithm>
 #include <type_traits>
 
@@ -141,7 +148,8 @@ __device__ __forceinline__ Scale new_scale(uint32_t amax, bool kept, float was) 
 }
 
 // One new row of each sequence: a wave takes it for one head, keys or values,
-// a lane 2 * NC channels.  What bounds it is the chain of dependent loads
+// a lane 2 * NC channels (9 us by the kernel for pages, 4.6 us by this one: 256
+// rows, 8 heads).  What bounds it is the chain of dependent loads
 // (kv_len -> table -> scale), so nothing else waits: the row is on its way
 // before the table's entry is looked at.
 template <bool VEC, int NC>

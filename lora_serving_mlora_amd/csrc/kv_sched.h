@@ -8,7 +8,8 @@
 // one long sequence is cut into many pieces and many short ones are packed
 // together, and no length is ever read by the host.  A cut that falls close to
 // an item's end is moved there (by both neighbours alike), which keeps pieces
-// from being tiny.  The order and the cuts depend on the batch
+// from being tiny; within 6 steps, as more unbalances long parts (an eighth of
+// the part: 256 requests 449 us, not 431; a 2048-token chunk 719 us, not 654).  The order and the cuts depend on the batch
 // alone, so results are the same from call to call.
 //
 // A cut item's pieces go to the caller's work buffer as (O, M, L) and are
@@ -131,7 +132,7 @@ __device__ __forceinline__ int64_t sched_place(const KvSched& d, int64_t share, 
 // The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p).
 // Everything that depends on the number of tiles is done by all 256 threads
 // side by side: one thread that went through the tiles of a long prompt alone
-// took longer than the products of a short one.
+// took longer than the products of a short one (8 prompts 90 us, not 66).
 template <int R>
 __device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, const KvSched& d, int w, SchedLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
