@@ -810,7 +810,7 @@ constexpr int kWholeSteps = 20;
 // Steps of an item at most, as far as the host can tell.
 int max_steps(const KvView& c, const KvAttn& a) {
   const int64_t cap = ((int64_t)c.width << c.lb) / kKvStep + 1;
-  return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, (a.window + c.max_new) / kKvStep + 2) : cap);
+  return (int)(a.causal && a.window > 0 ? std::min<int64_t>(cap, ((int64_t)a.window + c.max_new) / kKvStep + 2) : cap);
 }
 
 size_t tile_bytes(int D) { return (sched_bytes(tile_workers(D), 128, D) + 255) / 256 * 256; }

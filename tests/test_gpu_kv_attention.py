@@ -85,6 +85,17 @@ def test_masks(name, kw):
     _run(c, _queries(c, 4), f"{name} {kw}", **kw)
 
 
+def test_the_largest_window():
+    new, total = BATCHES["chunks"]
+    c = Case(41, new, total, 2, 64, 16, width=512)
+    q = _queries(c, 4)
+    _fill_new_plain(c)
+    a = _run(c, q, "no window")
+    b = _run(c, q, "window 2^31 - 1", window=2 ** 31 - 1)
+    torch = torch_cuda()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1)])
 def test_strided_and_unaligned_queries(pad, offset):
     new, total = BATCHES["chunks"]
