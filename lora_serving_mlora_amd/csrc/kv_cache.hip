@@ -3,11 +3,11 @@
 // side, 1 on the cache's) and, for a decode step, by the latency of a launch
 // with a few dependent loads (row_off -> table -> page):
 //   one new token of 256 requests (8 heads of 128 channels) written in 4.6 us,
-//   the 2200 tokens of the pages read back in 8.3 us;
+//   the 2200 tokens of the pages read back in 7.4 us;
 //   4238 tokens of 8 prompts written in 12 us (26 MB);
 //   32768 tokens read back in 44 us from memory (201 MB, 4.6 TB/s; a plain copy
 //   reaches 5.1) and 31 us from the last-level cache;
-//   64 histories of 1 .. 1500 tokens, 80 channels, in 18 us (5.0 TB/s).
+//   64 histories of 1 .. 1500 tokens, 80 channels, in 17 us (5.4 TB/s).
 //
 // A page of one head, keys or values, is written by the waves of one
 // workgroup, so its scale is found and used without another launch, and no two
@@ -25,7 +25,7 @@ namespace mlora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kReadGroups = 16384;  // workgroups that a read is split into where it has the units
+constexpr int kReadGroups = 1792;  // workgroups of the read kernel that the card holds at once
 
 struct Item {
   int seq, blk;    // sequence, index in it of the page or token block (blk < 0: nothing to do)
@@ -478,9 +478,11 @@ hipError_t launch_kv_append(const KvView& c, const uint16_t* k, const uint16_t* 
 
 hipError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, hipStream_t stream) {
   const bool single = c.max_new == 1;
-  const int items = item_count(c, 4, single), most = (c.H * c.D + kThreads - 1) / kThreads;
-  // a unit a thread until there are enough workgroups, then several
-  const int split = std::min(most, std::max(1, kReadGroups / items));
+  const int items = item_count(c, 4, single), full = std::max(1, c.H * c.D / kThreads);
+  // A unit a thread where all workgroups run at once, and where there are many
+  // rounds of them anyway (32768 tokens 31 us, 33 us with four units a thread);
+  // in between as many as fill one round (256 requests' pages 8.5 -> 7.4 us).
+  const int split = items > kReadGroups ? full : std::min(full, kReadGroups / items);
   MLORA_LAUNCH("kv_read", kv_read_kernel, dim3(items, split), dim3(kThreads), 0, stream, c, k, v, single);
   return launched();
 }
