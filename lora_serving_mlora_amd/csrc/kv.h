@@ -53,12 +53,6 @@ __device__ __forceinline__ KvSeq kv_seq_scalar(const KvView& c, int i) {
 }
 
 // page of sequence i's page-index p, -1 where it has none that exists
-__device__ __forceinline__ int kv_page(const KvView& c, int i, int p) {
-  int id = -1;
-  if (p >= 0 && p < c.width) id = c.table[(size_t)i * c.table_stride + p];
-  return (unsigned)id < (unsigned)c.n_blocks ? id : -1;
-}
-
 __device__ __forceinline__ int kv_page_scalar(const KvView& c, int i, int p) {
   int id = -1;
   if (p >= 0 && p < c.width) id = kv_scalar(c.table + (size_t)i * c.table_stride + p);

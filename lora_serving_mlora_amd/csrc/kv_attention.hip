@@ -212,8 +212,9 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
         st[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[x][i].x, kw[x][i].y, ks), qf[i][0], st[x], 0, 0, 0);
-          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(kw[x][i].z, kw[x][i].w, ks), qf[i][1], st[x], 0, 0, 0);
+          const bf16x8 lo = frag_fp8(kw[x][i].x, kw[x][i].y, ks), hi = frag_fp8(kw[x][i].z, kw[x][i].w, ks);
+          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, qf[i][0], st[x], 0, 0, 0);
+          st[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, qf[i][1], st[x], 0, 0, 0);
         }
       }
       if (more) {
@@ -296,10 +297,9 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
       }
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].x, vw[i].y, vsc), frag(pw[0], pw[1], pw[2], pw[3]),
-                                                       o[i], 0, 0, 0);
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag_fp8(vw[i].z, vw[i].w, vsc), frag(pw[4], pw[5], pw[6], pw[7]),
-                                                       o[i], 0, 0, 0);
+        const bf16x8 lo = frag_fp8(vw[i].x, vw[i].y, vsc), hi = frag_fp8(vw[i].z, vw[i].w, vsc);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, frag(pw[0], pw[1], pw[2], pw[3]), o[i], 0, 0, 0);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, frag(pw[4], pw[5], pw[6], pw[7]), o[i], 0, 0, 0);
       }
       if (more) load_v();
     }

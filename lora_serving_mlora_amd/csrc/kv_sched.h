@@ -4,13 +4,14 @@
 // An item is a tile of R rows of one (sequence, key/value head); it walks its
 // visible tokens in steps of 64.  Items lie on a line in the order (sequence,
 // head, tile), each as long as its steps plus `over` for what an item costs
-// besides; workgroup w takes the w-th of 2^lw (nearly) equal parts of the line, so
-// one long sequence is cut into many pieces and many short ones are packed
-// together, and no length is ever read by the host.  A cut that falls close to
-// an item's end is moved there (by both neighbours alike), which keeps pieces
-// from being tiny; within 6 steps, as more unbalances long parts (an eighth of
-// the part: 256 requests 449 us, not 431; a 2048-token chunk 719 us, not 654).  The order and the cuts depend on the batch
-// alone, so results are the same from call to call.
+// besides; workgroup w takes the w-th of 2^lw (nearly) equal parts of the
+// line, so one long sequence is cut into many pieces and many short ones are
+// packed together, and no length is ever read by the host.  A cut that falls
+// within 6 steps of an item's end is moved there (by both neighbours alike),
+// which keeps pieces from being tiny; farther moves leave long parts unequal
+// (an eighth of the part: 256 requests 449 us, not 431; a 2048-token chunk 719
+// us, not 654).  The order and the cuts depend on the batch alone, so results
+// are the same from call to call.
 //
 // A cut item's pieces go to the caller's work buffer as (O, M, L) and are
 // joined by join_part: worker w's slot 2w holds the piece that its part
