@@ -399,7 +399,10 @@ struct TileLds {
   uint4 v[2][8 * X::DV];        // [16-token block][half][channel]: 8 tokens a unit
   uint32_t mark[2][4 * X::DV];  // [block][channel]: a bit for each token whose value is NaN
   uint32_t bad[2];              // a byte for each block without a page
-  int nan[2];                   // step with marks, plus 1
+  // Step with marks, plus 1.  It has no first value, as storing one would race
+  // with another wave's first mark; whatever it holds is right, because a step
+  // that rows differ in writes all its marks, and unmarked values change nothing.
+  int nan[2];
   SchedLds sched;
 };
 
@@ -411,7 +414,6 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
   const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
   const float cs = a.scale * 1.4426950408889634f;
-  if (tid < 2) lds.nan[tid] = 0;
 
   // Piece i of this lane: bytes 16 (lane + 64 i) of the block's keys and of its
   // values (both 16 D bytes); its places in LDS.
