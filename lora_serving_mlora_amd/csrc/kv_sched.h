@@ -130,6 +130,14 @@ __device__ __forceinline__ int64_t sched_place(const KvSched& d, int64_t share, 
   return share * w + (share * more * d.skew >> 8);
 }
 
+// Which head holds the place `off` into a sequence whose heads take `head` each.
+// A division in 64 bits takes half a microsecond, so one in 32 serves where
+// both fit; one head passes 2^32 for a prompt of 3 M tokens and 8 query heads.
+__host__ __device__ __forceinline__ int sched_head(int64_t off, int64_t head) {
+  if (off < head) return 0;
+  return off <= INT32_MAX ? (int)((uint32_t)off / (uint32_t)head) : (int)(off / head);
+}
+
 // The part of worker w: its first place (L.pos[0]) and its end (L.pos[1].p).
 // Everything that depends on the number of tiles is done by all 256 threads
 // side by side: one thread that went through the tiles of a long prompt alone
@@ -197,8 +205,7 @@ __device__ __forceinline__ void sched_part(const KvView& c, const KvAttn& a, con
         at += head * c.H;
         continue;
       }
-      // (a division in 64 bits takes half a microsecond)
-      const int h = p - at <= INT32_MAX ? (int)((uint32_t)(p - at) / (uint32_t)head) : (int)((p - at) / head);
+      const int h = sched_head(p - at, head);
       L.pos[b] = {p, i, h, 0, 0};
       L.at[b] = at + h * head;
       break;
@@ -270,11 +277,12 @@ struct Pieces {
   const KvView& c;
   const KvAttn& a;
   const KvSched& d;
-  int w, left, first, tail[3], seq, h, k, off;
+  int64_t left;  // of the part
+  int w, first, tail[3], seq, h, k, off;
   KvSeq s;
 
   __device__ __forceinline__ Pieces(const KvView& c_, const KvAttn& a_, const KvSched& d_, SchedLds& L)
-      : c(c_), a(a_), d(d_), w(blockIdx.x), left(1), first(0), tail{-1, 0, 0}, h(0), k(0), off(0) {
+      : c(c_), a(a_), d(d_), left(1), w(blockIdx.x), first(0), tail{-1, 0, 0}, h(0), k(0), off(0) {
     if constexpr (!WHOLE) {
       // neighbours on the line go to one XCD (workgroups are dealt to the 8 in
       // turn), whose L2 then serves the tiles that share keys and values
@@ -282,7 +290,8 @@ struct Pieces {
       sched_part<R>(c, a, d, w, L);
       const SchedPos b = L.pos[0];
       const int64_t length = L.pos[1].p - b.p;
-      left = __builtin_amdgcn_readfirstlane((int)min<int64_t>(length, INT32_MAX));
+      left = (int64_t)__builtin_amdgcn_readfirstlane((int)(length >> 32)) << 32 |
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)length);
       seq = __builtin_amdgcn_readfirstlane(b.seq), h = __builtin_amdgcn_readfirstlane(b.h);
       k = __builtin_amdgcn_readfirstlane(b.k), off = __builtin_amdgcn_readfirstlane(b.off);
       if (left > 0) load();
@@ -343,7 +352,7 @@ struct Pieces {
           off = 0;
           continue;
         }
-        const int take = min(left, len - off);
+        const int take = (int)min<int64_t>(left, len - off);
         const bool head = off == 0, end = off + take == len;
         if (!head) first = end ? 1 : 2;
         if (head && !end) tail[0] = seq, tail[1] = h, tail[2] = p.tile;
