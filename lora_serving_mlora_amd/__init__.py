@@ -536,8 +536,10 @@ class KVCache:
                 raise TypeError(f"storage: {name} must be a contiguous {dt} CUDA tensor")
             if tuple(x.shape) != shape:
                 raise ValueError(f"storage: {name} has shape {tuple(x.shape)}, expected {shape}")
+            if x.get_device() != storage[0].get_device():
+                raise ValueError(f"storage: {name} is on another device than k")
         self.k, self.v, self.k_scale, self.v_scale = storage
-        self.device_index = self.k.device.index
+        self.device_index = self.k.get_device()
         self._d = _KVCacheDesc(n_layers, kv_heads, dim, block, n_blocks, *(x.data_ptr() for x in storage))
         self._ref = ctypes.addressof(self._d)
 
@@ -557,24 +559,31 @@ class KVBatch:
                 raise TypeError(f"{name} must be an int32 CUDA tensor of {nd} dimension(s)")
             if x.shape[-1] > 1 and x.stride(-1) != 1:
                 raise TypeError(f"{name} must be dense in its last dimension")
+            if x.get_device() != table.get_device():
+                raise ValueError(f"{name} is on another device than table")
         n_seq = kv_len.shape[0]
         if table.shape[0] != n_seq or row_off.shape[0] != n_seq + 1:
             raise ValueError(f"table must have {n_seq} rows and row_off {n_seq + 1} entries, as kv_len has {n_seq}")
         self.table, self.kv_len, self.row_off, self.n_rows, self.n_seq = table, kv_len, row_off, n_rows, n_seq
         self.max_new = n_rows if max_new is None else max_new
+        self.device_index = table.get_device()
         width = table.shape[1]
         self._d = _KVBatchDesc(table.data_ptr(), kv_len.data_ptr(), row_off.data_ptr(), n_seq, width,
                                table.stride(0) if n_seq > 1 else width, n_rows, self.max_new)
         self._ref = ctypes.addressof(self._d)
 
 
-def _kv_rows(x, name: str, batch: KVBatch, heads: int, dim: int):
-    """Checks bf16 rows [n_rows][heads][dim]; strides in elements."""
-    if x.dtype is not _torch().bfloat16 or not x.is_cuda:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+def _kv_rows(x, name: str, cache: KVCache, batch: KVBatch, heads: int):
+    """Checks bf16 rows [n_rows][heads][dim] and where they and the batch are;
+    strides in elements."""
+    device = cache.device_index
+    if x.dtype is not _torch().bfloat16 or x.get_device() != device:
+        raise TypeError(f"{name} must be a bfloat16 tensor on cuda:{device}, as the cache is")
+    if batch.device_index != device:
+        raise ValueError(f"the batch must be on cuda:{device}, as the cache is")
     shape = x.shape
-    if len(shape) != 3 or shape[0] != batch.n_rows or shape[2] != dim or (heads and shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{batch.n_rows}][{heads or 'heads'}][{dim}]")
+    if len(shape) != 3 or shape[0] != batch.n_rows or shape[2] != cache.dim or (heads and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{batch.n_rows}][{heads or 'heads'}][{cache.dim}]")
     st = x.stride()
     if st[2] != 1:
         raise TypeError(f"{name} must be dense in its channels")
@@ -589,8 +598,8 @@ def _kv_stream(cache: KVCache) -> int:
 def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
     """Quantises the batch's new rows, bf16 [n_rows][kv_heads][dim] (slices
     of a joint projection's output serve as they are), into the cache."""
-    st = _kv_rows(k, "k", batch, cache.kv_heads, cache.dim)
-    if _kv_rows(v, "v", batch, cache.kv_heads, cache.dim) != st:
+    st = _kv_rows(k, "k", cache, batch, cache.kv_heads)
+    if _kv_rows(v, "v", cache, batch, cache.kv_heads) != st:
         k, v = k.contiguous(), v.contiguous()
         st = k.stride()
     status = lib().mlora_kv_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), st[0], st[1], batch._ref,
@@ -602,6 +611,8 @@ def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
 def kv_read(cache: KVCache, layer: int, batch: KVBatch):
     """The batch's rows of the cache as bf16: (k, v), [n_rows][kv_heads][dim]."""
     torch = _torch()
+    if batch.device_index != cache.device_index:
+        raise ValueError(f"the batch must be on cuda:{cache.device_index}, as the cache is")
     shape, dev = (batch.n_rows, cache.kv_heads, cache.dim), cache.k.device
     k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
@@ -627,14 +638,16 @@ def kv_attention(cache: KVCache, layer: int, q, batch: KVBatch, causal: bool = T
     """Attention of q, bf16 [n_rows][heads][dim], over the batch's sequences;
     scale defaults to dim ** -0.5.  Returns bf16 [n_rows][heads][dim]."""
     torch = _torch()
-    rs, hs, _ = _kv_rows(q, "q", batch, 0, cache.dim)
+    rs, hs, _ = _kv_rows(q, "q", cache, batch, 0)
     shape = (batch.n_rows, q.shape[1], cache.dim)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
-    elif tuple(_bf16_dev(out, "out").shape) != shape:
-        raise ValueError(f"out must be {list(shape)}")
+    elif tuple(_bf16_dev(out, "out").shape) != shape or out.get_device() != cache.device_index:
+        raise ValueError(f"out must be {list(shape)} on cuda:{cache.device_index}, as the cache is")
     if work is None:
         work = new_kv_work(cache, batch, shape[1])
+    elif not isinstance(work, torch.Tensor) or work.get_device() != cache.device_index or not work.is_contiguous():
+        raise TypeError(f"work must be a contiguous tensor on cuda:{cache.device_index}, as the cache is")
     status = lib().mlora_kv_attention(cache._ref, layer, q.data_ptr(), rs, hs, shape[1], batch._ref, causal, window,
                                       cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), work.data_ptr(),
                                       work.nbytes, _kv_stream(cache))
