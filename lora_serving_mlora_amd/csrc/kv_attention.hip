@@ -1,9 +1,9 @@
 // Attention over the paged 8-bit key/value cache.
 //
 // For a row with query q at position x, over the tokens t that it sees:
-//   s_t = q . k_t,  p_t = 2^(s_t c - M),  o = sum_t p_t v_t / sum_t p_t,
+//   s_t = q . k_t,  p_t = 2^((s_t - M) c),  o = sum_t p_t v_t / sum_t p_t,
 // c = scale * log2(e), in one pass: M is a running reference for the largest
-// s_t c, and what was summed under an older one is multiplied by the quotient.
+// s_t, and what was summed under an older one is multiplied by the quotient.
 // The codes become bf16 in registers, times their page's scale: exact, so the
 // products lose nothing against an unquantised bf16 cache.  (The 8-bit matrix
 // instruction would take the codes as they are and run at twice the rate, but
@@ -18,9 +18,25 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr float kInf = __builtin_huge_valf();
+constexpr float kInf = __builtin_huge_valf(), kMax = 0x1.fffffep127f;
 constexpr int kWaves = 4;
 constexpr float kSlack = 8.f;  // log2 by which a score may pass M before the sums are rescaled
+
+// An exponent is s * cs - ref, one operation.  What ref = M * cs was rounded by,
+// 2^-25 of it, is what the exponent of the largest score is off by: too much
+// for any probability to stay finite, or above 0, once ref passes 2^31.  From
+// kHuge on, scores that differ at all do so by 2^5 in the exponent, so the
+// largest has all the weight whatever the factor: a power of two makes ref exact.
+constexpr float kHuge = 0x1p30f;
+struct Ref {
+  float cs, ref;
+  __device__ __forceinline__ Ref(float M, float scale) {
+    const float pow2 = __uint_as_float(__float_as_uint(scale) & 0x7f800000u);
+    cs = fabsf(M * scale) >= kHuge ? pow2 : scale;
+    ref = M == -kInf ? 0.f : M * cs;
+  }
+  __device__ __forceinline__ float p(float s) const { return __builtin_amdgcn_exp2f(__builtin_fmaf(s, cs, -ref)); }
+};
 
 __device__ __forceinline__ bf16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8, uint4{a, b, c, d});
@@ -108,7 +124,7 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 15, g = lane >> 4, kblk = q >> 2, B = 1 << c.lb;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
-  const float cs = a.scale * 1.4426950408889634f;
+  const float cs = a.scale * 1.4426950408889634f, slack = fminf(kSlack / cs, kMax);
 
   typedef Piece<16> P;
   bf16x8 qf[R][2];
@@ -276,21 +292,22 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
       float mx = -kInf;
 #pragma unroll
       for (int x = 0; x < 4; ++x) mx = fmaxf(fmaxf(fmaxf(mx, st[x][0]), fmaxf(st[x][1], st[x][2])), st[x][3]);
-      mx = max_rows(mx) * cs;
-      if (__ballot(mx > M + kSlack)) {
-        const float Mn = fmaxf(M, mx), f = Mn == M ? 1.f : __builtin_amdgcn_exp2f(M - Mn);
+      mx = max_rows(mx);
+      if (__ballot(mx > M + slack)) {
+        const float Mn = fmaxf(M, mx);
+        const float f = Mn == M ? 1.f : __builtin_amdgcn_exp2f((M - Mn) * cs);
         M = Mn;
         L *= f;
 #pragma unroll
         for (int i = 0; i < T; ++i) o[i] *= f;
       }
-      const float ref = M == -kInf ? 0.f : M;
+      const Ref ref(M, cs);
       uint32_t pw[8];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[x][e], cs, -ref));
+        for (int e = 0; e < 4; ++e) p[e] = ref.p(st[x][e]);
         L += (p[0] + p[1]) + (p[2] + p[3]);
         pw[2 * x] = pack_bf2_hw(p[0], p[1]);
         pw[2 * x + 1] = pack_bf2_hw(p[2], p[3]);
@@ -307,7 +324,7 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
 
     // join the waves
     if (g == 0) {
-      lds.m[wave][q] = M;
+      lds.m[wave][q] = M * cs;
       lds.l[wave][q] = L;
     }
 #pragma unroll
@@ -413,7 +430,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.rs * 2) | (uintptr_t)(a.hs * 2)) & 15u) == 0;
-  const float cs = a.scale * 1.4426950408889634f;
+  const float cs = a.scale * 1.4426950408889634f, slack = fminf(kSlack / cs, kMax);
 
   // Piece i of this lane: bytes 16 (lane + 64 i) of the block's keys and of its
   // values (both 16 D bytes); its places in LDS.
@@ -657,13 +674,14 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
           float m = fmaxf(st[0][n][0], st[1][n][0]);
 #pragma unroll
           for (int e = 1; e < 16; ++e) m = fmaxf(fmaxf(m, st[0][n][e]), st[1][n][e]);
-          mx[n] = max_halves(m) * cs;
-          up |= mx[n] > M[n] + kSlack;
+          mx[n] = max_halves(m);
+          up |= mx[n] > M[n] + slack;
         }
         if (__ballot(up)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const float Mn = fmaxf(M[n], mx[n]), f = Mn == M[n] ? 1.f : __builtin_amdgcn_exp2f(M[n] - Mn);
+            const float Mn = fmaxf(M[n], mx[n]);
+            const float f = Mn == M[n] ? 1.f : __builtin_amdgcn_exp2f((M[n] - Mn) * cs);
             M[n] = Mn;
             L[n] *= f;
 #pragma unroll
@@ -673,16 +691,14 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
         // Group c of 8 tokens: its probabilities, then its products, beside which
         // the next group's probabilities are made, and the reads as above.
         {
-          float ref[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) ref[n] = M[n] == -kInf ? 0.f : M[n];
+          static_assert(NT == 1);
+          const Ref ref(M[0], cs);
           uint32_t pw[NT][2][4];  // groups c and c + 1
           auto prob = [&](int c, int e) {  // tokens 2 e and 2 e + 1 of group c
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c >> 1][n][8 * (c & 1) + 2 * e], cs, -ref[n]));
-              const float p1 =
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(st[c >> 1][n][8 * (c & 1) + 2 * e + 1], cs, -ref[n]));
+              const float p0 = ref.p(st[c >> 1][n][8 * (c & 1) + 2 * e]);
+              const float p1 = ref.p(st[c >> 1][n][8 * (c & 1) + 2 * e + 1]);
               L[n] += p0 + p1;
               pw[n][c & 1][e] = pack_bf2_hw(p0, p1);
             }
@@ -741,7 +757,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
               *reinterpret_cast<f32x4*>(dst + row * D + ch) =
                   f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]};
           }
-        if (hf == 0) dst[X::R * D + row] = M[n], dst[X::R * D + X::R + row] = l;
+        if (hf == 0) dst[X::R * D + row] = M[n] * cs, dst[X::R * D + X::R + row] = l;
       } else {
         // The two halves of the wave hold four channels in turn; they change
         // places so that a lane has eight in a row: half as many stores.
