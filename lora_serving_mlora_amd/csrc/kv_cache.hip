@@ -134,17 +134,18 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float f) {
   return uint4{rescale4(w.x, f), rescale4(w.y, f), rescale4(w.z, f), rescale4(w.w, f)};
 }
 
-// exponent of a page's new scale, and what its older tokens take for it
+// exponent of a page's new scale, and what its older tokens take for it.  A
+// scale outside the range, in pages that the caller filled, is brought into it.
 struct Scale {
   int e;
-  bool grown;  // older tokens have to be rounded to it
+  bool moved;  // older tokens have to be rounded to it
   float inv, again;
 };
 __device__ __forceinline__ Scale new_scale(uint32_t amax, bool kept, float was) {
   const int need = scale_exp(amax);
-  const int old = min(max((int)((__float_as_uint(was) >> 23) & 255u) - 127, kKvExpMin), kKvExpMax);
-  const int e = kept ? max(old, need) : need;
-  return {e, kept && e > old, exp2i(-e), exp2i(max(old - e, -126))};
+  const int old = (int)((__float_as_uint(was) >> 23) & 255u) - 127;
+  const int e = kept ? min(max(old, need), kKvExpMax) : need;
+  return {e, kept && e != old, exp2i(-e), exp2i(max(old - e, -126))};
 }
 
 // One new row of each sequence: a wave takes it for one head, keys or values,
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_one_kernel(KvView c, const
     if (d >= D) continue;
     const uint32_t code = to_codes4<true>(lo_bf(x[i]), hi_bf(x[i]), 0.f, 0.f, s.inv);
     if (!is_v) {
-      if (s.grown)
+      if (s.moved)
         for (int j = 0; j < t; ++j) {
           uint16_t* w = reinterpret_cast<uint16_t*>(page + (size_t)j * D + d);
           *w = (uint16_t)rescale4(*w, s.again);
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_one_kernel(KvView c, const
       *reinterpret_cast<uint16_t*>(page + (size_t)t * D + d) = (uint16_t)code;
       continue;
     }
-    if (s.grown)
+    if (s.moved)
       for (int b = 0; 16 * b < t; ++b) {
         uint4* w = reinterpret_cast<uint4*>(page + ((size_t)16 * b * D + d * kKvBlk));
         w[0] = rescale16(w[0], s.again), w[1] = rescale16(w[1], s.again);
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, const uin
   slow |= s.e == kKvExpMax;
   if (on && r == 0 && lane == 0) *scale = exp2i(s.e);
 
-  if (s.grown && on) {
+  if (s.moved && on) {
     // the older tokens to the new scale, what is also written below by the same
     // lane (bytes of tokens to come may change: they hold nothing)
     const int end = (t0 - 1) >> 4;
