@@ -448,7 +448,8 @@ mlora_status mlora_merge(const mlora_pool* pool, int32_t adapter_id, int32_t pro
  * outside [0, n_blocks) or past `width` is not followed (append drops its
  * tokens, read gives NaN, attention gives NaN in the rows that see it), and
  * rows at a negative position (kv_len < m) are dropped by append, read as
- * NaN, and see nothing in attention.
+ * NaN, and see nothing in causal attention (without `causal` every row sees
+ * all of its sequence's tokens).
  * ------------------------------------------------------------------------- */
 typedef struct mlora_kv_cache {
   int32_t n_layers; /* >= 1                                                   */
