@@ -37,7 +37,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvView& c, int i) {
 }
 
 // a place that is the same for the whole wave: a scalar load (the batch's
-// tables, and while attention runs the scales, do not change)
+// tables, which do not change while a kernel runs)
 template <class T>
 __device__ __forceinline__ T kv_scalar(const T* p) {
   typedef const T __attribute__((address_space(4))) * constant;

@@ -366,7 +366,7 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
 }
 
 // ----------------------------------------------------------------------------
-// Many rows: 128 * NT rows of one (sequence, key/value head), 32 * NT a wave.
+// Many rows: 128 rows of one (sequence, key/value head), 32 a wave.
 // A step's 64 tokens are converted to bf16 once for the workgroup, on the way
 // from registers into LDS (two buffers, one barrier a step: the next step's
 // codes are converted and the one after's loads issued before the products),
@@ -394,24 +394,24 @@ __device__ __forceinline__ float sum_halves(float x) {
 }
 constexpr int kAhead = 8;  // reads of an operand from LDS ahead of its product
 
-template <int D, int NT>
+template <int D>
 struct ManyTile {
-  static constexpr int R = 128 * NT;
+  static constexpr int R = 128;
   static constexpr int U = D / 8;                 // 16-byte units of a token's keys in LDS
   static constexpr int G = U % 16 == 0 ? 16 : U % 8 == 0 ? 8 : U % 4 == 0 ? 4 : 2;
   static constexpr int SH = G == 16 ? 0 : G == 8 ? 1 : G == 4 ? 2 : 3;
   static constexpr int T = (D + 31) / 32, DV = 32 * T;
   static constexpr int NP = (D + 63) / 64;        // 16-byte pieces of a lane: a wave brings in one 16-token block
   // workgroups of a CU: what registers (two waves a SIMD) and LDS allow
-  static constexpr int PER_CU = NT == 1 && D <= 128 ? 2 : 1;
+  static constexpr int PER_CU = D <= 128 ? 2 : 1;
   // Units of a row change places with its number, so that 16 lanes of a
   // read (16 rows, one unit) fall on different banks.
   static __device__ __forceinline__ int k_unit(int row, int u) { return row * U + (u ^ ((row >> SH) & (G - 1))); }
 };
 
-template <int D, int NT>
+template <int D>
 struct TileLds {
-  typedef ManyTile<D, NT> X;
+  typedef ManyTile<D> X;
   uint4 k[2][64 * X::U];
   uint4 v[2][8 * X::DV];        // [16-token block][half][channel]: 8 tokens a unit
   uint32_t mark[2][4 * X::DV];  // [block][channel]: a bit for each token whose value is NaN
@@ -423,9 +423,9 @@ struct TileLds {
   SchedLds sched;
 };
 
-template <int D, int NT, bool WHOLE>
-__device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, const KvSched& d, TileLds<D, NT>& lds) {
-  typedef ManyTile<D, NT> X;
+template <int D, bool WHOLE>
+__device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, const KvSched& d, TileLds<D>& lds) {
+  typedef ManyTile<D> X;
   constexpr int T = X::T, NP = X::NP, QF = D / 16;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int q = lane & 31, hf = lane >> 5, B = 1 << c.lb;
@@ -442,23 +442,20 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
   }
 
   typedef Piece<X::R> P;
-  bf16x8 qf[NT][QF];
+  bf16x8 qf[QF];
   auto load_q = [&](const P& p) {
+    const int r = min(p.t.r0 + wave * 32 + q, p.t.r1), j = r / a.G;
+    const uint16_t* src = a.q + (size_t)(p.s.row0 + j) * a.rs + (size_t)(p.h * a.G + r % a.G) * a.hs + 8 * hf;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = min(p.t.r0 + wave * 32 * NT + 32 * n + q, p.t.r1), j = r / a.G;
-      const uint16_t* src = a.q + (size_t)(p.s.row0 + j) * a.rs + (size_t)(p.h * a.G + r % a.G) * a.hs + 8 * hf;
-#pragma unroll
-      for (int i = 0; i < QF; ++i) {
-        uint4 x{};
-        if (vec) {
-          x = *reinterpret_cast<const uint4*>(src + 16 * i);
-        } else {
-          auto two = [&](int e) { return src[16 * i + e] | (uint32_t)src[16 * i + e + 1] << 16; };
-          x = uint4{two(0), two(2), two(4), two(6)};
-        }
-        qf[n][i] = __builtin_bit_cast(bf16x8, x);
+    for (int i = 0; i < QF; ++i) {
+      uint4 x{};
+      if (vec) {
+        x = *reinterpret_cast<const uint4*>(src + 16 * i);
+      } else {
+        auto two = [&](int e) { return src[16 * i + e] | (uint32_t)src[16 * i + e + 1] << 16; };
+        x = uint4{two(0), two(2), two(4), two(6)};
       }
+      qf[i] = __builtin_bit_cast(bf16x8, x);
     }
   };
   // Page and scales of this wave's block, one for all its lanes, come by
@@ -501,25 +498,18 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     const bool have_next = pieces.next(next);
     int next_id = 0;
     if (have_next) ids(next, next.t.step0 + next.s0, next_id);
-    const int w0 = t.r0 + wave * 32 * NT;  // the wave's rows
+    const int w0 = t.r0 + wave * 32;  // the wave's rows
     const bool active = w0 <= t.r1;
-    Span mine[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) mine[n] = row_span(c, a, s, min(w0 + 32 * n + q, t.r1) / a.G);
+    const Span mine = row_span(c, a, s, min(w0 + q, t.r1) / a.G);
     // what all and what some of the wave's rows see
-    const Span wa = row_span(c, a, s, min(w0, t.r1) / a.G), wb = row_span(c, a, s, min(w0 + 32 * NT - 1, t.r1) / a.G);
+    const Span wa = row_span(c, a, s, min(w0, t.r1) / a.G), wb = row_span(c, a, s, min(w0 + 31, t.r1) / a.G);
 
-    f32x16 o[NT][T];
-    float M[NT], L[NT];
+    f32x16 o[T];
+    float M = -kInf, L = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      M[n] = -kInf;
-      L[n] = 0.f;
+    for (int i = 0; i < T; ++i)
 #pragma unroll
-      for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[n][i][e] = 0.f;
-    }
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
 
     auto split = [&](int step) {  // rows differ in what they see of it
       return step * kKvStep < t.every_lo || (step + 1) * kKvStep > t.every_hi;
@@ -579,7 +569,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
     for (int step = begin; step < end; ++step) {
       const int buf = (step - begin) & 1, base = step * kKvStep;
       const bool run = active && base < wb.hi && base + kKvStep > wa.lo;
-      f32x16 st[2][NT];
+      f32x16 st[2];
       // The next step's codes go into the other buffer beside the products
       // (after the last step the old ones do, which nobody reads).
       if (step + 1 < end) mark(step + 1, buf ^ 1);
@@ -587,9 +577,7 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) st[x][n][e] = 0.f;
+          for (int e = 0; e < 16; ++e) st[x][e] = 0.f;
         // Two chains of products.  Reads from LDS run kAhead products ahead of
         // their use and the order is fixed (left alone, the compiler puts each
         // read right before its product, which then waits for it).
@@ -601,10 +589,8 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
 #pragma unroll
           for (int g = 0; g < 2 * QF; ++g) {
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              st[g & 1][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g % kAhead]),
-                                                                     qf[n][g >> 1], st[g & 1][n], 0, 0, 0);
+            st[g & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g % kAhead]), qf[g >> 1],
+                                                                st[g & 1], 0, 0, 0);
             if (g + kAhead < 2 * QF) read(g + kAhead);
 #pragma unroll
             for (int j = 4 * NP * g / (2 * QF); j < 4 * NP * (g + 1) / (2 * QF); ++j) store(j, buf ^ 1);
@@ -618,18 +604,15 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
       ids(p, step + 3, id_next);
       if (run) {
         const uint32_t bads = __builtin_amdgcn_readfirstlane(lds.bad[buf]);
+        const int lo = mine.lo - base - 16 * hf, hi = mine.hi - base - 16 * hf;
         if (bads != 0 || base < wb.lo || base + kKvStep > wa.hi) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+          for (int x = 0; x < 2; ++x) {
+            const bool none = (bads >> (8 * (2 * x + hf))) & 1;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const bool none = (bads >> (8 * (2 * x + hf))) & 1;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (none) st[x][n][e] = __builtin_nanf("");
-                if (32 * x + e < lo || 32 * x + e >= hi) st[x][n][e] = -kInf;
-              }
+            for (int e = 0; e < 16; ++e) {
+              if (none) st[x][e] = __builtin_nanf("");
+              if (32 * x + e < lo || 32 * x + e >= hi) st[x][e] = -kInf;
             }
           }
         }
@@ -637,71 +620,53 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
           // the rows that see a marked value: a product of their view (ones)
           // with the marks (ones)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int lo = mine[n].lo - base - 16 * hf, hi = mine[n].hi - base - 16 * hf;
+          for (int i = 0; i < T; ++i) {
+            f32x16 hit;
 #pragma unroll
-            for (int i = 0; i < T; ++i) {
-              f32x16 hit;
+            for (int e = 0; e < 16; ++e) hit[e] = 0.f;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) hit[e] = 0.f;
+            for (int x = 0; x < 2; ++x) {
+              const int ch = 32 * i + q;
+              const uint32_t mark = ch < D ? lds.mark[buf][(2 * x + hf) * X::DV + ch] : 0;
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int ch = 32 * i + q;
-                const uint32_t mark = ch < D ? lds.mark[buf][(2 * x + hf) * X::DV + ch] : 0;
+              for (int u = 0; u < 2; ++u) {
+                uint32_t see[4], at[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  uint32_t see[4], at[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int b = 8 * u + 2 * k, e = 32 * x + b;
-                    see[k] = (e >= lo && e < hi ? 0x3f80u : 0u) | (e + 1 >= lo && e + 1 < hi ? 0x3f800000u : 0u);
-                    at[k] = (mark >> b & 1 ? 0x3f80u : 0u) | (mark >> (b + 1) & 1 ? 0x3f800000u : 0u);
-                  }
-                  hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(at[0], at[1], at[2], at[3]),
-                                                                frag(see[0], see[1], see[2], see[3]), hit, 0, 0, 0);
+                for (int k = 0; k < 4; ++k) {
+                  const int b = 8 * u + 2 * k, e = 32 * x + b;
+                  see[k] = (e >= lo && e < hi ? 0x3f80u : 0u) | (e + 1 >= lo && e + 1 < hi ? 0x3f800000u : 0u);
+                  at[k] = (mark >> b & 1 ? 0x3f80u : 0u) | (mark >> (b + 1) & 1 ? 0x3f800000u : 0u);
                 }
+                hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(at[0], at[1], at[2], at[3]),
+                                                              frag(see[0], see[1], see[2], see[3]), hit, 0, 0, 0);
               }
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (hit[e] > 0.f) o[n][i][e] = __builtin_nanf("");
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (hit[e] > 0.f) o[i][e] = __builtin_nanf("");
           }
         }
-        float mx[NT];
-        bool up = false;
+        float mx = fmaxf(st[0][0], st[1][0]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float m = fmaxf(st[0][n][0], st[1][n][0]);
+        for (int e = 1; e < 16; ++e) mx = fmaxf(fmaxf(mx, st[0][e]), st[1][e]);
+        mx = max_halves(mx);
+        if (__ballot(mx > M + slack)) {
+          const float Mn = fmaxf(M, mx);
+          const float f = Mn == M ? 1.f : __builtin_amdgcn_exp2f((M - Mn) * cs);
+          M = Mn;
+          L *= f;
 #pragma unroll
-          for (int e = 1; e < 16; ++e) m = fmaxf(fmaxf(m, st[0][n][e]), st[1][n][e]);
-          mx[n] = max_halves(m);
-          up |= mx[n] > M[n] + slack;
-        }
-        if (__ballot(up)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float Mn = fmaxf(M[n], mx[n]);
-            const float f = Mn == M[n] ? 1.f : __builtin_amdgcn_exp2f((M[n] - Mn) * cs);
-            M[n] = Mn;
-            L[n] *= f;
-#pragma unroll
-            for (int i = 0; i < T; ++i) o[n][i] *= f;
-          }
+          for (int i = 0; i < T; ++i) o[i] *= f;
         }
         // Group c of 8 tokens: its probabilities, then its products, beside which
         // the next group's probabilities are made, and the reads as above.
         {
-          static_assert(NT == 1);
-          const Ref ref(M[0], cs);
-          uint32_t pw[NT][2][4];  // groups c and c + 1
+          const Ref ref(M, cs);
+          uint32_t pw[2][4];  // groups c and c + 1
           auto prob = [&](int c, int e) {  // tokens 2 e and 2 e + 1 of group c
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float p0 = ref.p(st[c >> 1][n][8 * (c & 1) + 2 * e]);
-              const float p1 = ref.p(st[c >> 1][n][8 * (c & 1) + 2 * e + 1]);
-              L[n] += p0 + p1;
-              pw[n][c & 1][e] = pack_bf2_hw(p0, p1);
-            }
+            const float p0 = ref.p(st[c >> 1][8 * (c & 1) + 2 * e]), p1 = ref.p(st[c >> 1][8 * (c & 1) + 2 * e + 1]);
+            L += p0 + p1;
+            pw[c & 1][e] = pack_bf2_hw(p0, p1);
           };
           uint4 vf[kAhead];
           auto read = [&](int g) {
@@ -718,11 +683,9 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
             for (int i = 0; i < T; ++i) {
               const int g = c * T + i;
               __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, vf[g % kAhead]),
-                    frag(pw[n][c & 1][0], pw[n][c & 1][1], pw[n][c & 1][2], pw[n][c & 1][3]), o[n][i], 0, 0, 0);
+              o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8, vf[g % kAhead]),
+                  frag(pw[c & 1][0], pw[c & 1][1], pw[c & 1][2], pw[c & 1][3]), o[i], 0, 0, 0);
               if (g + kAhead < 4 * T) read(g + kAhead);
               if (c < 3)
 #pragma unroll
@@ -741,45 +704,41 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
       load_q(next);
     }
     const int Hq = c.H * a.G;
+    const float l = sum_halves(L);
+    const int row = wave * 32 + q, rr = t.r0 + row;
+    const bool there = rr <= t.r1;  // (the same in both lanes of a row)
+    if (there && slot >= 0) {
+      float* dst = sched_slot(a.work, slot, X::R, D);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float l = sum_halves(L[n]);
-      const int row = wave * 32 * NT + 32 * n + q, rr = t.r0 + row;
-      if (rr > t.r1) continue;  // (both lanes of a row)
-      if (slot >= 0) {
-        float* dst = sched_slot(a.work, slot, X::R, D);
+      for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int e = 0; e < 16; e += 4) {
+          const int ch = 32 * i + 2 * e + 4 * hf;
+          if (ch < D)
+            *reinterpret_cast<f32x4*>(dst + row * D + ch) = f32x4{o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]};
+        }
+      if (hf == 0) dst[X::R * D + row] = M * cs, dst[X::R * D + X::R + row] = l;
+    } else if (there) {
+      // The two halves of the wave hold four channels in turn; they change
+      // places so that a lane has eight in a row: half as many stores.
+      const float inv = mine.hi > mine.lo ? 1.f / l : 0.f;
+      uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + 8 * hf;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const int ch = 32 * i + 2 * e + 4 * hf;
-            if (ch < D)
-              *reinterpret_cast<f32x4*>(dst + row * D + ch) =
-                  f32x4{o[n][i][e], o[n][i][e + 1], o[n][i][e + 2], o[n][i][e + 3]};
-          }
-        if (hf == 0) dst[X::R * D + row] = M[n] * cs, dst[X::R * D + X::R + row] = l;
-      } else {
-        // The two halves of the wave hold four channels in turn; they change
-        // places so that a lane has eight in a row: half as many stores.
-        const float inv = mine[n].hi > mine[n].lo ? 1.f / l : 0.f;
-        uint16_t* dst = a.out + ((size_t)(s.row0 + rr / a.G) * Hq + h * a.G + rr % a.G) * D + 8 * hf;
+      for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int e = 0; e < 16; e += 8)
+          if (32 * i + 2 * e < D) {
+            uint32_t x[4];
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            if (32 * i + 2 * e < D) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const auto z = __builtin_amdgcn_permlane32_swap(
-                    pack_bf2_hw(o[n][i][e + 2 * k] * inv, o[n][i][e + 2 * k + 1] * inv),
-                    pack_bf2_hw(o[n][i][e + 4 + 2 * k] * inv, o[n][i][e + 5 + 2 * k] * inv), false, false);
-                x[k] = z[0];
-                x[2 + k] = z[1];
-              }
-              *reinterpret_cast<uint4*>(dst + 32 * i + 2 * e) = uint4{x[0], x[1], x[2], x[3]};
+            for (int k = 0; k < 2; ++k) {
+              const auto z = __builtin_amdgcn_permlane32_swap(
+                  pack_bf2_hw(o[i][e + 2 * k] * inv, o[i][e + 2 * k + 1] * inv),
+                  pack_bf2_hw(o[i][e + 4 + 2 * k] * inv, o[i][e + 5 + 2 * k] * inv), false, false);
+              x[k] = z[0];
+              x[2 + k] = z[1];
             }
-      }
+            *reinterpret_cast<uint4*>(dst + 32 * i + 2 * e) = uint4{x[0], x[1], x[2], x[3]};
+          }
     }
     p = next;
     have = have_next;
@@ -793,10 +752,10 @@ __global__ __launch_bounds__(64 * kWaves, RowsTile<D>::PER_CU) void kv_rows_kern
   rows_part<D, WHOLE>(c, a, d, lds);
 }
 
-template <int D, int NT, bool WHOLE>
-__global__ __launch_bounds__(256, (ManyTile<D, NT>::PER_CU)) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
-  __shared__ TileLds<D, NT> lds;
-  tile_part<D, NT, WHOLE>(c, a, d, lds);
+template <int D, bool WHOLE>
+__global__ __launch_bounds__(256, ManyTile<D>::PER_CU) void kv_tile_kernel(KvView c, KvAttn a, KvSched d) {
+  __shared__ TileLds<D> lds;
+  tile_part<D, WHOLE>(c, a, d, lds);
 }
 
 template <int R, int D>
@@ -838,9 +797,9 @@ size_t tile_bytes(int D) { return (sched_bytes(tile_workers(D), 128, D) + 255) /
 // is launched unless the batch cannot hold a sequence for it.
 template <int D>
 hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
-  constexpr int NT = 1, R = ManyTile<D, NT>::R;
+  constexpr int R = ManyTile<D>::R;
   constexpr int rw = rows_workers(D), tw = tile_workers(D);
-  static_assert(rw == 256 * RowsTile<D>::PER_CU && tw == 256 * ManyTile<D, NT>::PER_CU);
+  static_assert(rw == 256 * RowsTile<D>::PER_CU && tw == 256 * ManyTile<D>::PER_CU);
   const int64_t rows = (int64_t)c.max_new * a.G, heads = (int64_t)c.n_seq * c.H;
   const bool many = rows > kFewRows;
   // Whether sequences of few rows are left to the few-row form.  In a batch of
@@ -859,14 +818,14 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
       MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, true>), dim3((unsigned)(few_tiles * heads)), dim3(64 * kWaves), 0,
                    stream, c, a, fd);
     if (many)
-      MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT, true>), dim3((unsigned)(tiles * heads)), dim3(256), 0, stream, c,
+      MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, true>), dim3((unsigned)(tiles * heads)), dim3(256), 0, stream, c,
                    a, td);
     return launched();
   }
   KvAttn fa = a;
   if (many) fa.work = static_cast<char*>(a.work) + tile_bytes(D);
   if (few) MLORA_LAUNCH("kv_rows", (kv_rows_kernel<D, false>), dim3(rw), dim3(64 * kWaves), 0, stream, c, fa, fd);
-  if (many) MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, NT, false>), dim3(tw), dim3(256), 0, stream, c, a, td);
+  if (many) MLORA_LAUNCH("kv_tiles", (kv_tile_kernel<D, false>), dim3(tw), dim3(256), 0, stream, c, a, td);
   if (few && many)
     MLORA_LAUNCH("kv_join", (kv_join_both_kernel<R, D>), dim3(tw + rw, 8), dim3(256), 0, stream, c, a, tw, fa, rw);
   else if (many)
