@@ -101,10 +101,14 @@ template <int D>
 struct RowsTile {
   static constexpr int R = (D + 63) / 64;  // 16-byte loads of a lane for a token's keys
   static constexpr int T = D / 16;         // channel tiles of the output
-  // workgroups of a CU: at 256 channels the registers of two would not hold the
-  // output (64 sequences of 500 .. 4000 tokens: 93 us with two, 64 us with one;
-  // at 192 channels 46 and 49 us)
-  static constexpr int PER_CU = D > 192 ? 1 : 2;
+  // Workgroups of a CU.  In the form of parts the registers of two hold neither
+  // the output nor the next step's loads above 128 channels (256 requests of
+  // 1000 .. 8000 tokens: 606 us with one, 790 us with two at 192 channels, 516
+  // and 554 us at 160; 64 sequences of 500 .. 4000 at 256: 60 and 99 us).  Whole
+  // items, which carry no parts, do better with two up to 192 channels (window
+  // of 1024 over 96 sequences: 29.6 us with two, 32.1 us with one; at 160 23.4
+  // and 28.8 us).
+  static constexpr int PER_CU = D > 128 ? 1 : 2, WHOLE_PER_CU = D > 192 ? 1 : 2;
 };
 
 // Loads of the next step are issued as soon as the registers they go to have
@@ -747,7 +751,8 @@ __device__ __forceinline__ void tile_part(const KvView& c, const KvAttn& a, cons
 }
 
 template <int D, bool WHOLE>
-__global__ __launch_bounds__(64 * kWaves, RowsTile<D>::PER_CU) void kv_rows_kernel(KvView c, KvAttn a, KvSched d) {
+__global__ __launch_bounds__(64 * kWaves, WHOLE ? RowsTile<D>::WHOLE_PER_CU : RowsTile<D>::PER_CU) void kv_rows_kernel(
+    KvView c, KvAttn a, KvSched d) {
   __shared__ RowsLds<D> lds;
   rows_part<D, WHOLE>(c, a, d, lds);
 }
@@ -771,7 +776,7 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
     join_part<16, D>(c, few_a, few_workers, blockIdx.x - workers);
 }
 
-constexpr int rows_workers(int D) { return D > 192 ? 256 : 512; }
+constexpr int rows_workers(int D) { return D > 128 ? 256 : 512; }
 constexpr int tile_workers(int D) { return D > 128 ? 256 : 512; }
 // A chunk of 2048 tokens: workgroups 0 .. 255 end at 627 us and the others at
 // 768 us with equal parts; at 24 / 256 both ends meet (620 -> 604 us).
