@@ -380,9 +380,10 @@ __device__ __forceinline__ void rows_part(const KvView& c, const KvAttn& a, cons
 // which are its probabilities in the second product.
 //
 // A chunk of 2048 tokens over 16301 cached ones (32 query heads on 8, 128
-// channels, 581 GFLOP) takes 605 us, 960 TFLOP/s, where a library product of
-// 8192^3 reaches 1200; the clock is down to 2.1 GHz by then (matrix pipes busy
-// for 40 % of its cycles), so what makes the loop denser gives little time.
+// channels, 581 GFLOP) takes 605 .. 620 us, 940 .. 960 TFLOP/s, where a library
+// product of 8192^3 reaches 1200.  Under the counters the clock is down to 1.9
+// GHz and the matrix pipes are busy for 45 % of its cycles: what makes the loop
+// denser gives little time.
 // 64 rows a wave halve the reads from LDS, but take all registers of a SIMD
 // for one wave: 894 us when 32 rows took 736.
 // ----------------------------------------------------------------------------
@@ -779,14 +780,16 @@ __global__ __launch_bounds__(256) void kv_join_both_kernel(KvView c, KvAttn a, i
 constexpr int rows_workers(int D) { return D > 128 ? 256 : 512; }
 constexpr int tile_workers(int D) { return D > 128 ? 256 : 512; }
 // A chunk of 2048 tokens: workgroups 0 .. 255 end at 627 us and the others at
-// 768 us with equal parts; at 24 / 256 both ends meet (620 -> 604 us).
+// 768 us with equal parts; at 24 / 256 both ends meet (643 -> 633 us).
 constexpr int kSkew = 24;
 // 32 sequences of 20 rows: 51 us in the many-row form, 53 us as two 16-row tiles.
 constexpr int kFewRows = 16;
 // Up to this many steps an item goes to a workgroup whole: no parts to find, no
-// pieces to join, and the hardware deals the items.  8 prompts of 240 .. 890
-// tokens: 64 us in parts, 48 us whole; over a hundred batches of all kinds the
-// time over the floor is 2.19 / 2.18 / 2.48 times at 12 / 20 / 32 steps.
+// pieces to join, and the hardware deals the items.  4 short requests 17.5 us in
+// parts, 8.2 us whole; 8 prompts of 240 .. 890 tokens 64 and 49 us; 18 steps (a
+// window of 1024, 96 sequences) 22 and 12 us.  Over 120 batches of all kinds the
+// time over the floor is 3.6 times with parts alone and 2.26 .. 2.29 at 12, 20
+// and 32 steps: past 20 single batches gain or lose up to half.
 constexpr int kWholeSteps = 20;
 
 // Steps of an item at most, as far as the host can tell.
@@ -810,8 +813,8 @@ hipError_t launch_dim(const KvView& c, const KvAttn& a, hipStream_t stream) {
   // Whether sequences of few rows are left to the few-row form.  In a batch of
   // few sequences with more rows than that on average (prompts, drafts) the
   // many-row form takes them along, which saves a launch that may find nothing:
-  // 8 prompts 70 -> 65 us, 2 prompts with 6 single rows 81 -> 72 us, a chunk
-  // of 1024 with 8 single rows 144 -> 139 us.
+  // 8 drafts of 3 .. 9 rows 44 -> 27 us, 8 prompts 51 -> 50 us, 2 prompts with 6
+  // single rows 84 -> 75 us, a chunk of 1024 with 8 single rows 143 -> 138 us.
   const bool few = !many || (c.n_rows < (int64_t)c.max_new * c.n_seq &&
                              (c.n_seq > 16 || (int64_t)c.n_rows * a.G < kFewRows * (int64_t)c.n_seq));
   const int64_t few_tiles = (std::min<int64_t>(rows, kFewRows) + 15) / 16, tiles = (rows + R - 1) / R;

@@ -2,11 +2,12 @@
 // back.  Both are bound by memory traffic (2 bytes a channel on the bf16
 // side, 1 on the cache's) and, for a decode step, by the latency of a launch
 // with a few dependent loads (row_off -> table -> page):
-//   one new token of 256 requests (8 heads of 128 channels) written in 4.6 us,
-//   the 2200 tokens of the pages read back in 7.4 us;
-//   4238 tokens of 8 prompts written in 12 us (26 MB);
+//   one new token of 256 requests (8 heads of 128 channels) written in 4.7 us
+//   (5.8 .. 6.3 us between a layer's projections), the 2265 tokens of the pages
+//   read back in 8.7 us;
+//   6451 tokens of 8 prompts written in 13 us (40 MB, 3.1 TB/s);
 //   32768 tokens read back in 44 us from memory (201 MB, 4.6 TB/s; a plain copy
-//   reaches 5.1) and 31 us from the last-level cache;
+//   reaches 5.2) and 32 us from the last-level cache;
 //   64 histories of 1 .. 1500 tokens, 80 channels, in 17 us (5.4 TB/s).
 //
 // A page of one head, keys or values, is written by the waves of one
@@ -149,8 +150,8 @@ __device__ __forceinline__ Scale new_scale(uint32_t amax, bool kept, float was) 
 }
 
 // One new row of each sequence: a wave takes it for one head, keys or values,
-// a lane 2 * NC channels (9 us by the kernel for pages, 4.6 us by this one: 256
-// rows, 8 heads).  What bounds it is the chain of dependent loads
+// a lane 2 * NC channels (10.4 us by the kernel for pages, 4.7 us by this one:
+// 256 rows, 8 heads).  What bounds it is the chain of dependent loads
 // (kv_len -> table -> scale), so nothing else waits: the row is on its way
 // before the table's entry is looked at.
 template <bool VEC, int NC>
@@ -481,8 +482,9 @@ hipError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, hipStream_t
   const bool single = c.max_new == 1;
   const int items = item_count(c, 4, single), full = std::max(1, c.H * c.D / kThreads);
   // A unit a thread where all workgroups run at once, and where there are many
-  // rounds of them anyway (32768 tokens 31 us, 33 us with four units a thread);
-  // in between as many as fill one round (256 requests' pages 8.5 -> 7.4 us).
+  // rounds of them anyway (32768 tokens 36.4 us, 39.0 us with four units a
+  // thread); in between as many as fill one round (pages of 256 requests 8.8 us,
+  // 10.0 us with a unit a thread, 9.6 us with four).
   const int split = items > kReadGroups ? full : std::min(full, kReadGroups / items);
   MLORA_LAUNCH("kv_read", kv_read_kernel, dim3(items, split), dim3(kThreads), 0, stream, c, k, v, single);
   return launched();
