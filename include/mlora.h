@@ -516,6 +516,119 @@ mlora_status mlora_kv_attention(const mlora_kv_cache* cache, int32_t layer, cons
                                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * 4-bit base weights: the base weight W0 of the layer in 4 bits, the adapters
+ * on top of it as they are.
+ *
+ * A weight is an e2m1 code (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6) times
+ * the scale of its group of 32 consecutive input channels of a row, a power of
+ * two: scale byte b stands for 2^(b - 127), 2 <= b <= 252; a group with any
+ * other byte is NaN.  bf16 holds every weight exactly, and products with it
+ * are those of the bf16 weight (fp32 accumulation).
+ *   codes:  device uint8 [dout][din/2], channel 2i in the lower half of byte i,
+ *           16-byte aligned
+ *   scales: device uint8 [dout][din/32]
+ * both caller-owned and densely packed.
+ * ------------------------------------------------------------------------- */
+typedef struct mlora_q4_weight {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int32_t din;  /* a multiple of 32, at most 2^20 */
+  int32_t dout; /* 1 .. 2^24                      */
+} mlora_q4_weight;
+
+/* W (device bf16 [dout][din], 16-byte aligned) to codes and scales: the least
+ * scale whose 6 covers the group, each weight to the nearest code, halfway
+ * values to the even one.  Groups of zeros take b = 2; a group that holds an
+ * infinity or NaN takes b = 255; weights beyond 6 * 2^125 become that. */
+mlora_status mlora_q4_quantize(const uint16_t* W, int32_t dout, int32_t din, uint8_t* codes, uint8_t* scales,
+                               void* stream);
+/* The weight as bf16: W device bf16 [dout][din], 16-byte aligned. */
+mlora_status mlora_q4_dequantize(const mlora_q4_weight* w, uint16_t* W, void* stream);
+
+/* Y = X W^T for X device bf16 [n_rows][din] and Y device bf16 [n_rows][dout],
+ * X 16-byte aligned; and the whole layer, mlora_apply with W for W0 (seg_ws,
+ * proj and n_rows as there, pool of the weight's din and dout).
+ *   work: device scratch of mlora_q4_work_bytes(w, pool, n_rows) bytes (pool
+ *         NULL for mlora_q4_gemm), 256-byte aligned, contents free; calls
+ *         that share it must not overlap.
+ * Few rows multiply the codes as they are; more rows make the weight bf16 in
+ * `work` first.  Results are the same bit for bit from call to call. */
+size_t mlora_q4_work_bytes(const mlora_q4_weight* w, const mlora_pool* pool, int32_t n_rows);
+mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t* Y, int32_t n_rows, void* work,
+                           size_t work_bytes, void* stream);
+mlora_status mlora_q4_apply(const mlora_pool* pool, int32_t proj, const uint16_t* X, const mlora_q4_weight* w,
+                            const void* seg_ws, uint16_t* Y, int32_t n_rows, void* work, size_t work_bytes,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys and the rotation of their positions, in one pass:
+ * what comes between the joint projection and the cache.
+ *
+ * For each head x of a row (dim channels, a multiple of 16 up to 256):
+ *   x <- weight * x / sqrt(mean(x^2) + eps)           where weight is given
+ *   (a, b) <- factor * (a cos t - b sin t, a sin t + b cos t)
+ * for the rot / 2 pairs of the first rot channels, t = position * freq_i for
+ * pair i, made of channels i and i + rot / 2, or 2i and 2i + 1 (interleaved).
+ * The other channels keep what the norm gave.  fp32 throughout, rounded once;
+ * the angle is exact modulo a revolution at every position.
+ * Positions are those of the batch's rows (kv_len - m + j, see above); of the
+ * batch only kv_len, row_off, n_seq and n_rows are used.  Rows past the last
+ * sequence are left as they are.
+ *   freq: device uint64 [rot/2], revolutions per position times 2^64
+ *   rot:  a multiple of 8 up to dim
+ * The output may be the input itself (same pointer and strides), else it must
+ * not overlap any input or the other output.
+ * ------------------------------------------------------------------------- */
+typedef struct mlora_rotary {
+  const uint64_t* freq;
+  int32_t rot;
+  int32_t interleaved;
+  float factor;
+} mlora_rotary;
+
+typedef struct mlora_head_rows {
+  const uint16_t* x;       /* device bf16: channel c of head h of row r at r * row_stride + h * head_stride + c */
+  uint16_t* y;             /* device bf16, with the out_ strides             */
+  int64_t row_stride, head_stride, out_row_stride, out_head_stride;
+  const uint16_t* weight;  /* device bf16 [dim], or NULL: no norm            */
+  int32_t heads;           /* 1 .. 1024                                      */
+} mlora_head_rows;
+
+/* q and k: either may be NULL, not both. */
+mlora_status mlora_qk_norm_rotary(const mlora_kv_batch* batch, int32_t dim, const mlora_rotary* rotary,
+                                  const mlora_head_rows* q, const mlora_head_rows* k, float eps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Sampling: one token a row from its logits l and a random number u.
+ *
+ * With T = temperature, w_i = exp((l_i - max l) / T) (held to 2^-42).  The
+ * tokens stand in the order of falling logits, the lower index first.  Of
+ * these the first top_k are kept; of those the shortest beginning that holds
+ * top_p of their weight, one token at least; of those the ones with w >=
+ * min_p.  The result is the first kept token at which the running weight
+ * exceeds u times the weight kept.
+ *   logits:      device bf16 or fp32 (is_f32) [n_rows][vocab], row_stride
+ *                elements apart, vocab 1 .. 2^20
+ *   u:           device float [n_rows] in [0, 1) (values outside are clamped)
+ *   temperature: device float [n_rows]; 0 or less (or NaN) takes the first of
+ *                the largest logits.  NULL: 1 for every row
+ *   top_k:       device int32 [n_rows], 0 or less: all tokens.  NULL: all
+ *   top_p:       device float [n_rows], 1 or more (or NaN): all.  NULL: all
+ *   min_p:       device float [n_rows], 0 or less (or NaN): all.  NULL: all
+ *   out:         device int32 [n_rows]
+ *   work:        device scratch of mlora_sample_work_bytes() bytes, 256-byte
+ *                aligned, contents free; calls that share it must not overlap
+ * NaN logits count as -infinity; where the largest is +infinity, the tokens
+ * that have it share the weight; a row without any logit above -infinity
+ * gives -1.  Sums are exact, so the result does not depend on their order.
+ * ------------------------------------------------------------------------- */
+#define MLORA_MAX_VOCAB (1 << 20)
+size_t mlora_sample_work_bytes(int32_t n_rows, int32_t vocab);
+mlora_status mlora_sample(const void* logits, int32_t is_f32, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                          const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* out, void* work, size_t work_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement helpers: a plain streaming copy (dst = src, `bytes` a multiple
  * of 16, both 16-byte aligned), used to calibrate achievable HBM bandwidth
  * and hardware byte counters against a kernel of known traffic.

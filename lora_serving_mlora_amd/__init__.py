@@ -18,6 +18,13 @@ and, for the attention between a layer's projections::
     batch = KVBatch(table, kv_len, row_off, n_rows, max_new=max_new)   # device int32 tensors
     kv_append(cache, layer, k, v, batch)
     O = kv_attention(cache, layer, q, batch)                           # device bf16
+
+with a base weight in 4 bits, norms and rotation of the heads, and the next tokens::
+
+    w4 = q4_quantize(W0)
+    Y = q4_apply(pool, proj, X, w4, seg)                               # as apply, with w4 for W0
+    q, k = qk_norm_rotary(q, k, batch, Rotary(dim), q_weight=qw, k_weight=kw)
+    tokens = sample(logits, u, temperature=t, top_k=k, top_p=p, min_p=m)
 """
 from __future__ import annotations
 
@@ -32,6 +39,8 @@ __all__ = [
     "base_gemm", "shrink", "shrink_max_chunks", "expand", "fused", "shrink_rows", "gemm_lora", "new_work", "rows_t", "apply", "forward", "plan", "work_bytes",
     "forward_static", "STATIC_SCRATCH_BYTES", "merge", "hbm_copy", "hbm_read", "hbm_read_lds", "timing_arm", "timing_read", "VARIANTS", "ITEM_ROWS", "TILE_ROWS", "MAX_ROWS", "MAX_RANK", "SEG", "EXPORTS", "LIB_PATH",
     "KVCache", "KVBatch", "kv_append", "kv_read", "kv_attention", "kv_work_bytes", "new_kv_work",
+    "Q4Weight", "q4_quantize", "q4_dequantize", "q4_gemm", "q4_apply", "q4_work_bytes", "new_q4_work",
+    "Rotary", "qk_norm_rotary", "sample", "sample_work_bytes", "new_sample_work",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmlora.so")
@@ -64,6 +73,19 @@ class _KVCacheDesc(ctypes.Structure):
 class _KVBatchDesc(ctypes.Structure):
     _fields_ = [("table", _c_void_p), ("kv_len", _c_void_p), ("row_off", _c_void_p), ("n_seq", _i32), ("width", _i32),
                 ("table_stride", _i32), ("n_rows", _i32), ("max_new", _i32)]
+
+
+class _Q4Desc(ctypes.Structure):
+    _fields_ = [("codes", _c_void_p), ("scales", _c_void_p), ("din", _i32), ("dout", _i32)]
+
+
+class _RotaryDesc(ctypes.Structure):
+    _fields_ = [("freq", _c_void_p), ("rot", _i32), ("interleaved", _i32), ("factor", _f32)]
+
+
+class _HeadRows(ctypes.Structure):
+    _fields_ = [("x", _c_void_p), ("y", _c_void_p), ("row_stride", _i64), ("head_stride", _i64),
+                ("out_row_stride", _i64), ("out_head_stride", _i64), ("weight", _c_void_p), ("heads", _i32)]
 
 
 # name -> (restype, argtypes); every symbol include/mlora.h declares
@@ -106,6 +128,16 @@ EXPORTS = {
     "mlora_kv_work_bytes": (_sz, [_c_void_p, _c_void_p, _i32]),
     "mlora_kv_attention": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _i64, _i64, _i32, _c_void_p, _i32, _i32, _f32,
                                           _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "mlora_q4_quantize": (ctypes.c_int, [_c_void_p, _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "mlora_q4_dequantize": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p]),
+    "mlora_q4_work_bytes": (_sz, [_c_void_p, _c_void_p, _i32]),
+    "mlora_q4_gemm": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _sz, _c_void_p]),
+    "mlora_q4_apply": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p,
+                                      _sz, _c_void_p]),
+    "mlora_qk_norm_rotary": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _f32, _c_void_p]),
+    "mlora_sample_work_bytes": (_sz, [_i32, _i32]),
+    "mlora_sample": (ctypes.c_int, [_c_void_p, _i32, _i64, _i32, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
     "mlora_hbm_copy": (ctypes.c_int, [_c_void_p, _c_void_p, _sz, _c_void_p]),
     "mlora_hbm_read": (ctypes.c_int, [_c_void_p, _sz, _c_void_p, _c_void_p]),
     "mlora_hbm_read_lds": (ctypes.c_int, [_c_void_p, _sz, _c_void_p, _c_void_p]),
@@ -653,6 +685,247 @@ def kv_attention(cache: KVCache, layer: int, q, batch: KVBatch, causal: bool = T
                                       work.nbytes, _kv_stream(cache))
     if status != OK:
         raise MloraError(status, "mlora_kv_attention")
+    return out
+
+
+def _raw_stream(device: int) -> int:
+    # the handle alone: building a Stream object costs as much as a small launch
+    return _torch()._C._cuda_getCurrentRawStream(device)
+
+
+def _on_device(t, name: str, dtype, device: int, shape=None):
+    """Checks a contiguous tensor of `dtype` on cuda:`device`."""
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _work(work, device: int):
+    if not isinstance(work, _torch().Tensor) or work.get_device() != device or not work.is_contiguous():
+        raise TypeError(f"work must be a contiguous tensor on cuda:{device}")
+    return work
+
+
+class Q4Weight:
+    """A weight [dout][din] in 4 bits: codes uint8 [dout][din / 2], two e2m1
+    codes a byte with the lower half first, and scales uint8 [dout][din / 32],
+    byte b standing for 2^(b - 127) (include/mlora.h).  The tensors are kept,
+    not copied."""
+
+    def __init__(self, codes, scales):
+        torch = _torch()
+        for name, t in (("codes", codes), ("scales", scales)):
+            if (not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_cuda or t.dim() != 2
+                    or not t.is_contiguous()):
+                raise TypeError(f"{name} must be a contiguous uint8 CUDA matrix")
+        self.dout, self.din = codes.shape[0], 2 * codes.shape[1]
+        if self.din < 32 or self.din % 32 or tuple(scales.shape) != (self.dout, self.din // 32):
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not "
+                             "[dout][din / 2] and [dout][din / 32]")
+        if scales.get_device() != codes.get_device():
+            raise ValueError("scales is on another device than codes")
+        self.codes, self.scales = codes, scales
+        self.device_index = codes.get_device()
+        self._d = _Q4Desc(codes.data_ptr(), scales.data_ptr(), self.din, self.dout)
+        self._ref = ctypes.addressof(self._d)
+
+
+def q4_quantize(W) -> Q4Weight:
+    """W, device bf16 [dout][din] with din a multiple of 32, in 4 bits."""
+    torch = _torch()
+    if _bf16_dev(W, "W").dim() != 2 or W.shape[1] < 32 or W.shape[1] % 32:
+        raise ValueError(f"W has shape {tuple(W.shape)}, expected [dout][din], din a multiple of 32")
+    dout, din = W.shape
+    codes = torch.empty((dout, din // 2), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((dout, din // 32), dtype=torch.uint8, device=W.device)
+    _check(lib().mlora_q4_quantize(W.data_ptr(), dout, din, codes.data_ptr(), scales.data_ptr(),
+                                   _raw_stream(W.get_device())), "mlora_q4_quantize")
+    return Q4Weight(codes, scales)
+
+
+def q4_dequantize(w: Q4Weight, out=None):
+    """The weight as bf16 [dout][din] (every 4-bit weight is a bf16 value)."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty((w.dout, w.din), dtype=torch.bfloat16, device=w.codes.device)
+    _on_device(out, "out", torch.bfloat16, w.device_index, (w.dout, w.din))
+    _check(lib().mlora_q4_dequantize(w._ref, out.data_ptr(), _raw_stream(w.device_index)), "mlora_q4_dequantize")
+    return out
+
+
+def _pool_handle(pool: Optional[Pool], w: Q4Weight):
+    if pool is None:
+        return None
+    if (pool.dout, pool.din) != (w.dout, w.din):
+        raise ValueError(f"the weight is [{w.dout}][{w.din}], the pool's projections are [{pool.dout}][{pool.din}]")
+    if pool.meta.get_device() != w.device_index:
+        raise ValueError(f"the pool must be on cuda:{w.device_index}, as the weight is")
+    return pool.handle
+
+
+def q4_work_bytes(w: Q4Weight, n: int, pool: Optional[Pool] = None) -> int:
+    return int(lib().mlora_q4_work_bytes(w._ref, _pool_handle(pool, w), n))
+
+
+def new_q4_work(w: Q4Weight, n: int, pool: Optional[Pool] = None):
+    """A work buffer for q4_gemm of n rows, or with `pool` for q4_apply."""
+    torch = _torch()
+    return torch.empty(max(q4_work_bytes(w, n, pool), 256), dtype=torch.uint8, device=w.codes.device)
+
+
+def _q4_rows(X, w: Q4Weight, Y):
+    torch = _torch()
+    _on_device(X, "X", torch.bfloat16, w.device_index)
+    if X.dim() != 2 or X.shape[1] != w.din:
+        raise ValueError(f"X has shape {tuple(X.shape)}, expected [n][{w.din}]")
+    shape = (X.shape[0], w.dout)
+    if Y is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=X.device)
+    return _on_device(Y, "Y", torch.bfloat16, w.device_index, shape)
+
+
+def q4_gemm(X, w: Q4Weight, Y=None, work=None):
+    """Y = X W^T, X device bf16 [n][din]."""
+    Y = _q4_rows(X, w, Y)
+    n = X.shape[0]
+    work = new_q4_work(w, n) if work is None else _work(work, w.device_index)
+    status = lib().mlora_q4_gemm(w._ref, X.data_ptr(), Y.data_ptr(), n, work.data_ptr(), work.nbytes,
+                                 _raw_stream(w.device_index))
+    if status != OK:
+        raise MloraError(status, "mlora_q4_gemm")
+    return Y
+
+
+def q4_apply(pool: Pool, proj: int, X, w: Q4Weight, seg_ws, Y=None, work=None):
+    """apply() with the base weight in 4 bits: Y = X W^T + each row's delta."""
+    h = _pool_handle(pool, w)
+    Y = _q4_rows(X, w, Y)
+    n = X.shape[0]
+    _on_device(seg_ws, "seg_ws", _torch().int32, w.device_index)
+    if seg_ws.nbytes < segments_bytes(n):
+        raise ValueError("seg_ws too small")
+    work = new_q4_work(w, n, pool) if work is None else _work(work, w.device_index)
+    status = lib().mlora_q4_apply(h, proj, X.data_ptr(), w._ref, seg_ws.data_ptr(), Y.data_ptr(), n, work.data_ptr(),
+                                  work.nbytes, _raw_stream(w.device_index))
+    if status != OK:
+        raise MloraError(status, "mlora_q4_apply")
+    return Y
+
+
+class Rotary:
+    """Frequencies of a rotation of the first `dim` channels of a head, on the
+    current device.  Pair i turns by position * freqs[i] radians; freqs
+    defaults to base^(-2i / dim).  A pair is made of channels i and
+    i + dim / 2, or 2i and 2i + 1 (interleaved); the rotated pairs are
+    multiplied by `factor`."""
+
+    def __init__(self, dim: int, base: float = 10000.0, freqs=None, interleaved: bool = False, factor: float = 1.0):
+        torch = _torch()
+        if dim < 8 or dim % 8:
+            raise ValueError(f"Rotary: dim {dim} is not a positive multiple of 8")
+        if freqs is None:
+            freqs = base ** (-2.0 * np.arange(dim // 2) / dim)
+        elif isinstance(freqs, torch.Tensor):
+            freqs = freqs.detach().cpu().double().numpy()
+        freqs = np.asarray(freqs, np.float64)
+        if freqs.shape != (dim // 2,) or not np.isfinite(freqs).all():
+            raise ValueError(f"Rotary: freqs must be {dim // 2} finite numbers")
+        turns = freqs / (2 * np.pi)
+        # revolutions modulo 1 in 64-bit fixed point (a float64 fraction has at most 53 significant bits)
+        fixed = [int(t * 2.0 ** 64) % (1 << 64) for t in (turns - np.floor(turns)).tolist()]
+        self.dim, self.interleaved, self.factor = dim, bool(interleaved), float(factor)
+        self.freq = torch.from_numpy(np.array(fixed, np.uint64).view(np.int64)).to(
+            torch.device("cuda", torch.cuda.current_device()))
+        self.device_index = self.freq.get_device()
+        self._d = _RotaryDesc(self.freq.data_ptr(), dim, int(self.interleaved), self.factor)
+        self._ref = ctypes.addressof(self._d)
+
+
+def _head_rows(x, name: str, n: int, weight, out, device: int, dim: int):
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() != device:
+        raise TypeError(f"{name} must be a bfloat16 tensor on cuda:{device}, as the batch is")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{n}][heads][{dim}]")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    elif not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.get_device() != device:
+        raise TypeError(f"{name}_out must be a bfloat16 tensor on cuda:{device}, as the batch is")
+    elif out.shape != shape:
+        raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    st, ot = x.stride(), out.stride()
+    if st[2] != 1 or ot[2] != 1:
+        raise TypeError(f"{name} and {name}_out must be dense in their channels")
+    w = 0
+    if weight is not None:
+        w = _on_device(weight, f"{name}_weight", torch.bfloat16, device, (dim,)).data_ptr()
+    return out, _HeadRows(x.data_ptr(), out.data_ptr(), st[0], st[1], ot[0], ot[1], w, shape[1])
+
+
+def qk_norm_rotary(q, k, batch: KVBatch, rotary: Rotary, q_weight=None, k_weight=None, eps: float = 1e-6,
+                   q_out=None, k_out=None):
+    """The norm of each head of q and k, bf16 [n_rows][heads][dim] (slices of a
+    joint projection's output serve as they are), with weights bf16 [dim]
+    (None: no norm), then the rotation by each row's position in `batch`.  k
+    may be None.  q_out=q and k_out=k work in place; otherwise the outputs are
+    new.  Rows past the last sequence are left as they are.  Returns (q, k)."""
+    device = batch.device_index
+    if rotary.device_index != device:
+        raise ValueError(f"rotary must be on cuda:{device}, as the batch is")
+    dim = q.shape[-1]
+    q_out, qs = _head_rows(q, "q", batch.n_rows, q_weight, q_out, device, dim)
+    ks = None
+    if k is not None:
+        k_out, ks = _head_rows(k, "k", batch.n_rows, k_weight, k_out, device, dim)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    status = lib().mlora_qk_norm_rotary(batch._ref, dim, rotary._ref, ctypes.byref(qs),
+                                        ctypes.byref(ks) if ks is not None else None, eps, _raw_stream(device))
+    if status != OK:
+        raise MloraError(status, "mlora_qk_norm_rotary")
+    return q_out, k_out
+
+
+def sample_work_bytes(n: int, vocab: int) -> int:
+    return int(lib().mlora_sample_work_bytes(n, vocab))
+
+
+def new_sample_work(n: int, vocab: int, device=None):
+    """A work buffer for sample() of n rows of `vocab` logits."""
+    torch = _torch()
+    return torch.empty(max(sample_work_bytes(n, vocab), 256), dtype=torch.uint8,
+                       device=device if device is not None else torch.device("cuda", torch.cuda.current_device()))
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, work=None):
+    """One token a row of logits, device bf16 or fp32 [n][vocab], drawn with the
+    random numbers u, fp32 [n] in [0, 1).  temperature, top_p, min_p (fp32
+    [n]) and top_k (int32 [n]) are each row's own; None leaves that out.
+    Returns int32 [n] (-1 for a row without any logit above -infinity); the
+    definition is in include/mlora.h."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
+        raise TypeError("logits must be a bfloat16 or float32 CUDA tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise TypeError("logits must be [n][vocab], dense in the vocabulary")
+    (n, vocab), device = logits.shape, logits.get_device()
+    _on_device(u, "u", torch.float32, device, (n,))
+    ptr = []
+    for name, t, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        ptr.append(None if t is None else _on_device(t, name, dt, device, (n,)).data_ptr())
+    if out is None:
+        out = torch.empty(n, dtype=torch.int32, device=logits.device)
+    _on_device(out, "out", torch.int32, device, (n,))
+    work = new_sample_work(n, vocab, logits.device) if work is None else _work(work, device)
+    status = lib().mlora_sample(logits.data_ptr(), logits.dtype is torch.float32, logits.stride(0) if n > 1 else vocab,
+                                n, vocab, u.data_ptr(), *ptr, out.data_ptr(), work.data_ptr(), work.nbytes,
+                                _raw_stream(device))
+    if status != OK:
+        raise MloraError(status, "mlora_sample")
     return out
 
 

@@ -19,6 +19,9 @@
 
 #include "internal.h"
 #include "kv.h"
+#include "q4.h"
+#include "qk_rotary.h"
+#include "sample.h"
 
 using mlora::PoolView;
 
@@ -1266,6 +1269,266 @@ mlora_status mlora_kv_attention(const mlora_kv_cache* c, int32_t layer, const ui
   if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0) return fail(MLORA_EINVAL, "work must be 256-byte aligned");
   const mlora::KvAttn a{q, rs, hs, out, scale, heads / c->kv_heads, causal != 0, window, work};
   return hip_check(mlora::launch_kv_attention(view, a, as_stream(stream)), "attention launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------
+// 4-bit weights
+// ----------------------------------------------------------------------------
+
+namespace {
+mlora_status q4_shape(int64_t din, int64_t dout) {
+  if (din < 32 || din > (1 << 20) || din % mlora::kQ4Group != 0)
+    return fail(MLORA_EINVAL, "4-bit weight: din %lld is not a multiple of 32 up to 2^20", (long long)din);
+  if (dout < 1 || dout > (1 << 24)) return fail(MLORA_EINVAL, "4-bit weight: dout %lld outside [1, 2^24]", (long long)dout);
+  return MLORA_OK;
+}
+mlora_status q4_view(const mlora_q4_weight* w, mlora::Q4View* v) {
+  if (!w) return fail(MLORA_EINVAL, "4-bit weight must not be NULL");
+  const mlora_status st = q4_shape(w->din, w->dout);
+  if (st != MLORA_OK) return st;
+  if (!w->codes || !w->scales || !aligned16(w->codes))
+    return fail(MLORA_EINVAL, "4-bit weight: codes and scales must not be NULL, codes 16-byte aligned");
+  *v = {w->codes, w->scales, w->din, w->dout};
+  return MLORA_OK;
+}
+bool q4_few(const mlora_pool* p, int n) { return n <= mlora::kQ4Rows && (!p || (aligned16(p->d.down_pages))); }
+// work of a product: few rows the per-row T region (with a pool) and the
+// partial products; more rows the bf16 weight, then the bf16 product's own
+size_t q4_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
+  if (n <= 0) return 0;
+  if (q4_few(p, n))
+    return (p ? rows_t_bytes(p, n) : 0) +
+           align256(mlora::q4_plan(n, w.K, w.N, p != nullptr).part_floats(n, w.N) * sizeof(float));
+  const size_t weight = align256((size_t)w.K * w.N * 2);
+  if (p) return weight + mlora_work_bytes(p, n);
+  return weight + (n <= kRowsMax ? align256(mlora::gemm_lora_part_floats(n, w.N, w.K) * sizeof(float)) : 0);
+}
+mlora_status q4_work(const mlora::Q4View& w, const mlora_pool* p, int n, const void* work, size_t bytes) {
+  const size_t need = q4_bytes(w, p, n);
+  if (need > 0 && (!work || bytes < need)) return fail(MLORA_EINVAL, "work: %zu bytes given, %zu needed", bytes, need);
+  if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0) return fail(MLORA_EINVAL, "work must be 256-byte aligned");
+  return MLORA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+mlora_status mlora_q4_quantize(const uint16_t* W, int32_t dout, int32_t din, uint8_t* codes, uint8_t* scales,
+                               void* stream) {
+  g_err.clear();
+  const mlora_status st = q4_shape(din, dout);
+  if (st != MLORA_OK) return st;
+  if (!W || !codes || !scales || !aligned16(W) || !aligned16(codes))
+    return fail(MLORA_EINVAL, "W, codes and scales must not be NULL, W and codes 16-byte aligned");
+  return hip_check(mlora::launch_q4_quantize(W, codes, scales, (int64_t)dout * din, as_stream(stream)),
+                   "4-bit quantiser launch");
+}
+
+mlora_status mlora_q4_dequantize(const mlora_q4_weight* w, uint16_t* W, void* stream) {
+  g_err.clear();
+  mlora::Q4View v;
+  const mlora_status st = q4_view(w, &v);
+  if (st != MLORA_OK) return st;
+  if (!W || !aligned16(W)) return fail(MLORA_EINVAL, "W must not be NULL and be 16-byte aligned");
+  return hip_check(mlora::launch_q4_dequantize(v.codes, v.scales, W, (int64_t)v.N * v.K, as_stream(stream)),
+                   "4-bit weight to bf16 launch");
+}
+
+size_t mlora_q4_work_bytes(const mlora_q4_weight* w, const mlora_pool* p, int32_t n) {
+  mlora::Q4View v;
+  if (q4_view(w, &v) != MLORA_OK || n < 0 || n > MLORA_MAX_ROWS) return 0;
+  if (p && (p->d.din != v.K || p->d.dout != v.N)) return 0;
+  return q4_bytes(v, p, n);
+}
+
+mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t* Y, int32_t n, void* work,
+                           size_t work_bytes, void* stream) {
+  g_err.clear();
+  mlora::Q4View v;
+  mlora_status st = q4_view(w, &v);
+  if (st != MLORA_OK) return st;
+  if (n < 0 || n > MLORA_MAX_ROWS) return fail(MLORA_EINVAL, "n_rows %d outside [0, %d]", n, MLORA_MAX_ROWS);
+  if (n == 0) return MLORA_OK;
+  if (!X || !Y || !aligned16(X)) return fail(MLORA_EINVAL, "X and Y must not be NULL, X 16-byte aligned");
+  if ((st = q4_work(v, nullptr, n, work, work_bytes)) != MLORA_OK) return st;
+  hipStream_t s = as_stream(stream);
+  if (q4_few(nullptr, n))
+    return hip_check(mlora::launch_q4_rows(v, X, n, Y, static_cast<float*>(work), nullptr, 0, nullptr, nullptr, s),
+                     "4-bit product launch");
+  uint16_t* W = static_cast<uint16_t*>(work);
+  st = hip_check(mlora::launch_q4_dequantize(v.codes, v.scales, W, (int64_t)v.N * v.K, s), "4-bit weight to bf16 launch");
+  if (st != MLORA_OK) return st;
+  hipError_t e = hipErrorNotSupported;
+  if (n <= kRowsMax) {
+    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + align256((size_t)v.K * v.N * 2));
+    e = mlora::launch_base_split(X, W, Y, n, v.K, v.N, part, s);
+  }
+  if (e == hipErrorNotSupported) e = mlora::launch_base_gemm(X, W, Y, n, v.K, v.N, s);
+  return hip_check(e, "base GEMM launch");
+}
+
+mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X, const mlora_q4_weight* w,
+                            const void* seg_ws, uint16_t* Y, int32_t n, void* work, size_t work_bytes, void* stream) {
+  g_err.clear();
+  mlora_status st = check_branch_args(p, proj, seg_ws, n);
+  if (st != MLORA_OK) return st;
+  mlora::Q4View v;
+  if ((st = q4_view(w, &v)) != MLORA_OK) return st;
+  if (p->d.din != v.K || p->d.dout != v.N)
+    return fail(MLORA_EINVAL, "the weight is [%d][%d], the pool's projections are [%d][%d]", v.N, v.K, p->d.dout, p->d.din);
+  if (n == 0) return MLORA_OK;
+  if (!X || !Y || !aligned16(X)) return fail(MLORA_EINVAL, "X and Y must not be NULL, X 16-byte aligned");
+  if ((st = q4_work(v, p, n, work, work_bytes)) != MLORA_OK) return st;
+  if (q4_few(p, n)) {
+    const PoolView pv = p->view();
+    float* T = static_cast<float*>(work);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + rows_t_bytes(p, n));
+    const int32_t* row_key = static_cast<const int32_t*>(seg_ws) + MLORA_SEG_ROWKEY(n);
+    return hip_check(mlora::launch_q4_rows(v, X, n, Y, part, &pv, proj, row_key, T, as_stream(stream)),
+                     "4-bit product + low-rank term launch");
+  }
+  uint16_t* W = static_cast<uint16_t*>(work);
+  const size_t weight = align256((size_t)v.K * v.N * 2);
+  st = hip_check(mlora::launch_q4_dequantize(v.codes, v.scales, W, (int64_t)v.N * v.K, as_stream(stream)),
+                 "4-bit weight to bf16 launch");
+  if (st != MLORA_OK) return st;
+  return mlora_apply(p, proj, X, W, seg_ws, Y, n, static_cast<char*>(work) + weight, work_bytes - weight,
+                     MLORA_VARIANT_AUTO, stream);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------
+// norms of queries and keys with the rotation
+// ----------------------------------------------------------------------------
+
+namespace {
+// The elements that rows of heads reach over: [first, last), as addresses.
+struct HeadSpan {
+  uintptr_t first, last;
+};
+HeadSpan head_span(const uint16_t* p, int64_t rs, int64_t hs, int n, int heads, int dim) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + 2 * (uintptr_t)((n - 1) * rs + (heads - 1) * hs + dim)};
+}
+bool overlap(const HeadSpan& a, const HeadSpan& b) { return a.first < b.last && b.first < a.last; }
+// Two sets of heads that interleave as slices of the same rows: every row of
+// one lies between the rows of the other.
+bool apart_in_rows(const uint16_t* p, int64_t prs, int64_t phs, int ph, const uint16_t* q, int64_t qrs, int64_t qhs,
+                   int qh, int dim) {
+  if (prs != qrs || prs <= 0) return false;
+  if (p > q) return apart_in_rows(q, qrs, qhs, qh, p, prs, phs, ph, dim);
+  const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p));
+  if (bytes % 2 != 0) return false;
+  const int64_t d = bytes / 2 % prs;  // where q's heads start in a row of p
+  return (ph - 1) * phs + dim <= d && d + (qh - 1) * qhs + dim <= prs;
+}
+bool in_place(const mlora_head_rows& s) {
+  return s.x == s.y && s.row_stride == s.out_row_stride && s.head_stride == s.out_head_stride;
+}
+// output of s against the rows (p, rs, hs, heads) of something else
+bool clash(const mlora_head_rows& s, const uint16_t* p, int64_t rs, int64_t hs, int heads, int n, int dim) {
+  if (!overlap(head_span(s.y, s.out_row_stride, s.out_head_stride, n, s.heads, dim), head_span(p, rs, hs, n, heads, dim)))
+    return false;
+  return !apart_in_rows(s.y, s.out_row_stride, s.out_head_stride, s.heads, p, rs, hs, heads, dim);
+}
+}  // namespace
+
+extern "C" {
+
+mlora_status mlora_qk_norm_rotary(const mlora_kv_batch* b, int32_t dim, const mlora_rotary* rot,
+                                  const mlora_head_rows* q, const mlora_head_rows* k, float eps, void* stream) {
+  g_err.clear();
+  if (!b || !rot || (!q && !k)) return fail(MLORA_EINVAL, "batch, rotary and one of q and k must not be NULL");
+  if (dim < 16 || dim > 256 || dim % 16 != 0) return fail(MLORA_EINVAL, "dim %d is not a multiple of 16 up to 256", dim);
+  if (rot->rot < 8 || rot->rot > dim || rot->rot % 8 != 0)
+    return fail(MLORA_EINVAL, "rotary: %d channels are not a multiple of 8 up to %d", rot->rot, dim);
+  if (!rot->freq || (reinterpret_cast<uintptr_t>(rot->freq) & 7u) != 0)
+    return fail(MLORA_EINVAL, "rotary: freq must not be NULL and be 8-byte aligned");
+  if (!std::isfinite(rot->factor)) return fail(MLORA_EINVAL, "rotary: factor must be finite");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLORA_EINVAL, "eps must be finite and not below 0");
+  if (b->n_seq < 0 || b->n_seq > (1 << 20) || b->n_rows < 0 || b->n_rows > (1 << 24))
+    return fail(MLORA_EINVAL, "batch: %d sequences (at most 2^20), %d rows (at most 2^24)", b->n_seq, b->n_rows);
+  if (b->n_rows > 0) {
+    if (b->n_seq == 0) return fail(MLORA_EINVAL, "batch: %d rows without a sequence", b->n_rows);
+    if (!b->kv_len || !b->row_off) return fail(MLORA_EINVAL, "batch: a buffer is NULL");
+  }
+  const mlora_head_rows* side[2] = {q, k};
+  mlora::QkRotary a{};
+  for (int i = 0; i < 2; ++i) {
+    const mlora_head_rows* s = side[i];
+    if (!s) continue;
+    if (s->heads < 1 || s->heads > 1024) return fail(MLORA_EINVAL, "%d heads outside [1, 1024]", s->heads);
+    for (int64_t x : {s->row_stride, s->head_stride, s->out_row_stride, s->out_head_stride})
+      if (x < 0 || x > INT32_MAX) return fail(MLORA_EINVAL, "stride %lld outside [0, 2^31)", (long long)x);
+    if (b->n_rows == 0) continue;
+    if (!s->x || !s->y) return fail(MLORA_EINVAL, "x and y must not be NULL");
+    // the heads of the output lie apart
+    if ((s->heads > 1 && s->out_head_stride < dim) ||
+        (b->n_rows > 1 && s->out_row_stride < (s->heads - 1) * s->out_head_stride + dim))
+      return fail(MLORA_EINVAL, "output heads overlap: strides %lld, %lld", (long long)s->out_row_stride,
+                  (long long)s->out_head_stride);
+    a.side[i] = {s->x, s->y, s->row_stride, s->head_stride, s->out_row_stride, s->out_head_stride, s->weight, s->heads};
+  }
+  if (b->n_rows == 0) return MLORA_OK;
+  for (int i = 0; i < 2; ++i) {
+    const mlora_head_rows* s = side[i];
+    const mlora_head_rows* o = side[1 - i];
+    if (!s) continue;
+    bool bad = !in_place(*s) && clash(*s, s->x, s->row_stride, s->head_stride, s->heads, b->n_rows, dim);
+    if (o)
+      bad = bad || clash(*s, o->x, o->row_stride, o->head_stride, o->heads, b->n_rows, dim) ||
+            clash(*s, o->y, o->out_row_stride, o->out_head_stride, o->heads, b->n_rows, dim);
+    if (bad) return fail(MLORA_EINVAL, "an output overlaps an input or the other output");
+  }
+  if (!q) {  // the keys alone take the queries' place
+    a.side[0] = a.side[1];
+    a.side[1] = {};
+  }
+  a.kv_len = b->kv_len;
+  a.row_off = b->row_off;
+  a.n_seq = b->n_seq;
+  a.n_rows = b->n_rows;
+  a.D = dim;
+  a.rot = rot->rot;
+  a.interleaved = rot->interleaved != 0;
+  a.freq = rot->freq;
+  a.factor = rot->factor;
+  a.eps = eps;
+  return hip_check(mlora::launch_qk_rotary(a, as_stream(stream)), "norm + rotation launch");
+}
+
+// ----------------------------------------------------------------------------
+// sampling
+// ----------------------------------------------------------------------------
+
+static_assert(mlora::kSampleMaxVocab == MLORA_MAX_VOCAB, "the header states the largest vocabulary");
+
+size_t mlora_sample_work_bytes(int32_t n, int32_t vocab) {
+  if (n < 0 || n > MLORA_MAX_ROWS || vocab < 1 || vocab > MLORA_MAX_VOCAB) return 0;
+  return n == 0 ? 0 : mlora::sample_work_bytes(n, vocab);
+}
+
+mlora_status mlora_sample(const void* logits, int32_t is_f32, int64_t row_stride, int32_t n, int32_t vocab,
+                          const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* out, void* work, size_t work_bytes, void* stream) {
+  g_err.clear();
+  if (n < 0 || n > MLORA_MAX_ROWS) return fail(MLORA_EINVAL, "n_rows %d outside [0, %d]", n, MLORA_MAX_ROWS);
+  if (vocab < 1 || vocab > MLORA_MAX_VOCAB) return fail(MLORA_EINVAL, "vocab %d outside [1, 2^20]", vocab);
+  if (row_stride < 0 || row_stride > INT32_MAX)
+    return fail(MLORA_EINVAL, "row stride %lld outside [0, 2^31)", (long long)row_stride);
+  if (n == 0) return MLORA_OK;
+  if (!logits || !u || !out) return fail(MLORA_EINVAL, "logits, u and out must not be NULL");
+  if (reinterpret_cast<uintptr_t>(logits) % (is_f32 ? 4 : 2) != 0)
+    return fail(MLORA_EINVAL, "logits must be aligned to their elements");
+  const size_t need = mlora::sample_work_bytes(n, vocab);
+  if (need > 0 && (!work || work_bytes < need))
+    return fail(MLORA_EINVAL, "work: %zu bytes given, %zu needed", work_bytes, need);
+  if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0) return fail(MLORA_EINVAL, "work must be 256-byte aligned");
+  const mlora::SampleArgs a{logits, row_stride, n, vocab, is_f32 != 0, u, temperature, top_k, top_p, min_p, out};
+  return hip_check(mlora::launch_sample(a, work, as_stream(stream)), "sampling launch");
 }
 
 }  // extern "C"
