@@ -7,9 +7,18 @@
 // first; what top-k, top-p and min-p keep is a beginning of that order, and
 // the token drawn is the one at which the running weight passes u times the
 // weight kept.  So all that is asked of the order is where its running count
-// or weight reaches a given number.  A histogram over the logits (count and
-// weight of 2048 equal ranges from the largest down) finds the range, and the
-// few tokens of that range are compared among themselves; nothing is sorted.
+// or weight reaches a given number, and nothing but a few hundred tokens near
+// those places is ever put in order:
+//   1. the largest logit (one pass over the row);
+//   2. a histogram of the weights over 4096 equal ranges of logits (a pass;
+//      the exponentials and the LDS atomics bound it);
+//   3. the ranges in which the running numbers can reach what they are asked
+//      for are known then: their tokens go to a list (a pass), which is put in
+//      order by counting, and the exact places are read off its running sums.
+// A small top-k needs no histogram: the list holds the tokens down to the
+// range of the k-th largest of the threads' own largest logits.
+// Where too many tokens share a range (ties, narrow clusters), `reach` parts
+// it again and again instead, at two passes a part.
 #include "sample.h"
 
 namespace mlora {
@@ -18,188 +27,391 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048, kCap = 2048;
+constexpr int kBins = 4096, kPer = kBins / kThreads, kCap = 1024;
 constexpr int kFrac = 42;  // a weight of 1 is 2^42: 2^20 of them stay below 2^63
+constexpr int kSmallK = 512;  // largest top-k that is looked for among the threads' maxima
 constexpr float kNone = -__builtin_huge_valf();
 
 struct Shared {
-  u64 mass[kBins];
-  uint32_t count[kBins];
-  u64 key[kCap];  // tokens of the range: order, index
-  u64 w[kCap];
-  u64 red[kWaves];
-  uint32_t redc[kWaves];
+  __attribute__((aligned(16))) u64 mass[kBins + 2];  // histogram, then the weight before each range
+  __attribute__((aligned(16))) uint32_t count[kBins + 4];
+  u64 key[kCap], skey[kCap];  // listed tokens (order and index), the same in order
+  uint32_t rank[kCap];
+  struct Red {  // of a running sum over the workgroup
+    u64 m[kWaves];
+    uint32_t c[kWaves];
+  } red[3];
   float redf[2][kWaves];
-  int redi[kWaves];
-  u64 res[4];  // what one thread found for all
+  u64 got[4];  // what one thread found for all
+  int bins[6];
   uint32_t n_list;
-  int bin;
 };
 
-// bf16 or fp32 logits as floats: NaN counts as -infinity, -0 as 0
-__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : kNone; }
-
-// f(index, logit) for every logit of the row that falls to this thread, in
-// rising order of the index; 16-byte loads between the ends
-template <class T, class F>
+// f(i, x) for every piece of the row that falls to this thread: x[e] is logit
+// i + e of 16 bytes of them, NaN where there is none (the ends of the row come
+// one at a time).  U pieces are loaded at once.
+template <int U, class T, class F>
 __device__ __forceinline__ void for_row(const T* __restrict__ row, int V, F f) {
   constexpr int E = 16 / sizeof(T);
   const int tid = threadIdx.x;
   const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
-  const int body = (V - head) / E;
-  auto one = [&](int i) {
-    if constexpr (sizeof(T) == 2)
-      f(i, clean(bf2f(row[i])));
-    else
-      f(i, clean(row[i]));
-  };
-  if (tid < head) one(tid);
+  const int body = (V - head) / E, tail = head + body * E;
   const uint4* p = reinterpret_cast<const uint4*>(row + head);
-  constexpr int U = 4;
-  for (int v0 = tid; v0 < body; v0 += U * kThreads) {
-    uint4 x[U];
+  float x[E];
+  if (head + V - tail > 0) {
+    const int i = tid < head ? tid : tail + tid - head;
 #pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = p[min(v0 + k * kThreads, body - 1)];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int v = v0 + k * kThreads;
-      if (v < body) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float l;
-          if constexpr (sizeof(T) == 2)
-            l = (e & 1) ? hi_bf(w[e >> 1]) : lo_bf(w[e >> 1]);
-          else
-            l = __uint_as_float(w[e]);
-          f(head + v * E + e, clean(l));
-        }
-      }
+    for (int e = 1; e < E; ++e) x[e] = __builtin_nanf("");
+    if (i < V) {
+      if constexpr (sizeof(T) == 2)
+        x[0] = bf2f(row[i]);
+      else
+        x[0] = row[i];
+      f(i, x);
     }
   }
-  const int tail = head + body * E;
-  if (tail + tid < V) one(tail + tid);
+  auto piece = [&](int v, const uint4& y) {
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if constexpr (sizeof(T) == 2)
+        x[e] = (e & 1) ? hi_bf(w[e >> 1]) : lo_bf(w[e >> 1]);
+      else
+        x[e] = __uint_as_float(w[e]);
+    }
+    f(head + v * E, x);
+  };
+  int v = tid;
+  for (; v + (U - 1) * kThreads < body; v += U * kThreads) {
+    uint4 y[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) y[k] = p[v + k * kThreads];
+#pragma unroll
+    for (int k = 0; k < U; ++k) piece(v + k * kThreads, y[k]);
+  }
+  for (; v < body; v += kThreads) piece(v, p[v]);
 }
 
 struct Row {
-  float mx;        // largest logit
-  double inv_l2;   // log2(e) / T
-  float inv, fit;  // 1 / T, histogram ranges per nat
+  double mx, scale;  // largest logit; log2(e) / T
+  float fit, fit0;   // a logit's place in the histogram: fit0 - fit * logit
+  float least;       // the weight is 0 from here down
+  bool top;          // the largest is +infinity: those stand at 0, all else at -infinity
+  // A logit as it is compared: NaN counts as -infinity.
+  __device__ __forceinline__ float clean(float x) const {
+    x = fmaxf(x, kNone);
+    if (top) x = x == -kNone ? 0.f : kNone;
+    return x;
+  }
 };
 
-// weight of a logit, in multiples of 2^-42 (0 for -infinity)
+// Weight of a logit, in multiples of 2^-42.  ANY: of any clean logit; else of
+// one that is not below r.least.
+template <bool ANY = false>
 __device__ __forceinline__ u64 weight(const Row& r, float x) {
-  if (x == r.mx) return 1ull << kFrac;
-  const double d = ((double)x - (double)r.mx) * r.inv_l2;  // <= 0, -infinity or NaN where x is -infinity
-  if (!(d > -(kFrac + 1.0)) || x == kNone) return 0;
-  const double n = __builtin_rint(d), f = (d - n) * 0.69314718055994530942;
-  // e^f, |f| <= 0.347: the next term of the series is below 2^-52
-  double p = 1.0 / 6227020800.0;
-  p = fma(p, f, 1.0 / 479001600.0);
-  p = fma(p, f, 1.0 / 39916800.0);
-  p = fma(p, f, 1.0 / 3628800.0);
-  p = fma(p, f, 1.0 / 362880.0);
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
+  double d = ((double)x - r.mx) * r.scale;
+  if (ANY) d = fmax(d, -64.0);  // also for the NaN of -infinity * 0
+  const double t = d + 6755399441055744.0;  // 1.5 * 2^52: the nearest whole number in the low word
+  const double f = d - (t - 6755399441055744.0);
+  // 2^f, |f| <= 1/2: relative error 8e-14, 1 at f = 0 (minimax fit)
+  double p = 9.16811938851594e-08;
+  p = fma(p, f, 1.3255182784592006e-06);
+  p = fma(p, f, 1.5258493063907014e-05);
+  p = fma(p, f, 0.0001540345603665657);
+  p = fma(p, f, 0.0013333547331461978);
+  p = fma(p, f, 0.009618129159172244);
+  p = fma(p, f, 0.055504108739712246);
+  p = fma(p, f, 0.24022650695813708);
+  p = fma(p, f, 0.6931471805585505);
   p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
-  // adding 2^10 leaves the sum's last place at 2^-42: rounds to nearest
-  const double v = ldexp(p, (int)n) + 1024.0;
-  return (u64)__double_as_longlong(v) - (u64)__double_as_longlong(1024.0);
+  p = __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+  // in a sum with 2^10 the last place is 2^-42: rounded to nearest
+  return (u64)__double_as_longlong(p + 1024.0) & 0xfffffffffffffull;
 }
 
-// histogram range of a logit with a weight: falls with the logit, never the
-// other way (every step is monotone)
+// place of a logit in the histogram, and its range there: they fall with the
+// logit, never the other way (every step is monotone)
+__device__ __forceinline__ float place_of(const Row& r, float x) { return fmaf(x, -r.fit, r.fit0); }
 __device__ __forceinline__ int range_of(const Row& r, float x) {
-  return x == r.mx ? 0 : (int)fminf((r.mx - x) * r.inv * r.fit, kBins - 1);
+  return (int)__builtin_amdgcn_fmed3f(place_of(r, x), 0.f, (float)(kBins - 1));
 }
+
+// floats as whole numbers that rise with them
+__device__ __forceinline__ uint32_t rising(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_rising(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ float next_up(float x) { return from_rising(rising(x) + 1); }
 
 // place of a token in the order, rising: falling logits, then rising indices
 __device__ __forceinline__ u64 order_key(float x, int i) {
-  uint32_t b = __float_as_uint(x);
-  b ^= (b >> 31) ? 0xffffffffu : 0x80000000u;
-  return ((u64)~b << 32) | (uint32_t)i;
-}
-// inclusive running sum over the workgroup's threads; total in *all
-template <class N>
-__device__ __forceinline__ N block_scan(N v, N* red, N* all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    N o;
-    if constexpr (sizeof(N) == 8)
-      o = (N)__shfl_up((long long)v, d, 64);
-    else
-      o = (N)__shfl_up((int)v, d, 64);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();
-  if (lane == 63) red[wave] = v;
-  __syncthreads();
-  N before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += red[w];
-    total += red[w];
-  }
-  *all = total;
-  return v + before;
+  return ((u64)~rising(x + 0.f) << 32) | (uint32_t)i;  // -0 and 0 are alike
 }
 
-// Where the running number of the histogram (its counts or its weights)
-// first reaches `aim` (1 .. its total): that range in sh.bin, the count and
-// weight before it in sh.res[0], sh.res[1].
-__device__ __forceinline__ void find_bin(Shared& sh, u64 aim, bool by_count) {
-  const int t = threadIdx.x;
-  const u64 m0 = sh.mass[2 * t], m1 = sh.mass[2 * t + 1];
-  const uint32_t c0 = sh.count[2 * t], c1 = sh.count[2 * t + 1];
-  u64 mall;
-  uint32_t call;
-  const u64 m = block_scan(m0 + m1, sh.red, &mall) - (m0 + m1);
-  const uint32_t c = block_scan(c0 + c1, sh.redc, &call) - (c0 + c1);
-  const u64 b0 = by_count ? c : m, b1 = b0 + (by_count ? c0 : m0), b2 = b1 + (by_count ? c1 : m1);
-  if (b0 < aim && aim <= b2) {
-    const bool second = b1 < aim;
-    sh.bin = 2 * t + (second ? 1 : 0);
-    sh.res[0] = c + (second ? c0 : 0u);
-    sh.res[1] = m + (second ? m0 : 0ull);
+// the logit of a key
+__device__ __forceinline__ float key_logit(u64 key) { return from_rising(~(uint32_t)(key >> 32)); }
+
+// v of the lane that the DPP pattern names, 0 where there is none
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 dpp(u64 v) {
+  return (u64)dpp<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | dpp<CTRL, ROWS>((uint32_t)v);
+}
+template <class N>
+__device__ __forceinline__ N row_scan(N v) {  // inclusive, in rows of 16 lanes
+  v += dpp<0x111, 0xf>(v);
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  return v;
+}
+template <class N>
+__device__ __forceinline__ N wave_scan(N v) {
+  v = row_scan(v);
+  v += dpp<0x142, 0xa>(v);  // the row before's last lane
+  v += dpp<0x143, 0xc>(v);  // lane 31
+  return v;
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); }
+__device__ __forceinline__ u64 lane_value(u64 v, int l) {
+  return (u64)lane_value((uint32_t)(v >> 32), l) << 32 | lane_value((uint32_t)v, l);
+}
+// inclusive running sums of m and c over the workgroup's threads, in place;
+// the totals.  One barrier: `red` is free again after the next one.
+__device__ __forceinline__ void block_scan(u64& m, uint32_t& c, Shared::Red& red, u64& mall, uint32_t& call) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  m = wave_scan(m);
+  c = wave_scan(c);
+  if (lane == 63) {
+    red.m[wave] = m;
+    red.c[wave] = c;
   }
   __syncthreads();
+  static_assert(kWaves == 16, "a row of lanes holds the waves' sums");
+  const u64 wm = row_scan(red.m[lane & 15]);
+  const uint32_t wc = row_scan(red.c[lane & 15]);
+  mall = lane_value(wm, 15);
+  call = lane_value(wc, 15);
+  if (wave > 0) {
+    m += lane_value(wm, wave - 1);
+    c += lane_value(wc, wave - 1);
+  }
 }
 
 __device__ __forceinline__ void clear_bins(Shared& sh) {
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    sh.mass[i] = 0;
-    sh.count[i] = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    sh.mass[i * kThreads + threadIdx.x] = 0;
+    sh.count[i * kThreads + threadIdx.x] = 0;
   }
   __syncthreads();
 }
 
-// The token at which the running count or weight of the order first reaches
-// `aim`, given the histogram of the whole row in sh: its index in *token, the
-// weight up to and with it as the result.
-template <class T>
-__device__ u64 reach(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 aim, bool by_count, int* token) {
-  find_bin(sh, aim, by_count);
-  const int bin = sh.bin;
-  u64 c0 = sh.res[0], m0 = sh.res[1];
-  uint32_t size = sh.count[bin];
-  u64 lo = 0, hi = ~0ull;  // order keys of the tokens looked at, both inside
-  bool first = true;
+// This thread's ranges kPer * tid .. of the histogram: the running weight and
+// count before each (and after the last), also left in place of the histogram.
+struct Ends {
+  u64 m[kPer + 1];
+  uint32_t c[kPer + 1];
+};
+__device__ __forceinline__ Ends scan_bins(Shared& sh, u64& mass, uint32_t& count) {
+  static_assert(kPer == 4, "vector loads of a thread's ranges");
+  const int t = threadIdx.x * kPer;
+  const ulonglong2 m01 = *reinterpret_cast<const ulonglong2*>(&sh.mass[t]);
+  const ulonglong2 m23 = *reinterpret_cast<const ulonglong2*>(&sh.mass[t + 2]);
+  const uint4 c = *reinterpret_cast<const uint4*>(&sh.count[t]);
+  u64 m = m01.x + m01.y + m23.x + m23.y;
+  uint32_t n = c.x + c.y + c.z + c.w;
+  const u64 own = m;
+  const uint32_t nown = n;
+  block_scan(m, n, sh.red[0], mass, count);
+  Ends e;
+  e.m[0] = m - own;
+  e.m[1] = e.m[0] + m01.x;
+  e.m[2] = e.m[1] + m01.y;
+  e.m[3] = e.m[2] + m23.x;
+  e.m[4] = m;
+  e.c[0] = n - nown;
+  e.c[1] = e.c[0] + c.x;
+  e.c[2] = e.c[1] + c.y;
+  e.c[3] = e.c[2] + c.z;
+  e.c[4] = n;
+  *reinterpret_cast<ulonglong2*>(&sh.mass[t]) = make_ulonglong2(e.m[0], e.m[1]);
+  *reinterpret_cast<ulonglong2*>(&sh.mass[t + 2]) = make_ulonglong2(e.m[2], e.m[3]);
+  *reinterpret_cast<uint4*>(&sh.count[t]) = make_uint4(e.c[0], e.c[1], e.c[2], e.c[3]);
+  if (threadIdx.x == kThreads - 1) {
+    sh.mass[kBins] = m;
+    sh.count[kBins] = n;
+  }
   __syncthreads();
-  while (size > kCap) {
-    // too many for the list: their keys' own range in 2048 parts
-    if (first) {
+  return e;
+}
+// the range in which the running weight reaches `aim` (1 .. the total), to *bin
+__device__ __forceinline__ void find_mass(const Ends& e, u64 aim, int* bin) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (e.m[i] < aim && aim <= e.m[i + 1]) *bin = threadIdx.x * kPer + i;
+}
+__device__ __forceinline__ void find_count(const Ends& e, uint32_t aim, int* bin) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (e.c[i] < aim && aim <= e.c[i + 1]) *bin = threadIdx.x * kPer + i;
+}
+
+// the histogram of the row; returns this thread's weight of the tokens with at
+// least `least`
+template <class T>
+__device__ __forceinline__ u64 histogram(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 least,
+                                         bool counts) {
+  u64 strong = 0;
+  for_row<2>(row, V, [&](int, const float (&xs)[16 / sizeof(T)]) {
+#pragma unroll
+    for (int e = 0; e < (int)(16 / sizeof(T)); ++e) {
+      const float x = fmaxf(xs[e], r.least);
+      const u64 w = weight(r, x);
+      const int b = range_of(r, x);
+      if (x > r.least) {
+        atomicAdd(&sh.mass[b], w);
+        if (counts) atomicAdd(&sh.count[b], 1u);
+      }
+      if (least != 0 && w >= least) strong += w;
+      if (e & 1) __builtin_amdgcn_sched_barrier(0);  // keeps the next logits' work out of the registers
+    }
+  });
+  return strong;
+}
+
+// Lists the tokens whose places in the histogram lie in one of N intervals
+// (lo inside, hi outside): their keys, in any order; all are counted, the
+// first kCap of them held.
+struct Interval {
+  float lo, hi;
+};
+template <int N, class T>
+__device__ __forceinline__ void list_in(Shared& sh, const Row& r, const T* __restrict__ row, int V,
+                                        const Interval (&iv)[3]) {
+  constexpr int E = 16 / sizeof(T);
+  for_row<4>(row, V, [&](int i, const float (&xs)[E]) {
+    uint32_t hit = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float t = place_of(r, xs[e]);  // NaN is in none
+      bool in = t >= iv[0].lo && t < iv[0].hi;
+      if (N > 1) in = in || (t >= iv[1].lo && t < iv[1].hi);
+      if (N > 2) in = in || (t >= iv[2].lo && t < iv[2].hi);
+      hit |= in ? 1u << e : 0u;
+    }
+    while (hit) {
+      const int e = __builtin_ctz(hit);
+      hit &= hit - 1;
+      float x = xs[0];
+#pragma unroll
+      for (int j = 1; j < E; ++j) x = e == j ? xs[j] : x;
+      const uint32_t p = atomicAdd(&sh.n_list, 1u);
+      if (p < kCap) sh.key[p] = order_key(x, i + e);
+    }
+  });
+  __syncthreads();
+}
+template <class T>
+__device__ __forceinline__ void list_tokens(Shared& sh, const Row& r, const T* __restrict__ row, int V, int n,
+                                            const Interval (&iv)[3]) {
+  if (n == 1)
+    list_in<1>(sh, r, row, V, iv);
+  else if (n == 2)
+    list_in<2>(sh, r, row, V, iv);
+  else
+    list_in<3>(sh, r, row, V, iv);
+}
+
+// Puts the n listed tokens in order (skey) and returns, to thread i, the
+// running weight up to and with token i, in *c its running count and in *own
+// its weight, all from the beginning of the order: what lies between the
+// listed ranges is taken from the histogram (`ranged`; else the list is the
+// beginning).
+__device__ __forceinline__ u64 order_list(Shared& sh, const Row& r, int n, bool ranged, uint32_t* c, u64* own) {
+  const int tid = threadIdx.x;
+  sh.rank[tid] = 0;
+  __syncthreads();
+  // the rank is the number of smaller keys, counted by all threads
+  const int np = (n + 63) & ~63, parts = kThreads / np, i = tid % np, part = tid / np;
+  if (i < n && part < parts) {
+    const u64 k = sh.key[i];
+    uint32_t before = 0;
+#pragma unroll 8
+    for (int j = part; j < n; j += parts) before += sh.key[j] < k ? 1u : 0u;
+    if (parts == 1)
+      sh.rank[i] = before;
+    else
+      atomicAdd(&sh.rank[i], before);
+  }
+  __syncthreads();
+  if (tid < n) sh.skey[sh.rank[tid]] = sh.key[tid];
+  __syncthreads();
+  u64 m = 0, w = 0;
+  uint32_t k = 0;
+  if (tid < n) {
+    const float x = key_logit(sh.skey[tid]);
+    w = weight<true>(r, x);
+    m = w;
+    k = 1;
+    if (ranged) {
+      const int b = range_of(r, x), pb = tid > 0 ? range_of(r, key_logit(sh.skey[tid - 1])) : -1;
+      if (b != pb) {  // the first of its range: what lies since the range listed before
+        m += sh.mass[b] - sh.mass[pb + 1];
+        k += sh.count[b] - sh.count[pb + 1];
+      }
+    }
+  }
+  u64 mall;
+  uint32_t call;
+  *own = w;
+  block_scan(m, k, sh.red[1], mall, call);
+  *c = k;
+  return m;
+}
+
+// ceil(p * mass), at least 1, p below 1
+__device__ __forceinline__ u64 part_up(float p, u64 mass) {
+  if (!(p > 0.f)) return 1;
+  const u64 q = (u64)((double)p * 18446744073709551616.0);
+  const u64 a = __umul64hi(q, mass) + (q * mass != 0 ? 1 : 0);
+  return a > 0 ? a : 1;
+}
+// floor(u * mass) + 1, at most mass
+__device__ __forceinline__ u64 part_past(float u, u64 mass) {
+  if (!(u > 0.f)) return 1;
+  return __umul64hi((u64)((double)fminf(u, 0.99999994f) * 18446744073709551616.0), mass) + 1;
+}
+
+// The token at which the running count or weight of the order first reaches
+// `aim`, in whatever passes it takes: its index in *token, the weight up to
+// and with it as the result.  For ranges with more tokens than the list holds.
+template <class T>
+__device__ __forceinline__ u64 reach(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 aim,
+                                     bool by_count, int* token) {
+  constexpr int E = 16 / sizeof(T);
+  u64 m0 = 0, c0 = 0;      // before the tokens looked at
+  u64 lo = 0, hi = ~0ull;  // their keys lie from lo to hi
+  int bin = -1;            // their range (-1: any)
+  bool first = true;
+  while (true) {
+    int shift = 0;  // the histogram's ranges are of 2^shift keys, but the first one's
+    if (!first) {
+      // the least and the largest key that there are
       u64 a = ~0ull, b = 0;
-      for_row(row, V, [&](int i, float x) {
-        if (weight(r, x) != 0 && range_of(r, x) == bin) {
-          const u64 k = order_key(x, i);
+      for_row<1>(row, V, [&](int i, const float (&xs)[E]) {
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          const float x = r.clean(xs[e]);
+          const u64 k = order_key(x, i + e);
+          if (k < lo || k > hi || range_of(r, x) != bin || weight<true>(r, x) == 0) continue;
           a = min(a, k);
           b = max(b, k);
         }
@@ -209,189 +421,303 @@ __device__ u64 reach(Shared& sh, const Row& r, const T* __restrict__ row, int V,
         a = min(a, (u64)__shfl_xor((long long)a, d, 64));
         b = max(b, (u64)__shfl_xor((long long)b, d, 64));
       }
+      __syncthreads();
       if ((threadIdx.x & 63) == 0) {
         sh.key[threadIdx.x >> 6] = a;
-        sh.w[threadIdx.x >> 6] = b;
+        sh.skey[threadIdx.x >> 6] = b;
       }
       __syncthreads();
       lo = sh.key[0];
-      hi = sh.w[0];
+      hi = sh.skey[0];
       for (int i = 1; i < kWaves; ++i) {
         lo = min(lo, sh.key[i]);
-        hi = max(hi, sh.w[i]);
+        hi = max(hi, sh.skey[i]);
       }
-      first = false;
+      while (((hi - lo) >> shift) >= kBins) ++shift;
     }
-    int shift = 0;
-    while (((hi - lo) >> shift) >= kBins) ++shift;
     clear_bins(sh);
-    for_row(row, V, [&](int i, float x) {
-      const u64 k = order_key(x, i);
-      if (k < lo || k > hi) return;
-      const u64 w = weight(r, x);
-      if (w == 0 || range_of(r, x) != bin) return;
-      atomicAdd(&sh.mass[(k - lo) >> shift], w);
-      atomicAdd(&sh.count[(k - lo) >> shift], 1u);
+    for_row<1>(row, V, [&](int i, const float (&xs)[E]) {
+#pragma unroll 1
+      for (int e = 0; e < E; ++e) {
+        const float x = r.clean(xs[e]);
+        const u64 w = weight<true>(r, x);
+        if (w == 0) continue;
+        const int b = range_of(r, x);
+        int at = b;
+        if (!first) {
+          const u64 k = order_key(x, i + e);
+          if (b != bin || k < lo || k > hi) continue;
+          at = (int)((k - lo) >> shift);
+        }
+        atomicAdd(&sh.mass[at], w);
+        atomicAdd(&sh.count[at], 1u);
+      }
     });
     __syncthreads();
-    find_bin(sh, aim - (by_count ? c0 : m0), by_count);
-    c0 += sh.res[0];
-    m0 += sh.res[1];
-    size = sh.count[sh.bin];
-    lo += (u64)sh.bin << shift;
-    hi = min(hi, lo + ((1ull << shift) - 1));
+    u64 mall;
+    uint32_t call;
+    const Ends e = scan_bins(sh, mall, call);
+    if (by_count)
+      find_count(e, (uint32_t)(aim - c0), &sh.bins[0]);
+    else
+      find_mass(e, aim - m0, &sh.bins[0]);
     __syncthreads();
+    const int at = sh.bins[0];
+    const uint32_t size = sh.count[at + 1] - sh.count[at];
+    m0 += sh.mass[at];
+    c0 += sh.count[at];
+    if (first) {
+      bin = at;
+    } else {
+      lo += (u64)at << shift;
+      hi = min(hi, lo + ((1ull << shift) - 1));
+    }
+    first = false;
+    if (size <= kCap) break;
   }
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  for_row(row, V, [&](int i, float x) {
-    if (x == kNone || range_of(r, x) != bin) return;
-    const u64 k = order_key(x, i);
-    if (k < lo || k > hi) return;
-    const u64 w = weight(r, x);
-    if (w == 0) return;
-    const uint32_t at = atomicAdd(&sh.n_list, 1u);
-    sh.key[at] = k;
-    sh.w[at] = w;
+  for_row<1>(row, V, [&](int i, const float (&xs)[E]) {
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+      const float x = r.clean(xs[e]);
+      const u64 k = order_key(x, i + e);
+      if (range_of(r, x) != bin || k < lo || k > hi || weight<true>(r, x) == 0) continue;
+      sh.key[atomicAdd(&sh.n_list, 1u)] = k;
+    }
   });
   __syncthreads();
-  const uint32_t n = sh.n_list;
-  const u64 left = aim - (by_count ? c0 : m0);
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const u64 k = sh.key[i];
-    u64 m = 0;
-    uint32_t c = 0;
-    for (uint32_t j = 0; j < n; ++j) {
-      const bool before = sh.key[j] < k;
-      m += before ? sh.w[j] : 0ull;
-      c += before ? 1u : 0u;
-    }
-    const u64 b = by_count ? c : m, e = b + (by_count ? 1ull : sh.w[i]);
-    if (b < left && left <= e) {
-      sh.res[2] = m0 + m + sh.w[i];
-      sh.res[3] = k & 0xffffffffu;
+  const int n = (int)sh.n_list;
+  uint32_t c;
+  u64 w;
+  const u64 m = order_list(sh, r, n, false, &c, &w);
+  if ((int)threadIdx.x < n) {
+    const u64 left = aim - (by_count ? c0 : m0);
+    if (by_count ? left == c : m - w < left && left <= m) {
+      sh.got[0] = m0 + m;
+      sh.got[1] = sh.skey[threadIdx.x] & 0xffffffffu;
     }
   }
   __syncthreads();
-  *token = (int)sh.res[3];
-  const u64 got = sh.res[2];
+  *token = (int)sh.got[1];
+  const u64 got = sh.got[0];
   __syncthreads();
   return got;
-}
-
-// the histogram of the row; returns the weight of the tokens with at least `least`
-template <class T>
-__device__ u64 histogram(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 least) {
-  clear_bins(sh);
-  u64 strong = 0;
-  for_row(row, V, [&](int, float x) {
-    const u64 w = weight(r, x);
-    if (w == 0) return;
-    const int b = range_of(r, x);
-    atomicAdd(&sh.mass[b], w);
-    atomicAdd(&sh.count[b], 1u);
-    if (w >= least) strong += w;
-  });
-  u64 all;
-  block_scan(strong, sh.red, &all);
-  __syncthreads();
-  return all;
 }
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   __shared__ Shared sh;
+  constexpr int E = 16 / sizeof(T);
   const int row_i = blockIdx.x, V = a.V, tid = threadIdx.x;
   const T* row = static_cast<const T*>(a.logits) + row_i * a.stride;
   const float temp = a.temperature ? a.temperature[row_i] : 1.f;
+  const int top_k = a.top_k ? a.top_k[row_i] : 0;
+  const float top_p = a.top_p ? a.top_p[row_i] : 1.f;
+  const float min_p = a.min_p ? a.min_p[row_i] : 0.f;
+  const float u = a.u[row_i];
 
-  // the largest logit, the first token that has it, the smallest above -infinity
-  float mx = kNone, mn = __builtin_huge_valf();
-  int at = 0x7fffffff;
-  for_row(row, V, [&](int i, float x) {
-    if (x > mx) {
-      mx = x;
-      at = i;
+  // the largest and the smallest logit (fmax and fmin pass over NaN)
+  float mx = kNone, mn = -kNone;
+  for_row<4>(row, V, [&](int, const float (&xs)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      mx = fmaxf(mx, xs[e]);
+      mn = fminf(mn, xs[e]);
     }
-    if (x != kNone) mn = fminf(mn, x);
   });
+  const float mine = mx;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
-    const float ox = __shfl_xor(mx, d, 64);
-    const int oi = __shfl_xor(at, d, 64);
-    if (ox > mx || (ox == mx && oi < at)) {
-      mx = ox;
-      at = oi;
-    }
+    mx = fmaxf(mx, __shfl_xor(mx, d, 64));
     mn = fminf(mn, __shfl_xor(mn, d, 64));
   }
   if ((tid & 63) == 0) {
     sh.redf[0][tid >> 6] = mx;
     sh.redf[1][tid >> 6] = mn;
-    sh.redi[tid >> 6] = at;
   }
+  if (tid == 0) sh.n_list = 0;
   __syncthreads();
-  mx = sh.redf[0][0];
-  mn = sh.redf[1][0];
-  at = sh.redi[0];
-  for (int w = 1; w < kWaves; ++w) {
-    const float ox = sh.redf[0][w];
-    if (ox > mx || (ox == mx && sh.redi[w] < at)) {
-      mx = ox;
-      at = sh.redi[w];
-    }
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    mx = fmaxf(mx, sh.redf[0][w]);
     mn = fminf(mn, sh.redf[1][w]);
   }
-  __syncthreads();
-  if (mx == kNone || !(temp > 0.f)) {  // nothing to draw from, or the largest asked for
-    if (tid == 0) a.out[row_i] = mx == kNone ? -1 : at;
+  if (mx == kNone) {  // nothing to draw from
+    if (tid == 0) a.out[row_i] = -1;
+    return;
+  }
+  if (!(temp > 0.f)) {  // the first of the largest
+    int at = 0x7fffffff;
+    for_row<4>(row, V, [&](int i, const float (&xs)[E]) {
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (xs[e] == mx) at = min(at, i + e);
+    });
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) at = min(at, __shfl_xor(at, d, 64));
+    if ((tid & 63) == 0) sh.red[0].c[tid >> 6] = (uint32_t)at;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWaves; ++w) at = min(at, (int)sh.red[0].c[w]);
+      a.out[row_i] = at;
+    }
     return;
   }
 
   Row r;
+  r.top = mx == -kNone;
+  const u64 least = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFrac)) : 0ull;
+  const bool limit_p = top_p < 1.f;
+  // The ranges run over what has a weight, down to 30 nats or the smallest
+  // logit.  Numbers past those of any model take the passes of `reach` alone.
+  bool plain = fabsf(mx) <= 1e30f && temp >= 1e-20f && temp <= 1e20f;
+  if (r.top) mx = mn = 0.f;
   r.mx = mx;
-  r.inv_l2 = 1.4426950408889634074 / (double)temp;
-  r.inv = 1.f / temp;
-  // ranges over what has a weight: down to 30 nats, or to the smallest logit
-  const float span = fminf((mx - mn) * r.inv, 30.f);
-  r.fit = span > 0.f ? (float)kBins / span : 0.f;
+  r.scale = 1.4426950408889634074 / (double)temp;
+  r.least = mx - 31.f * fminf(temp, 1e30f);  // 44.7 powers of two down
+  const float span = fminf(mx - mn, 30.f * temp);
+  r.fit = span > 0.f ? fminf((float)kBins / span, 1e36f / fmaxf(fabsf(mx), 1.f)) : 0.f;
+  r.fit0 = mx * r.fit;
 
-  const float mp = a.min_p ? a.min_p[row_i] : 0.f;
-  const u64 least = mp > 0.f ? (u64)ceil((double)fminf(mp, 1.f) * (double)(1ull << kFrac)) : 0ull;
-  u64 kept = histogram(sh, r, row, V, least);  // by min-p
-  u64 all;
-  uint32_t live;
-  block_scan(sh.mass[2 * tid] + sh.mass[2 * tid + 1], sh.red, &all);
-  block_scan(sh.count[2 * tid] + sh.count[2 * tid + 1], sh.redc, &live);
-  __syncthreads();
-
-  // each filter keeps a beginning of the order, so the least of their weights is what all keep
-  int token = at;
-  u64 mass = all;
-  const int k = a.top_k ? a.top_k[row_i] : 0;
-  bool spoilt = false;  // the histogram was used for a smaller range
-  auto find = [&](u64 aim, bool by_count) {
-    if (spoilt) histogram(sh, r, row, V, 0);
-    find_bin(sh, aim, by_count);
-    spoilt = sh.count[sh.bin] > kCap;
+  // the list: for a small vocabulary all of it, for a small top-k the tokens
+  // down to the least of the k largest of the threads' maxima, else the ranges
+  // in which the running numbers get to where they have to
+  Interval iv[3];
+  iv[0] = {kNone, -kNone};
+  int n_iv = V <= kCap ? 1 : 0;
+  if (plain && n_iv == 0 && top_k > 0 && top_k <= kSmallK) {
+    clear_bins(sh);
+    const float t = place_of(r, mine);
+    const int b = mine != kNone ? range_of(r, mine) : kBins;
+    if (b < kBins) atomicAdd(&sh.count[b], 1u);
+    if (tid == 0) sh.rank[0] = 0;
     __syncthreads();
-    return reach(sh, r, row, V, aim, by_count, &token);
-  };
-  if (k > 0 && (uint32_t)k < live) mass = find(k, true);
-  const float tp = a.top_p ? a.top_p[row_i] : 1.f;
-  if (tp < 1.f) {
-    u64 aim = 1;
-    if (tp > 0.f) {
-      const u64 p = (u64)((double)tp * 18446744073709551616.0);
-      aim = max(aim, __umul64hi(p, mass) + (p * mass != 0 ? 1 : 0));
+    u64 mall;
+    uint32_t call;
+    const Ends e = scan_bins(sh, mall, call);
+    if ((uint32_t)top_k <= call) {
+      find_count(e, (uint32_t)top_k, &sh.bins[0]);
+      __syncthreads();
+      // the farthest place of those in the ranges so far
+      if (b <= sh.bins[0]) atomicMax(&sh.rank[0], rising(t));
+      __syncthreads();
+      iv[0].hi = next_up(from_rising(sh.rank[0]));
+      n_iv = 1;
     }
-    mass = find(aim, false);
   }
-  kept = min(kept, mass);
-  const float u = a.u[row_i];
-  u64 aim = 0;
-  if (u > 0.f) aim = __umul64hi((u64)((double)fminf(u, 0.99999994f) * 18446744073709551616.0), kept);
-  find(aim + 1, false);
+  const bool ranged = n_iv == 0;
+  u64 kept = ~0ull, all = 0;  // weight that min-p keeps; of all tokens
+  uint32_t live = 0;          // tokens that may have a weight
+  if (plain && ranged) {
+    clear_bins(sh);
+    u64 strong = histogram(sh, r, row, V, least, top_k > 0);
+    uint32_t none = 0;
+    __syncthreads();
+    const Ends e = scan_bins(sh, all, live);
+    if (least != 0) {
+      u64 sum;
+      block_scan(strong, none, sh.red[2], sum, none);
+      kept = sum;
+    }
+    // the ranges in which each number is reached, from the first that it can
+    // be to the last: top-k's, then with its weight between the ends of that
+    // range top-p's, and so on
+    u64 mlo = all, mhi = all;
+    int pl = -1, ph = -1;
+    const float end = next_up(place_of(r, r.least));
+    auto add = [&](int l, int h) {
+      if (l != pl || h != ph) iv[n_iv++] = {l > 0 ? (float)l : kNone, h < kBins - 1 ? (float)(h + 1) : end};
+      pl = l;
+      ph = h;
+    };
+    if (top_k > 0 && (uint32_t)top_k < live) {
+      find_count(e, (uint32_t)top_k, &sh.bins[0]);
+      __syncthreads();
+      add(sh.bins[0], sh.bins[0]);
+      mlo = sh.mass[pl] + 1;
+      mhi = sh.mass[ph + 1];
+    }
+    if (limit_p) {
+      find_mass(e, part_up(top_p, mlo), &sh.bins[2]);
+      find_mass(e, part_up(top_p, mhi), &sh.bins[3]);
+      __syncthreads();
+      add(sh.bins[2], sh.bins[3]);
+      mlo = sh.mass[pl] + 1;
+      mhi = sh.mass[ph + 1];
+    }
+    find_mass(e, part_past(u, min(mlo, kept)), &sh.bins[4]);
+    find_mass(e, part_past(u, min(mhi, kept)), &sh.bins[5]);
+    __syncthreads();
+    add(sh.bins[4], sh.bins[5]);
+  }
+  int n = kCap + 1;
+  if (plain) {
+    list_tokens(sh, r, row, V, n_iv, iv);
+    n = (int)sh.n_list;
+  }
+  if (n <= kCap) {
+    uint32_t c;
+    u64 w;
+    const u64 m = order_list(sh, r, n, ranged, &c, &w);
+    u64 mass = all;
+    if (!ranged) {
+      live = (uint32_t)n;
+      if (tid == n - 1) sh.got[0] = m;
+      // the last token that min-p keeps: weights fall along the order
+      if (least > 0 && tid < n && w >= least && (tid == n - 1 || weight<true>(r, key_logit(sh.skey[tid + 1])) < least))
+        sh.got[3] = m;
+    }
+    if (top_k > 0 && (uint32_t)top_k < live && tid < n && c == (uint32_t)top_k) sh.got[1] = m;
+    __syncthreads();
+    if (!ranged) {
+      mass = sh.got[0];
+      if (least > 0) kept = sh.got[3];
+    }
+    if (top_k > 0 && (uint32_t)top_k < live) mass = sh.got[1];
+    if (limit_p) {
+      const u64 aim = part_up(top_p, mass);
+      if (m - w < aim && aim <= m) sh.got[2] = m;
+      __syncthreads();
+      mass = sh.got[2];
+    }
+    const u64 aim = part_past(u, min(mass, kept));
+    if (m - w < aim && aim <= m) a.out[row_i] = (int32_t)(sh.skey[tid] & 0xffffffffu);
+    return;
+  }
+  // too many tokens in a range, or numbers past those of any model: one number
+  // after another
+  u64 strong = 0;
+  live = 0;
+  all = 0;
+  for_row<1>(row, V, [&](int, const float (&xs)[E]) {
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+      const u64 w = weight<true>(r, r.clean(xs[e]));
+      all += w;
+      live += w != 0;
+      if (w >= least) strong += w;
+    }
+  });
+  u64 mass;
+  uint32_t none = 0, tokens;
+  __syncthreads();
+  block_scan(all, live, sh.red[0], mass, tokens);
+  block_scan(strong, none, sh.red[1], kept, none);
+  int token = -1;
+  for (int step = 0; step < 3; ++step) {
+    u64 aim;
+    if (step == 0) {
+      if (!(top_k > 0 && (uint32_t)top_k < tokens)) continue;
+      aim = (u64)top_k;
+    } else if (step == 1) {
+      if (!limit_p) continue;
+      aim = part_up(top_p, mass);
+    } else {
+      aim = part_past(u, min(mass, kept));
+    }
+    mass = reach(sh, r, row, V, aim, step == 0, &token);
+  }
   if (tid == 0) a.out[row_i] = token;
 }
 
