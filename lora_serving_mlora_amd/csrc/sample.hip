@@ -32,18 +32,31 @@ constexpr int kFrac = 42;  // a weight of 1 is 2^42: 2^20 of them stay below 2^6
 constexpr int kSmallK = 512;  // largest top-k that is looked for among the threads' maxima
 constexpr float kNone = -__builtin_huge_valf();
 
-struct Shared {
+constexpr int kValues = 1 << 16;     // bf16 values
+constexpr int kValueVocab = 16384;  // smallest vocabulary whose bf16 values are counted
+
+struct Bins {
   __attribute__((aligned(16))) u64 mass[kBins + 2];  // histogram, then the weight before each range
   __attribute__((aligned(16))) uint32_t count[kBins + 4];
+};
+struct Red {  // of a running sum over the workgroup
+  u64 m[kWaves];
+  uint32_t c[kWaves];
+};
+// V: room for counts of every bf16 value, 16 bits each: word w holds that of
+// the bits w in its lower half and of w with the sign in its upper one
+template <bool V>
+struct SharedOf {
+  union {
+    Bins bins;
+    __attribute__((aligned(16))) uint32_t words[V ? kValues / 2 : 4];
+  };
   u64 key[kCap], skey[kCap];  // listed tokens (order and index), the same in order
   uint32_t rank[kCap];
-  struct Red {  // of a running sum over the workgroup
-    u64 m[kWaves];
-    uint32_t c[kWaves];
-  } red[3];
+  Red red[3];
   float redf[2][kWaves];
   u64 got[4];  // what one thread found for all
-  int bins[6];
+  int bin[6];
   uint32_t n_list;
 };
 
@@ -184,7 +197,7 @@ __device__ __forceinline__ u64 lane_value(u64 v, int l) {
 }
 // inclusive running sums of m and c over the workgroup's threads, in place;
 // the totals.  One barrier: `red` is free again after the next one.
-__device__ __forceinline__ void block_scan(u64& m, uint32_t& c, Shared::Red& red, u64& mall, uint32_t& call) {
+__device__ __forceinline__ void block_scan(u64& m, uint32_t& c, Red& red, u64& mall, uint32_t& call) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   m = wave_scan(m);
   c = wave_scan(c);
@@ -204,12 +217,13 @@ __device__ __forceinline__ void block_scan(u64& m, uint32_t& c, Shared::Red& red
   }
 }
 
-__device__ __forceinline__ void clear_bins(Shared& sh) {
+template <class S>
+__device__ __forceinline__ void clear_bins(S& sh) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    sh.mass[i * kThreads + threadIdx.x] = 0;
-    sh.count[i * kThreads + threadIdx.x] = 0;
+    sh.bins.mass[i * kThreads + threadIdx.x] = 0;
+    sh.bins.count[i * kThreads + threadIdx.x] = 0;
   }
   __syncthreads();
 }
@@ -220,12 +234,13 @@ struct Ends {
   u64 m[kPer + 1];
   uint32_t c[kPer + 1];
 };
-__device__ __forceinline__ Ends scan_bins(Shared& sh, u64& mass, uint32_t& count) {
+template <class S>
+__device__ __forceinline__ Ends scan_bins(S& sh, u64& mass, uint32_t& count) {
   static_assert(kPer == 4, "vector loads of a thread's ranges");
   const int t = threadIdx.x * kPer;
-  const ulonglong2 m01 = *reinterpret_cast<const ulonglong2*>(&sh.mass[t]);
-  const ulonglong2 m23 = *reinterpret_cast<const ulonglong2*>(&sh.mass[t + 2]);
-  const uint4 c = *reinterpret_cast<const uint4*>(&sh.count[t]);
+  const ulonglong2 m01 = *reinterpret_cast<const ulonglong2*>(&sh.bins.mass[t]);
+  const ulonglong2 m23 = *reinterpret_cast<const ulonglong2*>(&sh.bins.mass[t + 2]);
+  const uint4 c = *reinterpret_cast<const uint4*>(&sh.bins.count[t]);
   u64 m = m01.x + m01.y + m23.x + m23.y;
   uint32_t n = c.x + c.y + c.z + c.w;
   const u64 own = m;
@@ -242,12 +257,12 @@ __device__ __forceinline__ Ends scan_bins(Shared& sh, u64& mass, uint32_t& count
   e.c[2] = e.c[1] + c.y;
   e.c[3] = e.c[2] + c.z;
   e.c[4] = n;
-  *reinterpret_cast<ulonglong2*>(&sh.mass[t]) = make_ulonglong2(e.m[0], e.m[1]);
-  *reinterpret_cast<ulonglong2*>(&sh.mass[t + 2]) = make_ulonglong2(e.m[2], e.m[3]);
-  *reinterpret_cast<uint4*>(&sh.count[t]) = make_uint4(e.c[0], e.c[1], e.c[2], e.c[3]);
+  *reinterpret_cast<ulonglong2*>(&sh.bins.mass[t]) = make_ulonglong2(e.m[0], e.m[1]);
+  *reinterpret_cast<ulonglong2*>(&sh.bins.mass[t + 2]) = make_ulonglong2(e.m[2], e.m[3]);
+  *reinterpret_cast<uint4*>(&sh.bins.count[t]) = make_uint4(e.c[0], e.c[1], e.c[2], e.c[3]);
   if (threadIdx.x == kThreads - 1) {
-    sh.mass[kBins] = m;
-    sh.count[kBins] = n;
+    sh.bins.mass[kBins] = m;
+    sh.bins.count[kBins] = n;
   }
   __syncthreads();
   return e;
@@ -266,8 +281,8 @@ __device__ __forceinline__ void find_count(const Ends& e, uint32_t aim, int* bin
 
 // the histogram of the row; returns this thread's weight of the tokens with at
 // least `least`
-template <class T>
-__device__ __forceinline__ u64 histogram(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 least,
+template <class S, class T>
+__device__ __forceinline__ u64 histogram(S& sh, const Row& r, const T* __restrict__ row, int V, u64 least,
                                          bool counts) {
   u64 strong = 0;
   for_row<2>(row, V, [&](int, const float (&xs)[16 / sizeof(T)]) {
@@ -277,8 +292,8 @@ __device__ __forceinline__ u64 histogram(Shared& sh, const Row& r, const T* __re
       const u64 w = weight(r, x);
       const int b = range_of(r, x);
       if (x > r.least) {
-        atomicAdd(&sh.mass[b], w);
-        if (counts) atomicAdd(&sh.count[b], 1u);
+        atomicAdd(&sh.bins.mass[b], w);
+        if (counts) atomicAdd(&sh.bins.count[b], 1u);
       }
       if (least != 0 && w >= least) strong += w;
       if (e & 1) __builtin_amdgcn_sched_barrier(0);  // keeps the next logits' work out of the registers
@@ -293,8 +308,8 @@ __device__ __forceinline__ u64 histogram(Shared& sh, const Row& r, const T* __re
 struct Interval {
   float lo, hi;
 };
-template <int N, class T>
-__device__ __forceinline__ void list_in(Shared& sh, const Row& r, const T* __restrict__ row, int V,
+template <int N, class S, class T>
+__device__ __forceinline__ void list_in(S& sh, const Row& r, const T* __restrict__ row, int V,
                                         const Interval (&iv)[3]) {
   constexpr int E = 16 / sizeof(T);
   for_row<4>(row, V, [&](int i, const float (&xs)[E]) {
@@ -319,8 +334,8 @@ __device__ __forceinline__ void list_in(Shared& sh, const Row& r, const T* __res
   });
   __syncthreads();
 }
-template <class T>
-__device__ __forceinline__ void list_tokens(Shared& sh, const Row& r, const T* __restrict__ row, int V, int n,
+template <class S, class T>
+__device__ __forceinline__ void list_tokens(S& sh, const Row& r, const T* __restrict__ row, int V, int n,
                                             const Interval (&iv)[3]) {
   if (n == 1)
     list_in<1>(sh, r, row, V, iv);
@@ -335,7 +350,8 @@ __device__ __forceinline__ void list_tokens(Shared& sh, const Row& r, const T* _
 // its weight, all from the beginning of the order: what lies between the
 // listed ranges is taken from the histogram (`ranged`; else the list is the
 // beginning).
-__device__ __forceinline__ u64 order_list(Shared& sh, const Row& r, int n, bool ranged, uint32_t* c, u64* own) {
+template <class S>
+__device__ __forceinline__ u64 order_list(S& sh, const Row& r, int n, bool ranged, uint32_t* c, u64* own) {
   const int tid = threadIdx.x;
   sh.rank[tid] = 0;
   __syncthreads();
@@ -364,8 +380,8 @@ __device__ __forceinline__ u64 order_list(Shared& sh, const Row& r, int n, bool 
     if (ranged) {
       const int b = range_of(r, x), pb = tid > 0 ? range_of(r, key_logit(sh.skey[tid - 1])) : -1;
       if (b != pb) {  // the first of its range: what lies since the range listed before
-        m += sh.mass[b] - sh.mass[pb + 1];
-        k += sh.count[b] - sh.count[pb + 1];
+        m += sh.bins.mass[b] - sh.bins.mass[pb + 1];
+        k += sh.bins.count[b] - sh.bins.count[pb + 1];
       }
     }
   }
@@ -393,8 +409,8 @@ __device__ __forceinline__ u64 part_past(float u, u64 mass) {
 // The token at which the running count or weight of the order first reaches
 // `aim`, in whatever passes it takes: its index in *token, the weight up to
 // and with it as the result.  For ranges with more tokens than the list holds.
-template <class T>
-__device__ __forceinline__ u64 reach(Shared& sh, const Row& r, const T* __restrict__ row, int V, u64 aim,
+template <class S, class T>
+__device__ __forceinline__ u64 reach(S& sh, const Row& r, const T* __restrict__ row, int V, u64 aim,
                                      bool by_count, int* token) {
   constexpr int E = 16 / sizeof(T);
   u64 m0 = 0, c0 = 0;      // before the tokens looked at
@@ -449,8 +465,8 @@ __device__ __forceinline__ u64 reach(Shared& sh, const Row& r, const T* __restri
           if (b != bin || k < lo || k > hi) continue;
           at = (int)((k - lo) >> shift);
         }
-        atomicAdd(&sh.mass[at], w);
-        atomicAdd(&sh.count[at], 1u);
+        atomicAdd(&sh.bins.mass[at], w);
+        atomicAdd(&sh.bins.count[at], 1u);
       }
     });
     __syncthreads();
@@ -458,14 +474,14 @@ __device__ __forceinline__ u64 reach(Shared& sh, const Row& r, const T* __restri
     uint32_t call;
     const Ends e = scan_bins(sh, mall, call);
     if (by_count)
-      find_count(e, (uint32_t)(aim - c0), &sh.bins[0]);
+      find_count(e, (uint32_t)(aim - c0), &sh.bin[0]);
     else
-      find_mass(e, aim - m0, &sh.bins[0]);
+      find_mass(e, aim - m0, &sh.bin[0]);
     __syncthreads();
-    const int at = sh.bins[0];
-    const uint32_t size = sh.count[at + 1] - sh.count[at];
-    m0 += sh.mass[at];
-    c0 += sh.count[at];
+    const int at = sh.bin[0];
+    const uint32_t size = sh.bins.count[at + 1] - sh.bins.count[at];
+    m0 += sh.bins.mass[at];
+    c0 += sh.bins.count[at];
     if (first) {
       bin = at;
     } else {
@@ -505,9 +521,203 @@ __device__ __forceinline__ u64 reach(Shared& sh, const Row& r, const T* __restri
   return got;
 }
 
+// --- counts of every bf16 value ---------------------------------------------
+// Values in falling order: place 0 .. 32767 those without the sign, from bits
+// 0x7fff down, then those with it, from 0x8000 (-0, the same value as the one
+// before) up.  The ends are NaN.
+constexpr int kPlus0 = 32767, kMinus0 = 32768, kPlusInf = 0x7fff - 0x7f80;
+__device__ __forceinline__ float value_at(int place) {
+  return bf2f(place <= kPlus0 ? (uint32_t)(kPlus0 - place) : (uint32_t)place);
+}
+template <class S>
+__device__ __forceinline__ uint32_t count_at(const S& sh, int place) {
+  return place <= kPlus0 ? sh.words[kPlus0 - place] & 0xffffu : sh.words[place - kMinus0] >> 16;
+}
+constexpr int kGroup = kValues / kThreads;  // places of a group: a lane each, and a thread's share of the running sums
+static_assert(kGroup == 64, "a lane a place");
+
+// The place at which the running count or weight reaches `aim`, given the
+// running numbers before (c0, m0) and with (c1, m1) each thread's group of
+// places: the thread names its group, the first wave looks at the places side
+// by side.  The place in *place, how many of its tokens are needed in *nth, the
+// running weight with them as the result.
+template <class S>
+__device__ __forceinline__ u64 reach_value(S& sh, const Row& r, u64 aim, bool by_count, u64 m0, u64 m1, uint32_t c0,
+                                           uint32_t c1, int* place, uint32_t* nth) {
+  const int tid = threadIdx.x;
+  if (by_count ? c0 < aim && aim <= c1 : m0 < aim && aim <= m1) {
+    sh.bin[0] = tid;
+    sh.got[0] = m0;
+    sh.got[1] = c0;
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const int at = sh.bin[0] * kGroup + tid;
+    const float x = value_at(at);
+    const bool has = at >= kPlusInf && x > r.least;  // no NaN
+    const uint32_t n = has ? count_at(sh, at) : 0;
+    const u64 w = has ? weight(r, x) : 0;
+    const u64 m = wave_scan((u64)n * w) + sh.got[0], mb = m - n * w;
+    const uint32_t c = wave_scan(n) + (uint32_t)sh.got[1], cb = c - n;
+    if (by_count ? cb < aim && aim <= c : mb < aim && aim <= m) {
+      const uint32_t need = by_count ? (uint32_t)aim - cb : (uint32_t)((aim - mb + w - 1) / w);
+      sh.bin[1] = at;
+      sh.bin[2] = (int)need;
+      sh.got[2] = mb + need * w;
+    }
+  }
+  __syncthreads();
+  *place = sh.bin[1];
+  *nth = (uint32_t)sh.bin[2];
+  return sh.got[2];
+}
+
+// A row of bf16 logits by the counts of their values: one pass counts, then
+// all is settled among the values but for the index of the token drawn, which
+// another pass finds.  False (nothing drawn) where a count overran its 16
+// bits, the numbers are past those of any model, or more tokens than the list
+// holds share the value drawn.
+template <class S>
+__device__ __forceinline__ bool sample_values(S& sh, const uint16_t* __restrict__ row, int V, float temp, int top_k,
+                                              float top_p, float min_p, float u, int32_t* out) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kClear = kValues / 2 / 4 / kThreads;
+  uint4* words = reinterpret_cast<uint4*>(sh.words);
+#pragma unroll
+  for (int i = 0; i < kClear; ++i) words[i * kThreads + tid] = make_uint4(0u, 0u, 0u, 0u);
+  u64* group_mass = sh.key;
+  uint32_t* group_count = sh.rank;
+  group_mass[tid] = 0;
+  group_count[tid] = 0;
+  if (tid == 0) sh.n_list = 0;
+  __syncthreads();
+  float mx = kNone;
+  for_row<4>(row, V, [&](int, const float (&xs)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = __float_as_uint(xs[e]);
+      mx = fmaxf(mx, xs[e]);
+      atomicAdd(&sh.words[(b >> 16) & 0x7fffu], (b >> 31) ? 0x10000u : 1u);
+    }
+  });
+  __syncthreads();
+  // the largest logit; all counts together tell whether one overran (the
+  // pieces at the ends of the row count a NaN for each logit that they lack)
+  uint32_t sum = 0, all_held;
+  u64 none = 0, nothing;
+#pragma unroll
+  for (int i = 0; i < kClear; ++i) {
+    const uint4 w = words[i * kThreads + tid];
+    sum = __builtin_amdgcn_sad_u16(w.x, 0, sum);
+    sum = __builtin_amdgcn_sad_u16(w.y, 0, sum);
+    sum = __builtin_amdgcn_sad_u16(w.z, 0, sum);
+    sum = __builtin_amdgcn_sad_u16(w.w, 0, sum);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
+  if (lane == 0) sh.redf[0][wave] = mx;
+  block_scan(none, sum, sh.red[0], nothing, all_held);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sh.redf[0][w]);
+  const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2));
+  if (all_held != (uint32_t)(V + 7 * (head + (V - head) % 8))) return false;
+  if (mx == kNone) {  // nothing to draw from
+    if (tid == 0) *out = -1;
+    return true;
+  }
+  float x = mx;
+  uint32_t nth = 1;
+  int place = -1;
+  if (temp > 0.f) {
+    if (!(fabsf(mx) <= 1e30f && temp >= 1e-20f && temp <= 1e20f)) return false;
+    Row r;
+    r.mx = mx;
+    r.scale = 1.4426950408889634074 / (double)temp;
+    r.least = mx - 31.f * temp;
+    r.top = false;
+    r.fit = r.fit0 = 0.f;
+    const u64 least = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFrac)) : 0ull;
+    // weight and count of the groups that hold the largest logit down to r.least
+    auto group_of = [](float v) {
+      const uint32_t b = __float_as_uint(v) >> 16;
+      return (int)((b & 0x8000u) ? b : kPlus0 - b) / kGroup;
+    };
+    const int last = group_of(r.least);
+    u64 strong = 0;
+    int g = group_of(mx) + wave;
+    uint32_t next = count_at(sh, min(g, last) * kGroup + lane);
+    for (; g <= last; g += kWaves) {
+      uint32_t n = next;
+      next = count_at(sh, min(g + kWaves, last) * kGroup + lane);
+      if (__ballot(n != 0) == 0) continue;  // most are empty
+      const int at = g * kGroup + lane;
+      const float v = value_at(at);
+      if (at < kPlusInf || !(v > r.least)) n = 0;
+      const u64 w = n != 0 ? weight(r, v) : 0;
+      const u64 m = wave_scan(n * w);
+      if (w >= least) strong += n * w;
+      if (lane == 63) group_mass[g] = m;
+      if (top_k > 0) {
+        const uint32_t c = wave_scan(n);
+        if (lane == 63) group_count[g] = c;
+      }
+    }
+    __syncthreads();
+    const u64 m = group_mass[tid];
+    const uint32_t n = group_count[tid];
+    u64 m1 = m, all, kept;
+    uint32_t c1 = n, live, zero = 0;
+    block_scan(m1, c1, sh.red[1], all, live);
+    if (least != 0) {
+      block_scan(strong, zero, sh.red[2], kept, zero);
+    } else {
+      kept = all;
+    }
+    const u64 m0 = m1 - m;
+    const uint32_t c0 = c1 - n;
+    u64 mass = all;
+    if (top_k > 0 && (uint32_t)top_k < live)
+      mass = reach_value(sh, r, (u64)top_k, true, m0, m1, c0, c1, &place, &nth);
+    if (top_p < 1.f) mass = reach_value(sh, r, part_up(top_p, mass), false, m0, m1, c0, c1, &place, &nth);
+    reach_value(sh, r, part_past(u, min(mass, kept)), false, m0, m1, c0, c1, &place, &nth);
+    x = value_at(place);
+  }
+  // the nth token of that value (0: of either sign, those without it first)
+  const uint32_t b = __float_as_uint(x) >> 16;
+  uint32_t same;
+  if ((b & 0x7fffu) == 0) {
+    const uint32_t n0 = count_at(sh, kPlus0);
+    same = n0 + count_at(sh, kMinus0);
+    if (place == kMinus0) nth += n0;
+  } else {
+    same = count_at(sh, (b & 0x8000u) ? (int)b : kPlus0 - (int)b);
+  }
+  if (same > kCap) return false;
+  uint32_t* list = sh.rank;  // the groups' counts are not needed any more
+  for_row<4>(row, V, [&](int i, const float (&xs)[8]) {
+    uint32_t hit = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hit |= xs[e] == x ? 1u << e : 0u;
+    while (hit) {
+      const int e = __builtin_ctz(hit);
+      hit &= hit - 1;
+      list[atomicAdd(&sh.n_list, 1u)] = (uint32_t)(i + e);
+    }
+  });
+  __syncthreads();
+  if (tid < (int)same) {
+    const uint32_t i = list[tid];
+    uint32_t before = 0;
+#pragma unroll 4
+    for (uint32_t j = 0; j < same; ++j) before += list[j] < i ? 1u : 0u;
+    if (before == nth - 1) *out = (int32_t)i;
+  }
+  return true;
+}
+
 template <class T>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
-  __shared__ Shared sh;
+  __shared__ SharedOf<sizeof(T) == 2> sh;
   constexpr int E = 16 / sizeof(T);
   const int row_i = blockIdx.x, V = a.V, tid = threadIdx.x;
   const T* row = static_cast<const T*>(a.logits) + row_i * a.stride;
@@ -516,6 +726,13 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   const float top_p = a.top_p ? a.top_p[row_i] : 1.f;
   const float min_p = a.min_p ? a.min_p[row_i] : 0.f;
   const float u = a.u[row_i];
+
+  if constexpr (sizeof(T) == 2) {
+    if (V >= kValueVocab && !(temp > 0.f && top_k > 0 && top_k <= kSmallK)) {
+      if (sample_values(sh, row, V, temp, top_k, top_p, min_p, u, a.out + row_i)) return;
+      __syncthreads();
+    }
+  }
 
   // the largest and the smallest logit (fmax and fmin pass over NaN)
   float mx = kNone, mn = -kNone;
@@ -590,17 +807,17 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     clear_bins(sh);
     const float t = place_of(r, mine);
     const int b = mine != kNone ? range_of(r, mine) : kBins;
-    if (b < kBins) atomicAdd(&sh.count[b], 1u);
+    if (b < kBins) atomicAdd(&sh.bins.count[b], 1u);
     if (tid == 0) sh.rank[0] = 0;
     __syncthreads();
     u64 mall;
     uint32_t call;
     const Ends e = scan_bins(sh, mall, call);
     if ((uint32_t)top_k <= call) {
-      find_count(e, (uint32_t)top_k, &sh.bins[0]);
+      find_count(e, (uint32_t)top_k, &sh.bin[0]);
       __syncthreads();
       // the farthest place of those in the ranges so far
-      if (b <= sh.bins[0]) atomicMax(&sh.rank[0], rising(t));
+      if (b <= sh.bin[0]) atomicMax(&sh.rank[0], rising(t));
       __syncthreads();
       iv[0].hi = next_up(from_rising(sh.rank[0]));
       n_iv = 1;
@@ -632,24 +849,24 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
       ph = h;
     };
     if (top_k > 0 && (uint32_t)top_k < live) {
-      find_count(e, (uint32_t)top_k, &sh.bins[0]);
+      find_count(e, (uint32_t)top_k, &sh.bin[0]);
       __syncthreads();
-      add(sh.bins[0], sh.bins[0]);
-      mlo = sh.mass[pl] + 1;
-      mhi = sh.mass[ph + 1];
+      add(sh.bin[0], sh.bin[0]);
+      mlo = sh.bins.mass[pl] + 1;
+      mhi = sh.bins.mass[ph + 1];
     }
     if (limit_p) {
-      find_mass(e, part_up(top_p, mlo), &sh.bins[2]);
-      find_mass(e, part_up(top_p, mhi), &sh.bins[3]);
+      find_mass(e, part_up(top_p, mlo), &sh.bin[2]);
+      find_mass(e, part_up(top_p, mhi), &sh.bin[3]);
       __syncthreads();
-      add(sh.bins[2], sh.bins[3]);
-      mlo = sh.mass[pl] + 1;
-      mhi = sh.mass[ph + 1];
+      add(sh.bin[2], sh.bin[3]);
+      mlo = sh.bins.mass[pl] + 1;
+      mhi = sh.bins.mass[ph + 1];
     }
-    find_mass(e, part_past(u, min(mlo, kept)), &sh.bins[4]);
-    find_mass(e, part_past(u, min(mhi, kept)), &sh.bins[5]);
+    find_mass(e, part_past(u, min(mlo, kept)), &sh.bin[4]);
+    find_mass(e, part_past(u, min(mhi, kept)), &sh.bin[5]);
     __syncthreads();
-    add(sh.bins[4], sh.bins[5]);
+    add(sh.bin[4], sh.bin[5]);
   }
   int n = kCap + 1;
   if (plain) {
