@@ -1293,12 +1293,14 @@ mlora_status q4_view(const mlora_q4_weight* w, mlora::Q4View* v) {
   *v = {w->codes, w->scales, w->din, w->dout};
   return MLORA_OK;
 }
-bool q4_few(const mlora_pool* p, int n) { return n <= mlora::kQ4Rows && (!p || (aligned16(p->d.down_pages))); }
+bool q4_few(const mlora::Q4View& w, const mlora_pool* p, int n) {
+  return n <= mlora::kQ4Rows && w.K >= mlora::kQ4MinDin && (!p || aligned16(p->d.down_pages));
+}
 // work of a product: few rows the per-row T region (with a pool) and the
 // partial products; more rows the bf16 weight, then the bf16 product's own
 size_t q4_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
   if (n <= 0) return 0;
-  if (q4_few(p, n))
+  if (q4_few(w, p, n))
     return (p ? rows_t_bytes(p, n) : 0) +
            align256(mlora::q4_plan(n, w.K, w.N, p != nullptr).part_floats(n, w.N) * sizeof(float));
   const size_t weight = align256((size_t)w.K * w.N * 2);
@@ -1354,7 +1356,7 @@ mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t
   if (!X || !Y || !aligned16(X)) return fail(MLORA_EINVAL, "X and Y must not be NULL, X 16-byte aligned");
   if ((st = q4_work(v, nullptr, n, work, work_bytes)) != MLORA_OK) return st;
   hipStream_t s = as_stream(stream);
-  if (q4_few(nullptr, n))
+  if (q4_few(v, nullptr, n))
     return hip_check(mlora::launch_q4_rows(v, X, n, Y, static_cast<float*>(work), nullptr, 0, nullptr, nullptr, s),
                      "4-bit product launch");
   uint16_t* W = static_cast<uint16_t*>(work);
@@ -1381,7 +1383,7 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
   if (n == 0) return MLORA_OK;
   if (!X || !Y || !aligned16(X)) return fail(MLORA_EINVAL, "X and Y must not be NULL, X 16-byte aligned");
   if ((st = q4_work(v, p, n, work, work_bytes)) != MLORA_OK) return st;
-  if (q4_few(p, n)) {
+  if (q4_few(v, p, n)) {
     const PoolView pv = p->view();
     float* T = static_cast<float*>(work);
     float* part = reinterpret_cast<float*>(static_cast<char*>(work) + rows_t_bytes(p, n));

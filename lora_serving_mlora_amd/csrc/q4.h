@@ -35,16 +35,17 @@ hipError_t launch_q4_quantize(const uint16_t* W, uint8_t* codes, uint8_t* scales
 hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* W, int64_t n,
                                 hipStream_t stream);
 
-// Batches of at most this many rows multiply the codes as they are; larger
-// ones make the weight bf16 first and take the bf16 products.
-constexpr int kQ4Rows = 64;
+// Batches of at most this many rows (of at least kQ4MinDin channels) multiply
+// the codes as they are; larger ones make the weight bf16 first and take the bf16 products.
+constexpr int kQ4Rows = 64, kQ4MinDin = 128;
 // The form of a product of M rows: workgroups of 16 * cg columns, K in S
 // slices.  Without the low-rank term and with one slice the product is
 // written as it is; else partial products [S][M][N] go to scratch and a
 // finish pass sums them.
 struct Q4Plan {
-  int cg, S, xs_stride;
+  int cg, S;
   bool direct;
+  int SK;  // slices of din of the low-rank inner product
   size_t part_floats(int M, int N) const { return direct ? 0 : (size_t)S * M * N; }
 };
 Q4Plan q4_plan(int M, int K, int N, bool lora);

@@ -66,135 +66,288 @@ __global__ __launch_bounds__(kConvThreads) void q4_dequantize_kernel(const uint8
 // Products of up to 64 rows.  What bounds them is the codes' way from memory,
 // so each code is read once, by the lane whose operand it is: a lane takes
 // the 16 bytes (32 channels, one group) of one column at a time, the 16
-// columns of a wave by the 4 lane groups' next groups of channels, and feeds
+// columns of a group by the 4 lane groups' next groups of channels, and feeds
 // them as four 16x16x32 products.  Which channel stands where in K is free as
-// long as X agrees, so X is read from LDS in the same order.  8 waves: CG
-// column groups of 16, 8 / CG shares of the slice of K (its 128-channel steps
-// dealt in turn), summed through LDS in order.
-// LDS: X slice [M][xs_stride] in 1 KiB blocks whose 16-byte chunks are
-// XOR-swizzled by (row & 15), so that the 16 rows of a fragment hit 16
-// different chunk positions.
+// long as X agrees.  A workgroup has 16 * CG columns and a slice of K; its
+// waves take shares of the slice and all of the columns each, so that no two
+// of them need the same codes or the same part of X, and there is no barrier
+// before the shares are summed through LDS in order.
+// Codes and X come through LDS all the same, a wave's own: whole row pieces (64
+// bytes of codes, 256 of X) whose 16-byte chunks are XOR-ed with the row, so
+// that the 16 rows of an operand hit different banks.  (Operands loaded from
+// memory as they are have a row to a lane, which the address unit takes four
+// times as long for: 61 rows of 11008 channels 23.5 us, X alone through LDS
+// 18.8.)
+// Codes and X run D steps of 128 channels ahead.  With the low-rank term the
+// workgroups also compute T = Down x, a row and a slice of din at a time, while
+// their first codes are on the way.
 // ---------------------------------------------------------------------------
-constexpr int kRowsWaves = 8, kStep = 128, kRound = 4;
-constexpr size_t kXsMax = 128 << 10;  // bytes of LDS for X
+constexpr int kStep = 128, kStepGroups = kStep / kQ4Group;
 
-template <int MB, int CG, bool LORA>
-__global__ __launch_bounds__(64 * kRowsWaves) void q4_rows_kernel(Q4View w, const uint16_t* __restrict__ X, int M,
-                                                                  int S, int xs_stride, uint16_t* __restrict__ Y,
-                                                                  float* __restrict__ part, PoolView pv, int proj,
-                                                                  const int32_t* __restrict__ row_key,
-                                                                  float* __restrict__ T, int n_shrink) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t xs[];
-  constexpr int KH = kRowsWaves / CG;
-  if (LORA && (int)blockIdx.x < n_shrink) {
-    for (int k = blockIdx.x; k < M; k += n_shrink)
-      shrink_row_body<true, kRowsWaves>(pv, proj, X, row_key, k, T, row_desc(T, M, pv.max_rank));
-    return;
-  }
-  const int K = w.K, N = w.N, G = K / kQ4Group;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int cg = wave % CG, kh = wave / CG;
-  const int ncb = (N + 16 * CG - 1) / (16 * CG);
-  const int b = (int)blockIdx.x - (LORA ? n_shrink : 0);
-  const int cb = b % ncb, kq = b / ncb;
-  const int steps = (K + kStep - 1) / kStep;
-  const int s0 = (int)((long)steps * kq / S), ns = (int)((long)steps * (kq + 1) / S) - s0;
-  const int k0 = s0 * kStep, Kq = min(ns * kStep, K - k0);
-  const int r16 = lane & 15, q = lane >> 4;
+// a place that is the same for the whole wave: a scalar load (the pool's and
+// the batch's tables, which do not change while a kernel runs)
+template <class T>
+__device__ __forceinline__ T scalar(const T* p) {
+  typedef const T __attribute__((address_space(4))) * constant;
+  return *(constant)(uintptr_t)p;
+}
 
-  // X slice -> LDS: instruction (row r, 1 KiB block bl); lane l fetches chunk
-  // l ^ (r & 15) of the block into place l; nothing is fetched past the slice
-  const __amdgpu_buffer_rsrc_t rx =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(X), (short)0, M * K * 2, 0x00020000);
-  const int blocks = (Kq + 511) / 512;
-  for (int i = wave; i < M * blocks; i += kRowsWaves) {
-    const int r = i / blocks, bl = i % blocks;
-    if (bl * 64 + (lane ^ (r & 15)) < Kq / 8)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, xs + (size_t)r * xs_stride + bl * 512, 16,
-                                               (lane ^ (r & 15)) * 16, (r * K + k0 + bl * 512) * 2, 0, 0);
-  }
+// s_waitcnt immediate for "vmcnt <= v" (expcnt and lgkmcnt not waited)
+constexpr int vmcnt_imm(int v) { return (v & 15) | ((v >> 4) << 14) | (7 << 4) | (15 << 8); }
 
-  // the codes and scale bytes of kRound steps of this wave, from its step
-  // kh + KH * i on; past the weight's end the last group is read again
-  const int col = min(cb * 16 * CG + 16 * cg + r16, N - 1);
-  const uint8_t* wc = w.codes + (size_t)col * (K / 2);
-  const uint8_t* ws = w.scales + (size_t)col * G;
-  uint4 code[kRound], code_n[kRound];
-  uint32_t sb[kRound], sb_n[kRound];
-  auto fetch = [&](int i, uint4 (&c)[kRound], uint32_t (&s)[kRound]) {
+// Slice `sl` of SK of row k's low-rank inner product, T[sl][k][q] = Down[q] . x
+// over its channels (the scale is left out); slice 0 also writes the row's
+// descriptor.  A wave takes R ranks at a time, its lanes 8 channels each.
+template <int NW>
+__device__ __forceinline__ void shrink_slice(const PoolView& pv, int proj, const uint16_t* __restrict__ X,
+                                             const int32_t* __restrict__ row_key, int M, int k, int sl, int SK,
+                                             float* __restrict__ T) {
+  constexpr int R = 16 / NW;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int key = scalar(row_key + k);
+  if (sl == 0) write_row_desc(pv, proj, key, k, row_desc(T, M, pv.max_rank));
+  if (key < 0) return;
+  const int rank = scalar(pv.rank + key);
+  const int32_t* dpage = pv.down_page + ((size_t)key * pv.n_proj + proj) * pv.max_rank;
+  const int n8 = pv.din / 8, b0 = (int)((long)n8 * sl / SK), b1 = (int)((long)n8 * (sl + 1) / SK);
+  const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)k * pv.din);
+  for (int q0 = R * wave; q0 < rank; q0 += R * NW) {
+    const uint4* d[R];
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      const int g = min((s0 + kh + KH * (i + u)) * (kStep / kQ4Group) + q, G - 1);
-      c[u] = *reinterpret_cast<const uint4*>(wc + (size_t)g * 16);
-      s[u] = ws[g];
-    }
-  };
-  fetch(0, code, sb);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-
-  floatx4 acc[MB];
+    for (int e = 0; e < R; ++e)
+      d[e] = reinterpret_cast<const uint4*>(pv.down + (size_t)scalar(dpage + min(q0 + e, rank - 1)) * pv.din);
+    float v[R];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) acc[mb] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int mine = (ns - kh + KH - 1) / KH;  // steps of this wave
-  for (int i = 0; i < mine; i += kRound) {
-    if (i + kRound < mine) fetch(i + kRound, code_n, sb_n);
+    for (int e = 0; e < R; ++e) v[e] = 0.f;
+    constexpr int U = 4;
+    for (int i = b0 + lane; i < b1; i += 64 * U) {
+      uint4 x[U], w[U][R];
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      if (i + u < mine) {
-        const int s = kh + KH * (i + u);
-        const bool in = (s0 + s) * (kStep / kQ4Group) + q < G;  // false in the last step of a ragged K
-        const float scale = in ? q4_scale(sb[u]) : 1.f;
-        const uint32_t dw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+      for (int u = 0; u < U; ++u) {
+        const int at = min(i + 64 * u, b1 - 1);
+        x[u] = xr[at];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 f = q4_bf8(in ? dw[j] : 0u, scale);
-          const int c = s * 16 + q * 4 + j;  // 16-byte chunk of the slice row
+        for (int e = 0; e < R; ++e) w[u][e] = d[e][at];
+      }
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) {
-            const int r = min(mb * 16 + r16, M - 1);
-            uint4 a = *reinterpret_cast<const uint4*>(xs + (size_t)r * xs_stride + (c >> 6) * 512 +
-                                                      (((c & 63) ^ (r & 15)) << 3));
-            if (!in) a = make_uint4(0u, 0u, 0u, 0u);
-            acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(f), acc[mb], 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        if (i + 64 * u >= b1) x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i + 64 * u < b1) {
+          const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int e = 0; e < R; ++e) {
+            const uint32_t ww[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              v[e] = fmaf(lo_bf(ww[f]), lo_bf(xw[f]), v[e]);
+              v[e] = fmaf(hi_bf(ww[f]), hi_bf(xw[f]), v[e]);
+            }
           }
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      code[u] = code_n[u];
-      sb[u] = sb_n[u];
+    // halves of the wave, then quarters for four ranks, sum a rank each
+    float t;
+    int mine;
+    if constexpr (R == 2) {
+      const bool up = (lane & 32) != 0;
+      t = (up ? v[1] : v[0]) + __shfl_xor(up ? v[0] : v[1], 32, 64);
+      t += __shfl_xor(t, 16, 64);
+      mine = up ? 1 : 0;
+    } else {
+      static_assert(R == 4, "two or four ranks a wave");
+      const bool up = (lane & 32) != 0, odd = (lane & 16) != 0;
+      const float a = (up ? v[2] : v[0]) + __shfl_xor(up ? v[0] : v[2], 32, 64);
+      const float b = (up ? v[3] : v[1]) + __shfl_xor(up ? v[1] : v[3], 32, 64);
+      t = (odd ? b : a) + __shfl_xor(odd ? a : b, 16, 64);
+      mine = (up ? 2 : 0) + (odd ? 1 : 0);
     }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) t += __shfl_xor(t, m, 64);
+    if ((lane & (R == 2 ? 31 : 15)) == 0 && q0 + mine < rank) T[((size_t)sl * M + k) * pv.max_rank + q0 + mine] = t;
+  }
+}
+
+// The body of q4_rows_kernel.  x0 .. x3: LDS for a step, a slot of every
+// wave's (16 * MB rows of 256 bytes of X, 16 * CG of 64 bytes of codes); arrays
+// of their own, so that the compiler knows that reads of one do not wait for
+// what is on its way into another (the first D of them are used).
+template <int MB, int CG, int NW, int D, bool LORA>
+__device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __restrict__ X, int M, int S,
+                                             uint16_t* __restrict__ Y, float* __restrict__ part, const PoolView& pv,
+                                             int proj, const int32_t* __restrict__ row_key, float* __restrict__ T,
+                                             int SK, uint8_t* __restrict__ x0, uint8_t* __restrict__ x1,
+                                             uint8_t* __restrict__ x2, uint8_t* __restrict__ x3) {
+  static_assert(CG <= 4 && D >= 2 && D <= 4, "the waves' sums fit in a slot; slots are named below");
+  const int K = w.K, N = w.N, G = K / kQ4Group;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ncb = (N + 16 * CG - 1) / (16 * CG);
+  const int cb = (int)blockIdx.x % ncb, kq = (int)blockIdx.x / ncb;
+  const int steps = (K + kStep - 1) / kStep;
+  // this wave's steps [u0, u0 + mine) of the NW * S shares of K
+  const int u0 = (int)((long)steps * (kq * NW + wave) / (NW * S));
+  const int mine = (int)((long)steps * (kq * NW + wave + 1) / (NW * S)) - u0;
+  const int r16 = lane & 15, q = lane >> 4;
+
+  const int n0 = cb * 16 * CG, cols = min(16 * CG, N - n0);
+  const uint8_t* wc = w.codes + (size_t)n0 * (K / 2);
+  const uint8_t* ws = w.scales + (size_t)n0 * G;
+  constexpr int kX = MB * 4096, kSlot = kX + CG * 1024;  // bytes of a wave
+  uint32_t sb[D];                             // scale bytes of a step: lane l holds column l's four
+  constexpr int kLoads = 4 * MB + CG + 1;     // of a step
+  const int scol = min(lane, cols - 1), send = cols * G - 4;
+  // one step's part of X (four rows an instruction), codes and scales.  Past
+  // the end of a row X reads on (the next row, or zeros past the last) and the
+  // last group is read again; both count for nothing below.  A step past this
+  // wave's last makes the same loads of empty buffers, so that what is on its
+  // way can be told by its number.
+  auto fetch = [&](int u, uint8_t* slot, uint32_t& sv) {
+    const bool any = u < mine;
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(X), (short)0, any ? M * K * 2 : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wc), (short)0, any ? cols * (K / 2) : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ws), (short)0, any ? cols * G : 0, 0x00020000);
+    const int g0 = (u0 + u) * kStepGroups;
+#pragma unroll
+    for (int c = 0; c < CG; ++c) {
+      const int row = 16 * c + (lane >> 2), g = min(g0 + ((lane ^ (lane >> 4)) & 3), G - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, slot + wave * kSlot + kX + c * 1024, 16,
+                                               min(row, cols - 1) * (K / 2) + g * 16, 0, 0, 0);
+    }
+    sv = __builtin_amdgcn_raw_buffer_load_b32(rs, min(scol * G + g0, send), 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4 * MB; ++i) {
+      const int row = 4 * i + q, r = min(row, M - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, slot + wave * kSlot + i * 1024, 16,
+                                               r * 2 * K + ((r16 ^ (row & 15)) << 4), (u0 + u) * kStep * 2, 0, 0);
+    }
+    asm volatile("" ::: "memory");
+  };
+  auto slot_of = [&](int d) { return d == 0 ? x0 : (d == 1 ? x1 : (d == 2 ? x2 : x3)); };
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, slot_of(d), sb[d]);
+
+  if (LORA) {
+    for (int t = blockIdx.x; t < M * SK; t += gridDim.x) shrink_slice<NW>(pv, proj, X, row_key, M, t % M, t / M, SK, T);
   }
 
-  // the shares of K, in order
-  __syncthreads();
-  floatx4* red = reinterpret_cast<floatx4*>(xs);  // [KH - 1][CG][MB][64]
-  if (kh > 0) {
+  floatx4 acc[CG][MB];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) red[(((kh - 1) * CG + cg) * MB + mb) * 64 + lane] = acc[mb];
+  for (int c = 0; c < CG; ++c)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) acc[c][mb] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int u, const uint8_t* slot, uint32_t sv) {
+    const uint8_t* xs = slot + wave * kSlot;
+    uint4 xf[MB][4], code[CG];
+    float scale[CG];
+    const int g0 = (u0 + u) * kStepGroups;
+#pragma unroll
+    for (int c = 0; c < CG; ++c) {
+      code[c] = *reinterpret_cast<const uint4*>(xs + kX + (16 * c + r16) * 64 + ((q ^ (r16 >> 2)) << 4));
+      const int from = min(16 * c + r16, cols - 1);
+      const uint32_t four = (uint32_t)__builtin_amdgcn_ds_bpermute(from * 4, (int)sv);
+      scale[c] = q4_scale((four >> (8 * (q + max(from * G + g0 - send, 0)) & 31)) & 255u);
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        xf[mb][j] = *reinterpret_cast<const uint4*>(xs + (16 * mb + r16) * 256 + (((4 * q + j) ^ r16) << 4));
+    if (g0 + kStepGroups > G) {  // the last step of a ragged K
+      const bool in = g0 + q < G;
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+        code[c].x = in ? code[c].x : 0u;
+        code[c].y = in ? code[c].y : 0u;
+        code[c].z = in ? code[c].z : 0u;
+        code[c].w = in ? code[c].w : 0u;
+        scale[c] = in ? scale[c] : 1.f;
+      }
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          xf[mb][j].x = in ? xf[mb][j].x : 0u;
+          xf[mb][j].y = in ? xf[mb][j].y : 0u;
+          xf[mb][j].z = in ? xf[mb][j].z : 0u;
+          xf[mb][j].w = in ? xf[mb][j].w : 0u;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+        const uint4 v = code[c];
+        const uint4 f = q4_bf8(j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w)), scale[c]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+          acc[c][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf[mb][j]), as_bf16x8(f), acc[c][mb], 0, 0, 0);
+      }
+  };
+  int i = 0;
+  for (; i + D < mine; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((D - 1) * kLoads));  // this step has landed, those after it may not have
+      asm volatile("" ::: "memory");
+      multiply(i + d, slot_of(d), sb[d]);
+      // the slot's reads are done before it is filled again
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15 << 8));
+      fetch(i + d + D, slot_of(d), sb[d]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < D; ++d) {  // the last steps
+    if (D - 1 - d == 3)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(3 * kLoads));
+    else if (D - 1 - d == 2)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * kLoads));
+    else if (D - 1 - d == 1)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));
+    else
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    asm volatile("" ::: "memory");
+    if (i + d < mine) multiply(i + d, slot_of(d), sb[d]);
+  }
+
+  // the waves' shares of K, in order; a thread takes four rows of a column
+  __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (kh > 0) return;
+  floatx4* red = reinterpret_cast<floatx4*>(x0);  // [NW][CG][MB][64]
 #pragma unroll
-  for (int h = 0; h < KH - 1; ++h)
+  for (int c = 0; c < CG; ++c)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) acc[mb] += red[((h * CG + cg) * MB + mb) * 64 + lane];
-  const int c = cb * 16 * CG + 16 * cg + r16;
-  if (c >= N) return;
+    for (int mb = 0; mb < MB; ++mb) red[((wave * CG + c) * MB + mb) * 64 + lane] = acc[c][mb];
+  __syncthreads();
+  for (int e = wave; e < CG * MB; e += NW) {
+    floatx4 sum = red[e * 64 + lane];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
+    for (int h = 1; h < NW; ++h) sum += red[(h * CG * MB + e) * 64 + lane];
+    const int c = n0 + 16 * (e / MB) + r16;
+    if (c >= N) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int r = mb * 16 + q * 4 + v;
+      const int r = (e % MB) * 16 + q * 4 + v;
       if (r >= M) continue;
       if (part)
-        part[((size_t)kq * M + r) * N + c] = acc[mb][v];
+        part[((size_t)kq * M + r) * N + c] = sum[v];
       else
-        Y[(size_t)r * N + c] = (uint16_t)f2bf(acc[mb][v]);
+        Y[(size_t)r * N + c] = (uint16_t)f2bf(sum[v]);
     }
+  }
+}
+
+template <int MB, int CG, int NW, int D, bool LORA>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, 8))) void q4_rows_kernel(
+    Q4View w, const uint16_t* __restrict__ X, int M, int S, uint16_t* __restrict__ Y, float* __restrict__ part,
+    PoolView pv, int proj, const int32_t* __restrict__ row_key, float* __restrict__ T, int SK) {
+  constexpr int kSlot = NW * (MB * 4096 + CG * 1024);
+  __shared__ __attribute__((aligned(16))) uint8_t x0[kSlot], x1[kSlot], x2[D > 2 ? kSlot : 16], x3[D > 3 ? kSlot : 16];
+  q4_rows_body<MB, CG, NW, D, LORA>(w, X, M, S, Y, part, pv, proj, row_key, T, SK, x0, x1, x2, x3);
 }
 
 // Sums the S slices' partial products in order, adds the row's low-rank term
@@ -203,7 +356,7 @@ constexpr int kQ4FinishThreads = 64;
 template <bool VEC, bool LORA>
 __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float* __restrict__ part, int S,
                                                                      uint16_t* __restrict__ Y, int M, int N,
-                                                                     PoolView pv, const float* __restrict__ T) {
+                                                                     PoolView pv, const float* __restrict__ T, int SK) {
   const int t = blockIdx.x * kQ4FinishThreads + threadIdx.x;
   const int per_row = (N + 7) / 8;
   if (t >= M * per_row) return;
@@ -227,7 +380,7 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
   }
   if (LORA) {
     float y[8];
-    lora_delta8_desc<VEC, false, 16>(pv, row_desc(const_cast<float*>(T), M, pv.max_rank), T, r, M, c0, N, y);
+    lora_delta8_desc<VEC, true, 16>(pv, row_desc(const_cast<float*>(T), M, pv.max_rank), T, r, M, c0, N, y, SK);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += y[e];
   }
@@ -259,28 +412,30 @@ struct RowsArgs {
   float* T;
 };
 
-template <int MB, int CG, bool LORA>
+template <int MB, int CG, int NW, int D, bool LORA>
 hipError_t launch_rows(const RowsArgs& a, const Q4Plan& p, hipStream_t st) {
-  const int n_shrink = LORA ? min((a.M + 7) / 8 * 8, 256) : 0;
   const int ncb = (a.w.N + 16 * CG - 1) / (16 * CG);
-  const size_t red = (size_t)(kRowsWaves / CG - 1) * CG * MB * 64 * sizeof(floatx4);
-  const size_t x = (size_t)a.M * p.xs_stride * 2;
-  const size_t lds = x > red ? x : red;
-  static LdsLimit limit;
-  const hipError_t e = limit.ensure({(const void*)q4_rows_kernel<MB, CG, LORA>}, lds);
-  if (e != hipSuccess) return e;
-  MLORA_LAUNCH(LORA ? "q4_rows+shrink_rows" : "q4_rows", (q4_rows_kernel<MB, CG, LORA>), dim3(n_shrink + ncb * p.S),
-               dim3(64 * kRowsWaves), lds, st, a.w, a.X, a.M, p.S, p.xs_stride, a.Y, p.direct ? nullptr : a.part, a.pv,
-               a.proj, a.row_key, a.T, n_shrink);
+  MLORA_LAUNCH(LORA ? "q4_rows+shrink" : "q4_rows", (q4_rows_kernel<MB, CG, NW, D, LORA>), dim3(ncb * p.S), dim3(64 * NW),
+               0, st, a.w, a.X, a.M, p.S, a.Y, p.direct ? nullptr : a.part, a.pv, a.proj, a.row_key, a.T, p.SK);
   return launched();
 }
 
-template <int CG, bool LORA>
-hipError_t launch_rows_mb(const RowsArgs& a, const Q4Plan& p, hipStream_t st) {
-  if (a.M <= 16) return launch_rows<1, CG, LORA>(a, p, st);
-  if (a.M <= 32) return launch_rows<2, CG, LORA>(a, p, st);
-  if (a.M <= 48) return launch_rows<3, CG, LORA>(a, p, st);
-  return launch_rows<4, CG, LORA>(a, p, st);
+template <bool LORA>
+hipError_t launch_rows_form(const RowsArgs& a, const Q4Plan& p, hipStream_t st) {
+  if (a.M <= 16) {
+    if (p.cg == 1) return launch_rows<1, 1, 8, 2, LORA>(a, p, st);
+    if (p.cg == 2) return launch_rows<1, 2, 8, 2, LORA>(a, p, st);
+    if (p.cg == 3) return launch_rows<1, 3, 8, 2, LORA>(a, p, st);
+    return launch_rows<1, 4, 8, 2, LORA>(a, p, st);
+  }
+  if (a.M <= 32) {
+    if (p.cg == 1) return launch_rows<2, 1, 8, 2, LORA>(a, p, st);
+    if (p.cg == 2) return launch_rows<2, 2, 4, 3, LORA>(a, p, st);
+    if (p.cg == 3) return launch_rows<2, 3, 4, 3, LORA>(a, p, st);
+    return launch_rows<2, 4, 4, 3, LORA>(a, p, st);
+  }
+  if (a.M <= 48) return launch_rows<3, 4, 4, 2, LORA>(a, p, st);
+  return launch_rows<4, 4, 4, 2, LORA>(a, p, st);
 }
 
 }  // namespace
@@ -300,18 +455,31 @@ hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uin
 
 Q4Plan q4_plan(int M, int K, int N, bool lora) {
   Q4Plan p{};
-  const int steps = (K + kStep - 1) / kStep;
-  // the fewest slices whose X fits in LDS
-  const int deepest = (int)(kXsMax / 2 / M) / 512 * 512 / kStep;
-  int S = (steps + deepest - 1) / deepest;
-  p.cg = !lora && M <= 16 ? 1 : 4;
-  if (p.cg == 4) {
-    const int ncb = (N + 63) / 64;
-    while (ncb * S < 256 && steps / (S + 1) >= 2) ++S;
-  }
-  p.S = S;
-  p.direct = S == 1 && !lora;
-  p.xs_stride = ((steps + S - 1) / S * kStep + 511) / 512 * 512;
+  const int steps = (K + kStep - 1) / kStep, groups = (N + 15) / 16;
+  // Columns of a workgroup: as few groups of 16 as let one round of workgroups
+  // (one a CU) cover the columns (11008 columns, 16 rows: three groups 9.2 us,
+  // one 10.8, two 11.9, four 10.5); above 32 rows four, because X is read
+  // again by every workgroup; two where a wave has few steps (4096 x 4096, one
+  // row: 6.0 us, one group 6.6).
+  p.cg = M > 32 ? 4 : (groups + 255) / 256;
+  if (p.cg > 4) p.cg = 4;
+  if (M <= 16 && p.cg == 1 && steps <= 32) p.cg = 2;
+  // Slices of K where workgroups are few.  They cost a launch that sums them
+  // (4 us), so without the low-rank term, which has that launch anyway, only
+  // many rows or steps are sliced (61 rows of 11008 channels, 4096 columns:
+  // four slices 20.4 us, one 48; one row of it: one slice 8.3 us, two 11.3).
+  const int ncb = (groups + p.cg - 1) / p.cg, waves = M > 32 ? 4 : 8;
+  p.S = 1;
+  if (M > 32 || lora || steps > 16 * waves) p.S = 256 / ncb;
+  if (p.S > steps / waves) p.S = steps / waves;
+  if (p.S > 16) p.S = 16;
+  if (p.S < 1) p.S = 1;
+  p.direct = p.S == 1 && !lora;
+  // the low-rank inner product: a slice of a row to a workgroup
+  p.SK = ncb * p.S / M;
+  if (p.SK > rows_t_slices(M)) p.SK = rows_t_slices(M);
+  if (p.SK > (K + 511) / 512) p.SK = (K + 511) / 512;
+  if (p.SK < 1) p.SK = 1;
   return p;
 }
 
@@ -319,25 +487,21 @@ hipError_t launch_q4_rows(const Q4View& w, const uint16_t* X, int M, uint16_t* Y
                           int proj, const int32_t* row_key, float* T, hipStream_t stream) {
   const Q4Plan p = q4_plan(M, w.K, w.N, pv != nullptr);
   const RowsArgs a{w, X, M, Y, part, pv ? *pv : PoolView{}, proj, row_key, T};
-  hipError_t e;
-  if (pv)
-    e = launch_rows_mb<4, true>(a, p, stream);
-  else
-    e = p.cg == 1 ? launch_rows<1, 1, false>(a, p, stream) : launch_rows_mb<4, false>(a, p, stream);
+  const hipError_t e = pv ? launch_rows_form<true>(a, p, stream) : launch_rows_form<false>(a, p, stream);
   if (e != hipSuccess || p.direct) return e;
   const bool vec = w.N % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
                    (!pv || reinterpret_cast<uintptr_t>(pv->up) % 16 == 0);
   const dim3 g((M * ((w.N + 7) / 8) + kQ4FinishThreads - 1) / kQ4FinishThreads), b(kQ4FinishThreads);
   if (pv) {
     if (vec)
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T, p.SK);
     else
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T, p.SK);
   } else {
     if (vec)
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T, p.SK);
     else
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T, p.SK);
   }
   return launched();
 }
