@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -81,11 +82,6 @@ class _Q4Desc(ctypes.Structure):
 
 class _RotaryDesc(ctypes.Structure):
     _fields_ = [("freq", _c_void_p), ("rot", _i32), ("interleaved", _i32), ("factor", _f32)]
-
-
-class _HeadRows(ctypes.Structure):
-    _fields_ = [("x", _c_void_p), ("y", _c_void_p), ("row_stride", _i64), ("head_stride", _i64),
-                ("out_row_stride", _i64), ("out_head_stride", _i64), ("weight", _c_void_p), ("heads", _i32)]
 
 
 # name -> (restype, argtypes); every symbol include/mlora.h declares
@@ -179,9 +175,15 @@ def _check(status: int, where: str) -> None:
         raise MloraError(status, where)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
@@ -695,9 +697,10 @@ def _raw_stream(device: int) -> int:
 
 def _on_device(t, name: str, dtype, device: int, shape=None):
     """Checks a contiguous tensor of `dtype` on cuda:`device`."""
-    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+    if (not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.get_device() != device
+            or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -738,8 +741,8 @@ def q4_quantize(W) -> Q4Weight:
     if _bf16_dev(W, "W").dim() != 2 or W.shape[1] < 32 or W.shape[1] % 32:
         raise ValueError(f"W has shape {tuple(W.shape)}, expected [dout][din], din a multiple of 32")
     dout, din = W.shape
-    codes = torch.empty((dout, din // 2), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((dout, din // 32), dtype=torch.uint8, device=W.device)
+    codes = W.new_empty((dout, din // 2), dtype=torch.uint8)
+    scales = W.new_empty((dout, din // 32), dtype=torch.uint8)
     _check(lib().mlora_q4_quantize(W.data_ptr(), dout, din, codes.data_ptr(), scales.data_ptr(),
                                    _raw_stream(W.get_device())), "mlora_q4_quantize")
     return Q4Weight(codes, scales)
@@ -782,7 +785,7 @@ def _q4_rows(X, w: Q4Weight, Y):
         raise ValueError(f"X has shape {tuple(X.shape)}, expected [n][{w.din}]")
     shape = (X.shape[0], w.dout)
     if Y is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=X.device)
+        return X.new_empty(shape)
     return _on_device(Y, "Y", torch.bfloat16, w.device_index, shape)
 
 
@@ -843,26 +846,29 @@ class Rotary:
         self._ref = ctypes.addressof(self._d)
 
 
-def _head_rows(x, name: str, n: int, weight, out, device: int, dim: int):
+# mlora_head_rows as bytes: building one costs a third of filling a ctypes structure
+_head_rows = struct.Struct("<QQqqqqQi4x").pack
+
+
+def _qk_rows(x, name: str, shape, weight, out, device: int):
+    """Checks one side of qk_norm_rotary; its output and its descriptor."""
     torch = _torch()
-    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() != device:
+    if x.dtype is not torch.bfloat16 or x.get_device() != device:
         raise TypeError(f"{name} must be a bfloat16 tensor on cuda:{device}, as the batch is")
-    shape = x.shape
-    if len(shape) != 3 or shape[0] != n or shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{n}][heads][{dim}]")
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    elif not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.get_device() != device:
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [n_rows][heads][dim]")
+    if out is None:  # (empty_like takes a third of the time of empty)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype is not torch.bfloat16 or out.get_device() != device:
         raise TypeError(f"{name}_out must be a bfloat16 tensor on cuda:{device}, as the batch is")
     elif out.shape != shape:
         raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
-    st, ot = x.stride(), out.stride()
-    if st[2] != 1 or ot[2] != 1:
+    rs, hs, cs = x.stride()
+    ors, ohs, ocs = out.stride()
+    if cs != 1 or ocs != 1:
         raise TypeError(f"{name} and {name}_out must be dense in their channels")
-    w = 0
-    if weight is not None:
-        w = _on_device(weight, f"{name}_weight", torch.bfloat16, device, (dim,)).data_ptr()
-    return out, _HeadRows(x.data_ptr(), out.data_ptr(), st[0], st[1], ot[0], ot[1], w, shape[1])
+    w = 0 if weight is None else _on_device(weight, name + "_weight", torch.bfloat16, device, shape[2:]).data_ptr()
+    return out, _head_rows(x.data_ptr(), out.data_ptr(), rs, hs, ors, ohs, w, shape[1])
 
 
 def qk_norm_rotary(q, k, batch: KVBatch, rotary: Rotary, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -872,18 +878,22 @@ def qk_norm_rotary(q, k, batch: KVBatch, rotary: Rotary, q_weight=None, k_weight
     (None: no norm), then the rotation by each row's position in `batch`.  k
     may be None.  q_out=q and k_out=k work in place; otherwise the outputs are
     new.  Rows past the last sequence are left as they are.  Returns (q, k)."""
-    device = batch.device_index
+    device, shape = batch.device_index, q.shape
     if rotary.device_index != device:
         raise ValueError(f"rotary must be on cuda:{device}, as the batch is")
-    dim = q.shape[-1]
-    q_out, qs = _head_rows(q, "q", batch.n_rows, q_weight, q_out, device, dim)
+    q_out, qs = _qk_rows(q, "q", shape, q_weight, q_out, device)
+    n, _, dim = shape
     ks = None
     if k is not None:
-        k_out, ks = _head_rows(k, "k", batch.n_rows, k_weight, k_out, device, dim)
+        kshape = k.shape
+        k_out, ks = _qk_rows(k, "k", kshape, k_weight, k_out, device)
+        if kshape[0] != n or kshape[2] != dim:
+            raise ValueError(f"k has shape {tuple(kshape)}, expected [{n}][heads][{dim}]")
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    status = lib().mlora_qk_norm_rotary(batch._ref, dim, rotary._ref, ctypes.byref(qs),
-                                        ctypes.byref(ks) if ks is not None else None, eps, _raw_stream(device))
+    if n != batch.n_rows:
+        raise ValueError(f"q has {n} rows, the batch {batch.n_rows}")
+    status = lib().mlora_qk_norm_rotary(batch._ref, dim, rotary._ref, qs, ks, eps, _raw_stream(device))
     if status != OK:
         raise MloraError(status, "mlora_qk_norm_rotary")
     return q_out, k_out
@@ -918,8 +928,9 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
                         ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
         ptr.append(None if t is None else _on_device(t, name, dt, device, (n,)).data_ptr())
     if out is None:
-        out = torch.empty(n, dtype=torch.int32, device=logits.device)
-    _on_device(out, "out", torch.int32, device, (n,))
+        out = torch.empty_like(u, dtype=torch.int32)
+    else:
+        _on_device(out, "out", torch.int32, device, (n,))
     work = new_sample_work(n, vocab, logits.device) if work is None else _work(work, device)
     status = lib().mlora_sample(logits.data_ptr(), logits.dtype is torch.float32, logits.stride(0) if n > 1 else vocab,
                                 n, vocab, u.data_ptr(), *ptr, out.data_ptr(), work.data_ptr(), work.nbytes,

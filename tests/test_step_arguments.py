@@ -62,7 +62,7 @@ def _rotate(L, q=None, k=None, dim=64, rot=64, freq=P, factor=1.0, eps=1e-6, n_r
     for s in (q, k):
         d = dict(x=P, y=P, row_stride=512, head_stride=64, out_row_stride=512, out_head_stride=64, weight=None, heads=4)
         d.update(s or {})
-        sides.append(ctypes.byref(M._HeadRows(*d.values())))
+        sides.append(M._head_rows(*(v or 0 for v in d.values())))
     if k is None:
         sides[1] = None
     b = M._KVBatchDesc(None, kv_len, row_off, n_seq, 0, 0, n_rows, 0)
