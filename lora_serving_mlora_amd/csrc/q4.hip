@@ -230,10 +230,6 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d, slot_of(d), sb[d]);
 
-  if (LORA) {
-    for (int t = blockIdx.x; t < M * SK; t += gridDim.x) shrink_slice<NW>(pv, proj, X, row_key, M, t % M, t / M, SK, T);
-  }
-
   floatx4 acc[CG][MB];
 #pragma unroll
   for (int c = 0; c < CG; ++c)
@@ -312,6 +308,10 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
       __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     asm volatile("" ::: "memory");
     if (i + d < mine) multiply(i + d, slot_of(d), sb[d]);
+  }
+
+  if (LORA) {
+    for (int t = blockIdx.x; t < M * SK; t += gridDim.x) shrink_slice<NW>(pv, proj, X, row_key, M, t % M, t / M, SK, T);
   }
 
   // the waves' shares of K, in order; a thread takes four rows of a column
