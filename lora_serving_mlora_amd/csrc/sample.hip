@@ -94,15 +94,14 @@ __device__ __forceinline__ void for_row(const T* __restrict__ row, int V, F f) {
     }
     f(head + v * E, x);
   };
-  int v = tid;
-  for (; v + (U - 1) * kThreads < body; v += U * kThreads) {
+  for (int v = tid; v < body; v += U * kThreads) {
     uint4 y[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) y[k] = p[v + k * kThreads];
+    for (int k = 0; k < U; ++k) y[k] = p[min(v + k * kThreads, body - 1)];
 #pragma unroll
-    for (int k = 0; k < U; ++k) piece(v + k * kThreads, y[k]);
+    for (int k = 0; k < U; ++k)
+      if (v + k * kThreads < body) piece(v + k * kThreads, y[k]);
   }
-  for (; v < body; v += kThreads) piece(v, p[v]);
 }
 
 struct Row {
@@ -312,7 +311,17 @@ template <int N, class S, class T>
 __device__ __forceinline__ void list_in(S& sh, const Row& r, const T* __restrict__ row, int V,
                                         const Interval (&iv)[3]) {
   constexpr int E = 16 / sizeof(T);
+  // a logit below which none is in an interval (the place is off by two
+  // roundings at most), so that most pieces take a look at their largest only
+  float far = iv[0].hi;
+  if (N > 1) far = fmaxf(far, iv[1].hi);
+  if (N > 2) far = fmaxf(far, iv[2].hi);
+  const float from = (float)r.mx - (far / r.fit * 1.000001f + fabsf((float)r.mx) * 1e-6f);
   for_row<4>(row, V, [&](int i, const float (&xs)[E]) {
+    float top = xs[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) top = fmaxf(top, xs[e]);
+    if (top < from) return;
     uint32_t hit = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -754,6 +763,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     sh.redf[1][tid >> 6] = mn;
   }
   if (tid == 0) sh.n_list = 0;
+  sh.rank[tid] = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -804,22 +814,19 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   iv[0] = {kNone, -kNone};
   int n_iv = V <= kCap ? 1 : 0;
   if (plain && n_iv == 0 && top_k > 0 && top_k <= kSmallK) {
-    clear_bins(sh);
-    const float t = place_of(r, mine);
-    const int b = mine != kNone ? range_of(r, mine) : kBins;
-    if (b < kBins) atomicAdd(&sh.bins.count[b], 1u);
-    if (tid == 0) sh.rank[0] = 0;
+    // by a histogram of them over ranges four times as wide (the counts cleared above)
+    const int b = mine != kNone ? range_of(r, mine) / kPer : -1;
+    if (b >= 0) atomicAdd(&sh.rank[b], 1u);
     __syncthreads();
-    u64 mall;
-    uint32_t call;
-    const Ends e = scan_bins(sh, mall, call);
+    const uint32_t own = sh.rank[tid];
+    uint32_t c = own, call;
+    u64 none = 0, nothing;
+    block_scan(none, c, sh.red[0], nothing, call);
+    if (c - own < (uint32_t)top_k && (uint32_t)top_k <= c) sh.bin[0] = tid;
+    __syncthreads();
     if ((uint32_t)top_k <= call) {
-      find_count(e, (uint32_t)top_k, &sh.bin[0]);
-      __syncthreads();
-      // the farthest place of those in the ranges so far
-      if (b <= sh.bin[0]) atomicMax(&sh.rank[0], rising(t));
-      __syncthreads();
-      iv[0].hi = next_up(from_rising(sh.rank[0]));
+      const int last = sh.bin[0];
+      iv[0].hi = last < kThreads - 1 ? (float)((last + 1) * kPer) : next_up(place_of(r, r.least));
       n_iv = 1;
     }
   }
