@@ -965,6 +965,40 @@ mlora_status mlora_plan(const mlora_pool* p, int32_t n, int32_t variant, int32_t
   return MLORA_OK;
 }
 
+namespace {
+// The split plan of a large batch: shrink, the low-rank operands, then one GEMM
+// that adds the low-rank term itself (Y written once).  vb, Xb, W: what the
+// GEMM takes, the pool's view, X and the weight, or with more channels to a
+// row, zeros in X and W.
+mlora_status apply_big(const mlora_pool* p, int32_t proj, const uint16_t* X, const PoolView& vb, const uint16_t* Xb,
+                       const uint16_t* W, const int32_t* ws, uint16_t* Y, int n, void* work, hipStream_t s) {
+  const mlora_pool_desc& d = p->d;
+  const PoolView v = p->view();
+  mlora_status st;
+  const int chunks = split_chunks(p, n);
+  float* T = static_cast<float*>(work);
+  char* w = static_cast<char*>(work) + align256((size_t)chunks * n * d.max_rank * sizeof(float));
+  const int wt = mlora::t_rows_width(d.max_rank);
+  const EpilogueLayout L = epilogue_layout(p, n);
+  uint16_t* tb = reinterpret_cast<uint16_t*>(w);
+  int32_t* koff = reinterpret_cast<int32_t*>(w + L.koff);
+  int32_t* over = reinterpret_cast<int32_t*>(w + L.over);
+  int32_t* kx = reinterpret_cast<int32_t*>(w + L.kx);
+  uint16_t* tx = L.txw > 0 ? reinterpret_cast<uint16_t*>(w + L.tx) : nullptr;
+  uint16_t* upt = reinterpret_cast<uint16_t*>(w + L.upt);
+  st = hip_check(mlora::launch_shrink(v, proj, X, ws, n, T, chunks, chunk_elems_for(d.din, chunks), s), "shrink launch");
+  if (st != MLORA_OK) return st;
+  st = hip_check(mlora::launch_lora_prep(v, proj, ws, n, T, chunks, tb, wt, koff, upt, L.upt_units, over, tx,
+                                         L.txw, kx, s),
+                 "low-rank operand launch");
+  if (st != MLORA_OK) return st;
+  const mlora::LoraOperands lo{tb, koff, upt, wt, L.may_overrun ? over : nullptr, tx, L.txw, tx ? kx : nullptr};
+  st = hip_check(mlora::launch_big_lora(vb, Xb, W, ws, lo, Y, n, s), "GEMM + low-rank term launch");
+  if (st != MLORA_OK || !L.may_overrun) return st;
+  return hip_check(mlora::launch_expand_over(v, proj, T, chunks, ws, Y, n, over, s), "overrun expand launch");
+}
+}  // namespace
+
 mlora_status mlora_apply(const mlora_pool* p, int32_t proj, const uint16_t* X, const uint16_t* W0,
                          const void* seg_ws, uint16_t* Y, int32_t n, void* work, size_t work_bytes, int32_t variant,
                          void* stream) {
@@ -992,31 +1026,8 @@ mlora_status mlora_apply(const mlora_pool* p, int32_t proj, const uint16_t* X, c
     return hip_check(mlora::launch_gemm_lora(v, proj, X, W0, ws, w.T, w.part, Y, n, true, s),
                      "per-row shrink + GEMM + expand launch");
   }
-  if (variant == MLORA_VARIANT_SPLIT && big_epilogue_fits(p, n) && mlora::big_lora_ok(v, X, W0, n)) {
-    // large batch: shrink, the low-rank operands, then one GEMM that adds
-    // the low-rank term itself (Y written once)
-    const int chunks = split_chunks(p, n);
-    float* T = static_cast<float*>(work);
-    char* w = static_cast<char*>(work) + align256((size_t)chunks * n * d.max_rank * sizeof(float));
-    const int wt = mlora::t_rows_width(d.max_rank);
-    const EpilogueLayout L = epilogue_layout(p, n);
-    uint16_t* tb = reinterpret_cast<uint16_t*>(w);
-    int32_t* koff = reinterpret_cast<int32_t*>(w + L.koff);
-    int32_t* over = reinterpret_cast<int32_t*>(w + L.over);
-    int32_t* kx = reinterpret_cast<int32_t*>(w + L.kx);
-    uint16_t* tx = L.txw > 0 ? reinterpret_cast<uint16_t*>(w + L.tx) : nullptr;
-    uint16_t* upt = reinterpret_cast<uint16_t*>(w + L.upt);
-    st = hip_check(mlora::launch_shrink(v, proj, X, ws, n, T, chunks, chunk_elems_for(d.din, chunks), s), "shrink launch");
-    if (st != MLORA_OK) return st;
-    st = hip_check(mlora::launch_lora_prep(v, proj, ws, n, T, chunks, tb, wt, koff, upt, L.upt_units, over, tx,
-                                           L.txw, kx, s),
-                   "low-rank operand launch");
-    if (st != MLORA_OK) return st;
-    const mlora::LoraOperands lo{tb, koff, upt, wt, L.may_overrun ? over : nullptr, tx, L.txw, tx ? kx : nullptr};
-    st = hip_check(mlora::launch_big_lora(v, X, W0, ws, lo, Y, n, s), "GEMM + low-rank term launch");
-    if (st != MLORA_OK || !L.may_overrun) return st;
-    return hip_check(mlora::launch_expand_over(v, proj, T, chunks, ws, Y, n, over, s), "overrun expand launch");
-  }
+  if (variant == MLORA_VARIANT_SPLIT && big_epilogue_fits(p, n) && mlora::big_lora_ok(v, X, W0, n))
+    return apply_big(p, proj, X, v, X, W0, ws, Y, n, work, s);
   // the base GEMM: split over K with its partials in `work` (per-row
   // layout) when the batch and the buffer allow, else the plain form
   hipError_t ge = hipErrorNotSupported;
@@ -1294,7 +1305,14 @@ mlora_status q4_view(const mlora_q4_weight* w, mlora::Q4View* v) {
   return MLORA_OK;
 }
 bool q4_few(const mlora::Q4View& w, const mlora_pool* p, int n) {
-  return n <= mlora::kQ4Rows && w.K >= mlora::kQ4MinDin && (!p || aligned16(p->d.down_pages));
+  return mlora::q4_few_rows(n, w.K, w.N, p != nullptr) && (!p || aligned16(p->d.down_pages));
+}
+// channels of a row of the bf16 weight: the products of many rows want whole
+// steps, the per-row layer takes any (and rounds its result once)
+int q4_channels(const mlora::Q4View& w, int n) { return n > kRowsMax ? mlora::q4_padded(w.K) : w.K; }
+size_t q4_operand_bytes(const mlora::Q4View& w, int n) {
+  const int Kp = q4_channels(w, n);
+  return align256((size_t)Kp * w.N * 2) + (Kp == w.K ? 0 : align256((size_t)Kp * n * 2));
 }
 // work of a product: few rows the per-row T region (with a pool) and the
 // partial products; more rows the bf16 weight, then the bf16 product's own
@@ -1303,9 +1321,20 @@ size_t q4_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
   if (q4_few(w, p, n))
     return (p ? rows_t_bytes(p, n) : 0) +
            align256(mlora::q4_plan(n, w.K, w.N, p != nullptr).part_floats(n, w.N) * sizeof(float));
-  const size_t weight = align256((size_t)w.K * w.N * 2);
-  if (p) return weight + mlora_work_bytes(p, n);
-  return weight + (n <= kRowsMax ? align256(mlora::gemm_lora_part_floats(n, w.N, w.K) * sizeof(float)) : 0);
+  const size_t operands = q4_operand_bytes(w, n);
+  if (p) return operands + mlora_work_bytes(p, n);
+  return operands + (n <= kRowsMax ? align256(mlora::gemm_lora_part_floats(n, w.N, w.K) * sizeof(float)) : 0);
+}
+// the bf16 weight in `work`, and X where rows are padded: *X is what goes with it
+mlora_status q4_operands(const mlora::Q4View& w, int n, void* work, const uint16_t** X, hipStream_t s) {
+  uint16_t* W = static_cast<uint16_t*>(work);
+  const int Kp = q4_channels(w, n);
+  if (Kp == w.K)
+    return hip_check(mlora::launch_q4_dequantize(w.codes, w.scales, W, (int64_t)w.N * w.K, s), "4-bit weight to bf16 launch");
+  uint16_t* Xp = reinterpret_cast<uint16_t*>(static_cast<char*>(work) + align256((size_t)Kp * w.N * 2));
+  const uint16_t* x = *X;
+  *X = Xp;
+  return hip_check(mlora::launch_q4_pad(w, x, n, W, Xp, s), "4-bit weight to bf16 launch");
 }
 mlora_status q4_work(const mlora::Q4View& w, const mlora_pool* p, int n, const void* work, size_t bytes) {
   const size_t need = q4_bytes(w, p, n);
@@ -1359,15 +1388,15 @@ mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t
   if (q4_few(v, nullptr, n))
     return hip_check(mlora::launch_q4_rows(v, X, n, Y, static_cast<float*>(work), nullptr, 0, nullptr, nullptr, s),
                      "4-bit product launch");
-  uint16_t* W = static_cast<uint16_t*>(work);
-  st = hip_check(mlora::launch_q4_dequantize(v.codes, v.scales, W, (int64_t)v.N * v.K, s), "4-bit weight to bf16 launch");
-  if (st != MLORA_OK) return st;
+  if ((st = q4_operands(v, n, work, &X, s)) != MLORA_OK) return st;
+  const uint16_t* W = static_cast<const uint16_t*>(work);
+  const int K = q4_channels(v, n);
   hipError_t e = hipErrorNotSupported;
   if (n <= kRowsMax) {
-    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + align256((size_t)v.K * v.N * 2));
-    e = mlora::launch_base_split(X, W, Y, n, v.K, v.N, part, s);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + q4_operand_bytes(v, n));
+    e = mlora::launch_base_split(X, W, Y, n, K, v.N, part, s);
   }
-  if (e == hipErrorNotSupported) e = mlora::launch_base_gemm(X, W, Y, n, v.K, v.N, s);
+  if (e == hipErrorNotSupported) e = mlora::launch_base_gemm(X, W, Y, n, K, v.N, s);
   return hip_check(e, "base GEMM launch");
 }
 
@@ -1391,13 +1420,24 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
     return hip_check(mlora::launch_q4_rows(v, X, n, Y, part, &pv, proj, row_key, T, as_stream(stream)),
                      "4-bit product + low-rank term launch");
   }
-  uint16_t* W = static_cast<uint16_t*>(work);
-  const size_t weight = align256((size_t)v.K * v.N * 2);
-  st = hip_check(mlora::launch_q4_dequantize(v.codes, v.scales, W, (int64_t)v.N * v.K, as_stream(stream)),
-                 "4-bit weight to bf16 launch");
+  hipStream_t s = as_stream(stream);
+  const uint16_t* Xb = X;
+  if ((st = q4_operands(v, n, work, &Xb, s)) != MLORA_OK) return st;
+  const uint16_t* W = static_cast<const uint16_t*>(work);
+  const size_t operands = q4_operand_bytes(v, n);
+  char* rest = static_cast<char*>(work) + operands;
+  if (Xb == X) return mlora_apply(p, proj, X, W, seg_ws, Y, n, rest, work_bytes - operands, MLORA_VARIANT_AUTO, stream);
+  const int32_t* ws = static_cast<const int32_t*>(seg_ws);
+  PoolView vb = p->view();
+  vb.din = q4_channels(v, n);
+  if (big_epilogue_fits(p, n) && mlora::big_lora_ok(vb, Xb, W, n)) return apply_big(p, proj, X, vb, Xb, W, ws, Y, n, rest, s);
+  st = hip_check(mlora::launch_base_gemm(Xb, W, Y, n, vb.din, v.N, s), "base GEMM launch");
   if (st != MLORA_OK) return st;
-  return mlora_apply(p, proj, X, W, seg_ws, Y, n, static_cast<char*>(work) + weight, work_bytes - weight,
-                     MLORA_VARIANT_AUTO, stream);
+  const int chunks = split_chunks(p, n);
+  float* T = reinterpret_cast<float*>(rest);
+  st = hip_check(mlora::launch_shrink(p->view(), proj, X, ws, n, T, chunks, chunk_elems_for(p->d.din, chunks), s), "shrink launch");
+  if (st != MLORA_OK) return st;
+  return hip_check(mlora::launch_expand(p->view(), proj, T, chunks, ws, Y, n, s), "expand launch");
 }
 
 }  // extern "C"

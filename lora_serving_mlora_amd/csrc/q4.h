@@ -35,9 +35,16 @@ hipError_t launch_q4_quantize(const uint16_t* W, uint8_t* codes, uint8_t* scales
 hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* W, int64_t n,
                                 hipStream_t stream);
 
-// Batches of at most this many rows (of at least kQ4MinDin channels) multiply
-// the codes as they are; larger ones make the weight bf16 first and take the bf16 products.
-constexpr int kQ4Rows = 64, kQ4MinDin = 128;
+// Products of few rows take the codes as they are, 64 rows to a workgroup;
+// larger ones make the weight bf16 first and take the bf16 products.
+constexpr int kQ4RowBlock = 64, kQ4MinDin = 128;
+inline int q4_row_blocks(int M) { return (M + kQ4RowBlock - 1) / kQ4RowBlock; }
+bool q4_few_rows(int M, int K, int N, bool lora);
+// For the bf16 products of more rows: the weight, and X, in rows of a multiple
+// of 128 channels, zeros past K (the products are slow for other K: 2048 rows,
+// K 4064: 103 us, padded 80; with the low-rank term 117 and 96).
+__host__ __device__ constexpr int q4_padded(int K) { return (K + 127) / 128 * 128; }
+hipError_t launch_q4_pad(const Q4View& w, const uint16_t* X, int M, uint16_t* Wp, uint16_t* Xp, hipStream_t stream);
 // The form of a product of M rows: workgroups of 16 * cg columns, K in S
 // slices.  Without the low-rank term and with one slice the product is
 // written as it is; else partial products [S][M][N] go to scratch and a

@@ -62,8 +62,27 @@ __global__ __launch_bounds__(kConvThreads) void q4_dequantize_kernel(const uint8
     reinterpret_cast<uint4*>(W)[i] = q4_bf8(reinterpret_cast<const uint32_t*>(codes)[i], q4_scale(scales[i >> 2]));
 }
 
+// The same into rows of Kp channels, and the M rows of X into such rows behind
+// them: zeros past the K that there are.  A workgroup a row.
+__global__ __launch_bounds__(kConvThreads) void q4_pad_kernel(Q4View w, const uint16_t* __restrict__ X,
+                                                              uint16_t* __restrict__ Wp, uint16_t* __restrict__ Xp,
+                                                              int K8, int Kp8) {
+  const int r = (int)blockIdx.x;
+  if (r < w.N) {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(w.codes) + (size_t)r * K8;
+    const uint8_t* s = w.scales + (size_t)r * (K8 / 4);
+    uint4* o = reinterpret_cast<uint4*>(Wp) + (size_t)r * Kp8;
+    for (int j = threadIdx.x; j < Kp8; j += kConvThreads)
+      o[j] = j < K8 ? q4_bf8(c[j], q4_scale(s[j >> 2])) : make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    const uint4* x = reinterpret_cast<const uint4*>(X) + (size_t)(r - w.N) * K8;
+    uint4* o = reinterpret_cast<uint4*>(Xp) + (size_t)(r - w.N) * Kp8;
+    for (int j = threadIdx.x; j < Kp8; j += kConvThreads) o[j] = j < K8 ? x[j] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Products of up to 64 rows.  What bounds them is the codes' way from memory,
+// Products of few rows, 64 to a workgroup.  What bounds them is the codes' way from memory,
 // so each code is read once, by the lane whose operand it is: a lane takes
 // the 16 bytes (32 channels, one group) of one column at a time, the 16
 // columns of a group by the 4 lane groups' next groups of channels, and feeds
@@ -173,7 +192,7 @@ __device__ __forceinline__ void shrink_slice(const PoolView& pv, int proj, const
 // of their own, so that the compiler knows that reads of one do not wait for
 // what is on its way into another (the first D of them are used).
 template <int MB, int CG, int NW, int D, bool LORA>
-__device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __restrict__ X, int M, int S,
+__device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __restrict__ Xall, int rows, int S,
                                              uint16_t* __restrict__ Y, float* __restrict__ part, const PoolView& pv,
                                              int proj, const int32_t* __restrict__ row_key, float* __restrict__ T,
                                              int SK, uint8_t* __restrict__ x0, uint8_t* __restrict__ x1,
@@ -183,7 +202,9 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ncb = (N + 16 * CG - 1) / (16 * CG);
-  const int cb = (int)blockIdx.x % ncb, kq = (int)blockIdx.x / ncb;
+  const int cb = (int)blockIdx.x % ncb, kq = (int)blockIdx.x / ncb % S, m0 = (int)blockIdx.x / (ncb * S) * kQ4RowBlock;
+  const int M = min(rows - m0, kQ4RowBlock);  // rows of this workgroup, from m0 on
+  const uint16_t* X = Xall + (size_t)m0 * K;
   const int steps = (K + kStep - 1) / kStep;
   // this wave's steps [u0, u0 + mine) of the NW * S shares of K
   const int u0 = (int)((long)steps * (kq * NW + wave) / (NW * S));
@@ -311,7 +332,8 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   }
 
   if (LORA) {
-    for (int t = blockIdx.x; t < M * SK; t += gridDim.x) shrink_slice<NW>(pv, proj, X, row_key, M, t % M, t / M, SK, T);
+    for (int t = blockIdx.x; t < rows * SK; t += gridDim.x)
+      shrink_slice<NW>(pv, proj, Xall, row_key, rows, t % rows, t / rows, SK, T);
   }
 
   // the waves' shares of K, in order; a thread takes four rows of a column
@@ -334,9 +356,9 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
       const int r = (e % MB) * 16 + q * 4 + v;
       if (r >= M) continue;
       if (part)
-        part[((size_t)kq * M + r) * N + c] = sum[v];
+        part[((size_t)kq * rows + m0 + r) * N + c] = sum[v];
       else
-        Y[(size_t)r * N + c] = (uint16_t)f2bf(sum[v]);
+        Y[(size_t)(m0 + r) * N + c] = (uint16_t)f2bf(sum[v]);
     }
   }
 }
@@ -415,7 +437,8 @@ struct RowsArgs {
 template <int MB, int CG, int NW, int D, bool LORA>
 hipError_t launch_rows(const RowsArgs& a, const Q4Plan& p, hipStream_t st) {
   const int ncb = (a.w.N + 16 * CG - 1) / (16 * CG);
-  MLORA_LAUNCH(LORA ? "q4_rows+shrink" : "q4_rows", (q4_rows_kernel<MB, CG, NW, D, LORA>), dim3(ncb * p.S), dim3(64 * NW),
+  MLORA_LAUNCH(LORA ? "q4_rows+shrink" : "q4_rows", (q4_rows_kernel<MB, CG, NW, D, LORA>), dim3(ncb * p.S * q4_row_blocks(a.M)),
+               dim3(64 * NW),
                0, st, a.w, a.X, a.M, p.S, a.Y, p.direct ? nullptr : a.part, a.pv, a.proj, a.row_key, a.T, p.SK);
   return launched();
 }
@@ -453,6 +476,22 @@ hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uin
   return launched();
 }
 
+bool q4_few_rows(int M, int K, int N, bool lora) {
+  // The bf16 products have rates that these do not reach, but the weight has
+  // to be made first (4096 x 4096: 256 rows 18.3 against 30.0 us, with the
+  // low-rank term 27.9 against 32.8; 512 rows 32.6 against 34.5, with it 48.5
+  // against 43.8; 1024 rows 59 against 48), and they are slow where K is not
+  // whole steps or N not whole vectors (1024 rows, K 4064: 63 against 196 us).
+  if (K < kQ4MinDin) return false;
+  return M <= (K % kStep == 0 && N % 8 == 0 ? (lora ? 256 : 512) : 1024);
+}
+
+hipError_t launch_q4_pad(const Q4View& w, const uint16_t* X, int M, uint16_t* Wp, uint16_t* Xp, hipStream_t stream) {
+  MLORA_LAUNCH("q4_pad", q4_pad_kernel, dim3(w.N + M), dim3(kConvThreads), 0, stream, w, X, Wp, Xp, w.K / 8,
+               q4_padded(w.K) / 8);
+  return launched();
+}
+
 Q4Plan q4_plan(int M, int K, int N, bool lora) {
   Q4Plan p{};
   const int steps = (K + kStep - 1) / kStep, groups = (N + 15) / 16;
@@ -468,7 +507,7 @@ Q4Plan q4_plan(int M, int K, int N, bool lora) {
   // (4 us), so without the low-rank term, which has that launch anyway, only
   // many rows or steps are sliced (61 rows of 11008 channels, 4096 columns:
   // four slices 20.4 us, one 48; one row of it: one slice 8.3 us, two 11.3).
-  const int ncb = (groups + p.cg - 1) / p.cg, waves = M > 32 ? 4 : 8;
+  const int ncb = (groups + p.cg - 1) / p.cg * q4_row_blocks(M), waves = M > 32 ? 4 : 8;
   p.S = 1;
   if (M > 32 || lora || steps > 16 * waves) p.S = 256 / ncb;
   if (p.S > steps / waves) p.S = steps / waves;

@@ -90,7 +90,9 @@ def within(y, ref, mag, din, extra=0.0):
 
 SHAPES = [(1, 32, 1), (1, 4096, 256), (2, 96, 17), (5, 160, 64), (16, 4064, 200), (16, 128, 8), (17, 2048, 72),
           (33, 1056, 257), (48, 512, 16), (63, 544, 130), (64, 4096, 128), (64, 11008, 64), (16, 11008, 40),
-          (3, 20000, 24), (65, 512, 128), (100, 96, 33), (257, 1024, 264), (1025, 256, 136)]
+          (3, 20000, 24), (65, 512, 128), (100, 96, 33), (257, 1024, 264), (1025, 256, 136), (128, 4064, 200),
+          (300, 2080, 41), (511, 256, 520), (513, 256, 520), (700, 160, 1032), (1000, 96, 24), (1024, 1056, 17),
+          (1200, 1056, 264), (2100, 96, 2052), (1030, 32, 40)]
 
 
 @pytest.mark.parametrize("n,din,dout", SHAPES)
@@ -125,7 +127,10 @@ def test_nan_stays_in_its_row_and_column(M, n):
 
 LAYERS = [(1, 256, 64, {0: 8}), (13, 1056, 72, {0: 1, 1: 16, 2: 64}), (32, 4096, 256, {0: 16, 1: 16, 2: 16}),
           (48, 512, 33, {0: 4, 2: 33}), (64, 2080, 136, {0: 128, 1: 3}), (65, 512, 128, {0: 16, 1: 5}),
-          (200, 1024, 72, {0: 8, 1: 64}), (1100, 128, 72, {0: 8, 1: 40})]
+          (200, 1024, 72, {0: 8, 1: 64}), (1100, 128, 72, {0: 8, 1: 40}), (130, 2080, 72, {0: 128, 1: 16}),
+          (255, 512, 264, {0: 1, 1: 16, 2: 33}), (257, 512, 264, {0: 8, 1: 16}), (300, 1056, 33, {0: 16, 1: 3}),
+          (1000, 160, 72, {0: 8, 1: 40}), (70, 96, 40, {0: 4}), (1100, 160, 72, {0: 8, 1: 40}),
+          (2100, 160, 2050, {0: 8, 1: 40})]
 
 
 @pytest.mark.parametrize("n,din,dout,ranks", LAYERS)
