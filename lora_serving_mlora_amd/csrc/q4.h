@@ -37,7 +37,7 @@ hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uin
 
 // Products of few rows take the codes as they are, 64 rows to a workgroup;
 // larger ones make the weight bf16 first and take the bf16 products.
-constexpr int kQ4RowBlock = 64, kQ4MinDin = 128;
+constexpr int kQ4RowBlock = 64, kQ4MinDin = 128, kQ4TSlices = 16;
 inline int q4_row_blocks(int M) { return (M + kQ4RowBlock - 1) / kQ4RowBlock; }
 bool q4_few_rows(int M, int K, int N, bool lora);
 // For the bf16 products of more rows: the weight, and X, in rows of a multiple
@@ -52,7 +52,7 @@ hipError_t launch_q4_pad(const Q4View& w, const uint16_t* X, int M, uint16_t* Wp
 struct Q4Plan {
   int cg, S;
   bool direct;
-  int SK;  // slices of din of the low-rank inner product
+  int SK;  // slices of din of the low-rank inner product, at most kQ4TSlices
   size_t part_floats(int M, int N) const { return direct ? 0 : (size_t)S * M * N; }
 };
 Q4Plan q4_plan(int M, int K, int N, bool lora);

@@ -98,8 +98,7 @@ __global__ __launch_bounds__(kConvThreads) void q4_pad_kernel(Q4View w, const ui
 // times as long for: 61 rows of 11008 channels 23.5 us, X alone through LDS
 // 18.8.)
 // Codes and X run D steps of 128 channels ahead.  With the low-rank term the
-// workgroups also compute T = Down x, a row and a slice of din at a time, while
-// their first codes are on the way.
+// waves also compute T = Down x, once their share of the product is done.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128, kStepGroups = kStep / kQ4Group;
 
@@ -114,76 +113,73 @@ __device__ __forceinline__ T scalar(const T* p) {
 // s_waitcnt immediate for "vmcnt <= v" (expcnt and lgkmcnt not waited)
 constexpr int vmcnt_imm(int v) { return (v & 15) | ((v >> 4) << 14) | (7 << 4) | (15 << 8); }
 
-// Slice `sl` of SK of row k's low-rank inner product, T[sl][k][q] = Down[q] . x
-// over its channels (the scale is left out); slice 0 also writes the row's
-// descriptor.  A wave takes R ranks at a time, its lanes 8 channels each.
-template <int NW>
-__device__ __forceinline__ void shrink_slice(const PoolView& pv, int proj, const uint16_t* __restrict__ X,
-                                             const int32_t* __restrict__ row_key, int M, int k, int sl, int SK,
-                                             float* __restrict__ T) {
-  constexpr int R = 16 / NW;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int key = scalar(row_key + k);
-  if (sl == 0) write_row_desc(pv, proj, key, k, row_desc(T, M, pv.max_rank));
-  if (key < 0) return;
-  const int rank = scalar(pv.rank + key);
-  const int32_t* dpage = pv.down_page + ((size_t)key * pv.n_proj + proj) * pv.max_rank;
-  const int n8 = pv.din / 8, b0 = (int)((long)n8 * sl / SK), b1 = (int)((long)n8 * (sl + 1) / SK);
-  const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)k * pv.din);
-  for (int q0 = R * wave; q0 < rank; q0 += R * NW) {
-    const uint4* d[R];
+// The low-rank inner products T[sl][r][q] = Down[q] . x_r over slice sl of SK
+// of the channels (the scale is left out), of up to 64 rows from X on; a lane
+// holds the key and the rank of each (0: none).  An item is a slice of up to
+// 16 rows of one adapter by 16 of its ranks, one wave's; the waves take the
+// items in turn.  So rows that share an adapter share what is read of it (61
+// rows of 11008 channels, three adapters of up to 64 ranks: the layer 29.2 us,
+// with each row by itself 38.7).
+__device__ __forceinline__ void shrink_items(const PoolView& pv, int proj, const uint16_t* __restrict__ X,
+                                             int key, int rank, int worker, int workers, int SK,
+                                             float* __restrict__ T, size_t slice) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const uint64_t served = __ballot(rank > 0);
+  const int steps = pv.din / 32;
+  for (int t = worker;; t += workers) {
+    // the item's adapter: the first rows of each one's in turn
+    int unit = t / SK, k0 = 0, n_ranks = 0, chunk = 0, block = 0;
+    uint64_t left = served, rows = 0;
+    while (left) {
+      const int first = __builtin_ctzll(left);
+      k0 = __builtin_amdgcn_readlane(key, first);
+      n_ranks = __builtin_amdgcn_readlane(rank, first);
+      rows = __ballot(key == k0) & left;
+      const int blocks = (n_ranks + 15) / 16, units = (__popcll(rows) + 15) / 16 * blocks;
+      if (unit < units) {
+        chunk = unit / blocks, block = unit % blocks;
+        break;
+      }
+      unit -= units;
+      left &= ~rows;
+    }
+    if (!left) return;
+    const int sl = t % SK, u0 = (int)((long)steps * sl / SK), u1 = (int)((long)steps * (sl + 1) / SK);
+    // lanes r16 of every quarter hold row r16 of the chunk, or its first
+    const int at = __popcll(rows & ((1ull << lane) - 1)) - 16 * chunk, n = min(__popcll(rows) - 16 * chunk, 16);
+    int row = 0;
+    {
+      const bool mine = ((rows >> lane) & 1) != 0 && at >= 0 && at < 16;
+      // (the others send to lanes that nothing is read from)
+      row = __builtin_amdgcn_ds_permute((mine ? at : 16 + (lane & 31)) * 4, lane);
+      row = __shfl(row, r16 < n ? r16 : 0, 64);
+    }
+    const int32_t* dpage = pv.down_page + ((size_t)k0 * pv.n_proj + proj) * pv.max_rank;
+    const int page = dpage[min(16 * block + r16, n_ranks - 1)];
+    const uint4* x = reinterpret_cast<const uint4*>(X + (size_t)row * pv.din) + q;
+    const uint4* d = reinterpret_cast<const uint4*>(pv.down + (size_t)page * pv.din) + q;
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 8;
+    for (int u = u0; u < u1; u += U) {
+      uint4 xa[U], da[U];
 #pragma unroll
-    for (int e = 0; e < R; ++e)
-      d[e] = reinterpret_cast<const uint4*>(pv.down + (size_t)scalar(dpage + min(q0 + e, rank - 1)) * pv.din);
-    float v[R];
-#pragma unroll
-    for (int e = 0; e < R; ++e) v[e] = 0.f;
-    constexpr int U = 4;
-    for (int i = b0 + lane; i < b1; i += 64 * U) {
-      uint4 x[U], w[U][R];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = min(i + 64 * u, b1 - 1);
-        x[u] = xr[at];
-#pragma unroll
-        for (int e = 0; e < R; ++e) w[u][e] = d[e][at];
+      for (int e = 0; e < U; ++e) {
+        const int v = min(u + e, u1 - 1);
+        xa[e] = x[4 * v];
+        da[e] = d[4 * v];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + 64 * u >= b1) x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (i + 64 * u < b1) {
-          const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-          for (int e = 0; e < R; ++e) {
-            const uint32_t ww[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              v[e] = fmaf(lo_bf(ww[f]), lo_bf(xw[f]), v[e]);
-              v[e] = fmaf(hi_bf(ww[f]), hi_bf(xw[f]), v[e]);
-            }
-          }
-        }
+      for (int e = 0; e < U; ++e) {
+        if (u + e < u1)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xa[e]), as_bf16x8(da[e]), acc, 0, 0, 0);
       }
     }
-    // halves of the wave, then quarters for four ranks, sum a rank each
-    float t;
-    int mine;
-    if constexpr (R == 2) {
-      const bool up = (lane & 32) != 0;
-      t = (up ? v[1] : v[0]) + __shfl_xor(up ? v[0] : v[1], 32, 64);
-      t += __shfl_xor(t, 16, 64);
-      mine = up ? 1 : 0;
-    } else {
-      static_assert(R == 4, "two or four ranks a wave");
-      const bool up = (lane & 32) != 0, odd = (lane & 16) != 0;
-      const float a = (up ? v[2] : v[0]) + __shfl_xor(up ? v[0] : v[2], 32, 64);
-      const float b = (up ? v[3] : v[1]) + __shfl_xor(up ? v[1] : v[3], 32, 64);
-      t = (odd ? b : a) + __shfl_xor(odd ? a : b, 16, 64);
-      mine = (up ? 2 : 0) + (odd ? 1 : 0);
-    }
+    if (16 * block + r16 >= n_ranks) n_ranks = 0;  // a lane behind the last rank writes nothing
 #pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) t += __shfl_xor(t, m, 64);
-    if ((lane & (R == 2 ? 31 : 15)) == 0 && q0 + mine < rank) T[((size_t)sl * M + k) * pv.max_rank + q0 + mine] = t;
+    for (int v = 0; v < 4; ++v) {
+      const int r = __shfl(row, q * 4 + v, 64);
+      if (n_ranks > 0 && q * 4 + v < n) T[sl * slice + (size_t)r * pv.max_rank + 16 * block + r16] = acc[v];
+    }
   }
 }
 
@@ -248,8 +244,15 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
     asm volatile("" ::: "memory");
   };
   auto slot_of = [&](int d) { return d == 0 ? x0 : (d == 1 ? x1 : (d == 2 ? x2 : x3)); };
+  // (each row's adapter and rank, for later: loaded here, they are waited for
+  // with the first steps)
+  const int key = LORA && lane < M ? row_key[m0 + lane] : -1;
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d, slot_of(d), sb[d]);
+  asm volatile("" ::: "memory");
+  const int rank = key >= 0 ? pv.rank[key] : 0;
+  asm volatile("" ::: "memory");
 
   floatx4 acc[CG][MB];
 #pragma unroll
@@ -332,8 +335,8 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   }
 
   if (LORA) {
-    for (int t = blockIdx.x; t < rows * SK; t += gridDim.x)
-      shrink_slice<NW>(pv, proj, Xall, row_key, rows, t % rows, t / rows, SK, T);
+    shrink_items(pv, proj, X, key, rank, (int)(blockIdx.x % (ncb * S)) + ncb * S * wave, ncb * S * NW, SK,
+                 T + (size_t)m0 * pv.max_rank, (size_t)rows * pv.max_rank);
   }
 
   // the waves' shares of K, in order; a thread takes four rows of a column
@@ -373,47 +376,104 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 }
 
 // Sums the S slices' partial products in order, adds the row's low-rank term
-// and writes Y; 8 columns a thread.  VEC: N a multiple of 8, 16-byte aligned.
-constexpr int kQ4FinishThreads = 64;
+// (T's slices in order, then the ranks in order) and writes Y: a workgroup 512
+// columns of a row, eight to a thread, side by side with VEC (N a multiple of
+// 8, 16-byte aligned), 64 apart without (1024 rows of 4100 columns, 16 ranks:
+// 48 us, side by side 82).  What takes the time is waiting, so a round's pages
+// of Up are on their way while those of the round before are added.
+constexpr int kQ4FinishThreads = 64, kQ4FinishColumns = 8 * kQ4FinishThreads;
 template <bool VEC, bool LORA>
 __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float* __restrict__ part, int S,
                                                                      uint16_t* __restrict__ Y, int M, int N,
-                                                                     PoolView pv, const float* __restrict__ T, int SK) {
-  const int t = blockIdx.x * kQ4FinishThreads + threadIdx.x;
-  const int per_row = (N + 7) / 8;
-  if (t >= M * per_row) return;
-  const int r = t / per_row, c0 = (t % per_row) * 8;
+                                                                     PoolView pv, int proj,
+                                                                     const int32_t* __restrict__ row_key,
+                                                                     const float* __restrict__ T, int SK) {
+  const int lane = threadIdx.x, r = (int)blockIdx.y, b0 = (int)blockIdx.x * kQ4FinishColumns;
+  // past the last column: the last again, not written
+  const auto column = [&](int e) { return VEC ? min(b0 + 8 * lane, N - 8) + e : min(b0 + lane + 64 * e, N - 1); };
+  const int key = LORA ? scalar(row_key + r) : -1;
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  const float* p = part + (size_t)r * N + c0;
+  const float* p = part + (size_t)r * N;
   const size_t stride = (size_t)M * N;
 #pragma unroll 4
   for (int s = 0; s < S; ++s, p += stride) {
     if (VEC) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      const float4 a = *reinterpret_cast<const float4*>(p + column(0)), b = *reinterpret_cast<const float4*>(p + column(4));
       sum[0] += a.x; sum[1] += a.y; sum[2] += a.z; sum[3] += a.w;
       sum[4] += b.x; sum[5] += b.y; sum[6] += b.z; sum[7] += b.w;
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c0 + e < N) sum[e] += p[e];
+      for (int e = 0; e < 8; ++e) sum[e] += p[column(e)];
     }
   }
-  if (LORA) {
-    float y[8];
-    lora_delta8_desc<VEC, true, 16>(pv, row_desc(const_cast<float*>(T), M, pv.max_rank), T, r, M, c0, N, y, SK);
+  if (LORA && key >= 0) {
+    const int rank = scalar(pv.rank + key);
+    const float scale = scalar(pv.scale + key);
+    const int32_t* upage = pv.up_page + ((size_t)key * pv.n_proj + proj) * pv.max_rank;
+    float low[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += y[e];
+    for (int e = 0; e < 8; ++e) low[e] = 0.f;
+    constexpr int Q = VEC ? 16 : 8;  // ranks of a round
+    struct Round { uint4 u[Q]; };
+    for (int q0 = 0; q0 < rank; q0 += 64) {
+      const int n = min(rank - q0, 64), own = q0 + min(lane, n - 1);  // a rank a lane
+      const int page = upage[own];
+      float t = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < SK; ++k) t += T[((size_t)k * M + r) * pv.max_rank + own];
+      t *= scale;
+      const auto load = [&](int j, Round& o) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          const uint16_t* up = pv.up + (size_t)__builtin_amdgcn_readlane(page, min(j + i, n - 1)) * N;
+          if (VEC) {
+            o.u[i] = *reinterpret_cast<const uint4*>(up + column(0));
+          } else {
+            o.u[i] = make_uint4(up[column(0)] | (uint32_t)up[column(1)] << 16, up[column(2)] | (uint32_t)up[column(3)] << 16,
+                                up[column(4)] | (uint32_t)up[column(5)] << 16, up[column(6)] | (uint32_t)up[column(7)] << 16);
+          }
+        }
+      };
+      const auto add = [&](int j, const Round& o) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          if (j + i >= n) break;
+          const float ti = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(t), j + i));
+          const uint32_t w[4] = {o.u[i].x, o.u[i].y, o.u[i].z, o.u[i].w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            low[2 * f] = fmaf(ti, lo_bf(w[f]), low[2 * f]);
+            low[2 * f + 1] = fmaf(ti, hi_bf(w[f]), low[2 * f + 1]);
+          }
+        }
+      };
+      Round a, b;
+      load(0, a);
+      for (int j = 0; j < n; j += 2 * Q) {
+        if (j + Q < n) load(j + Q, b);
+        add(j, a);
+        if (j + 2 * Q < n) load(j + 2 * Q, a);
+        if (j + Q < n) add(j + Q, b);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += low[e];
   }
-  uint16_t* y = Y + (size_t)r * N + c0;
+  if (LORA && key == -2) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = __uint_as_float(0x7fc00000u);
+  }
+  uint16_t* y = Y + (size_t)r * N;
   if (VEC) {
-    *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3]),
-                                              pack_bf2(sum[4], sum[5]), pack_bf2(sum[6], sum[7]));
+    if (b0 + 8 * lane < N)
+      *reinterpret_cast<uint4*>(y + b0 + 8 * lane) = make_uint4(pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3]),
+                                                                pack_bf2(sum[4], sum[5]), pack_bf2(sum[6], sum[7]));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (c0 + e < N) y[e] = (uint16_t)f2bf(sum[e]);
+      if (b0 + lane + 64 * e < N) y[b0 + lane + 64 * e] = (uint16_t)f2bf(sum[e]);
   }
 }
 
@@ -514,11 +574,9 @@ Q4Plan q4_plan(int M, int K, int N, bool lora) {
   if (p.S > 16) p.S = 16;
   if (p.S < 1) p.S = 1;
   p.direct = p.S == 1 && !lora;
-  // the low-rank inner product: a slice of a row to a workgroup
-  p.SK = ncb * p.S / M;
-  if (p.SK > rows_t_slices(M)) p.SK = rows_t_slices(M);
-  if (p.SK > (K + 511) / 512) p.SK = (K + 511) / 512;
-  if (p.SK < 1) p.SK = 1;
+  // the low-rank inner product: slices of 512 channels or more
+  p.SK = (K + 511) / 512;
+  if (p.SK > kQ4TSlices) p.SK = kQ4TSlices;
   return p;
 }
 
@@ -530,17 +588,21 @@ hipError_t launch_q4_rows(const Q4View& w, const uint16_t* X, int M, uint16_t* Y
   if (e != hipSuccess || p.direct) return e;
   const bool vec = w.N % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
                    (!pv || reinterpret_cast<uintptr_t>(pv->up) % 16 == 0);
-  const dim3 g((M * ((w.N + 7) / 8) + kQ4FinishThreads - 1) / kQ4FinishThreads), b(kQ4FinishThreads);
+  const dim3 g((w.N + kQ4FinishColumns - 1) / kQ4FinishColumns, M), b(kQ4FinishThreads);
   if (pv) {
     if (vec)
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T, p.SK);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
+                   row_key, T, p.SK);
     else
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, true>), g, b, 0, stream, part, p.S, Y, M, w.N, *pv, T, p.SK);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, true>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
+                   row_key, T, p.SK);
   } else {
     if (vec)
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T, p.SK);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
+                   row_key, T, p.SK);
     else
-      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, T, p.SK);
+      MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
+                   row_key, T, p.SK);
   }
   return launched();
 }
