@@ -729,6 +729,9 @@ class Q4Weight:
                              "[dout][din / 2] and [dout][din / 32]")
         if scales.get_device() != codes.get_device():
             raise ValueError("scales is on another device than codes")
+        self._hold(codes, scales)
+
+    def _hold(self, codes, scales):
         self.codes, self.scales = codes, scales
         self.device_index = codes.get_device()
         self._d = _Q4Desc(codes.data_ptr(), scales.data_ptr(), self.din, self.dout)
@@ -740,19 +743,19 @@ def q4_quantize(W) -> Q4Weight:
     torch = _torch()
     if _bf16_dev(W, "W").dim() != 2 or W.shape[1] < 32 or W.shape[1] % 32:
         raise ValueError(f"W has shape {tuple(W.shape)}, expected [dout][din], din a multiple of 32")
-    dout, din = W.shape
-    codes = W.new_empty((dout, din // 2), dtype=torch.uint8)
-    scales = W.new_empty((dout, din // 32), dtype=torch.uint8)
-    _check(lib().mlora_q4_quantize(W.data_ptr(), dout, din, codes.data_ptr(), scales.data_ptr(),
-                                   _raw_stream(W.get_device())), "mlora_q4_quantize")
-    return Q4Weight(codes, scales)
+    w = Q4Weight.__new__(Q4Weight)
+    w.dout, w.din = W.shape
+    w._hold(W.new_empty((w.dout, w.din // 2), dtype=torch.uint8), W.new_empty((w.dout, w.din // 32), dtype=torch.uint8))
+    _check(lib().mlora_q4_quantize(W.data_ptr(), w.dout, w.din, w._d.codes, w._d.scales, _raw_stream(w.device_index)),
+           "mlora_q4_quantize")
+    return w
 
 
 def q4_dequantize(w: Q4Weight, out=None):
     """The weight as bf16 [dout][din] (every 4-bit weight is a bf16 value)."""
     torch = _torch()
     if out is None:
-        out = torch.empty((w.dout, w.din), dtype=torch.bfloat16, device=w.codes.device)
+        out = w.codes.new_empty((w.dout, w.din), dtype=torch.bfloat16)
     _on_device(out, "out", torch.bfloat16, w.device_index, (w.dout, w.din))
     _check(lib().mlora_q4_dequantize(w._ref, out.data_ptr(), _raw_stream(w.device_index)), "mlora_q4_dequantize")
     return out

@@ -377,20 +377,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 
 // Sums the S slices' partial products in order, adds the row's low-rank term
 // (T's slices in order, then the ranks in order) and writes Y: a workgroup 512
-// columns of a row, eight to a thread, side by side with VEC (N a multiple of
-// 8, 16-byte aligned), 64 apart without (1024 rows of 4100 columns, 16 ranks:
-// 48 us, side by side 82).  What takes the time is waiting, so a round's pages
-// of Up are on their way while those of the round before are added.
+// columns of a row, eight side by side to a thread, loaded at once wherever
+// they begin (rows of an odd N have no alignment; 1024 rows of 4100 columns,
+// 16 ranks: 14 us, a column at a time 48).  The last thread of a row takes the
+// last eight and writes what is its own.  What takes the time is waiting, so a
+// round's pages of Up are on their way while those of the round before are
+// added.  WIDE: N >= 8; else a column at a time.
+struct __attribute__((packed, aligned(2))) Words4 { uint32_t v[4]; };
+struct __attribute__((packed, aligned(4))) Floats8 { float v[8]; };
 constexpr int kQ4FinishThreads = 64, kQ4FinishColumns = 8 * kQ4FinishThreads;
-template <bool VEC, bool LORA>
+template <bool WIDE, bool LORA>
 __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float* __restrict__ part, int S,
                                                                      uint16_t* __restrict__ Y, int M, int N,
                                                                      PoolView pv, int proj,
                                                                      const int32_t* __restrict__ row_key,
                                                                      const float* __restrict__ T, int SK) {
   const int lane = threadIdx.x, r = (int)blockIdx.y, b0 = (int)blockIdx.x * kQ4FinishColumns;
-  // past the last column: the last again, not written
-  const auto column = [&](int e) { return VEC ? min(b0 + 8 * lane, N - 8) + e : min(b0 + lane + 64 * e, N - 1); };
+  const int c0 = b0 + 8 * lane, at = WIDE ? min(c0, N - 8) : 0;  // this thread's columns, and the eight it loads
   const int key = LORA ? scalar(row_key + r) : -1;
   float sum[8];
 #pragma unroll
@@ -399,13 +402,13 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
   const size_t stride = (size_t)M * N;
 #pragma unroll 4
   for (int s = 0; s < S; ++s, p += stride) {
-    if (VEC) {
-      const float4 a = *reinterpret_cast<const float4*>(p + column(0)), b = *reinterpret_cast<const float4*>(p + column(4));
-      sum[0] += a.x; sum[1] += a.y; sum[2] += a.z; sum[3] += a.w;
-      sum[4] += b.x; sum[5] += b.y; sum[6] += b.z; sum[7] += b.w;
+    if (WIDE) {
+      const Floats8 f = *reinterpret_cast<const Floats8*>(p + at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += f.v[e];
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += p[column(e)];
+      for (int e = 0; e < 8; ++e) sum[e] += p[min(e, N - 1)];
     }
   }
   if (LORA && key >= 0) {
@@ -415,8 +418,8 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
     float low[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) low[e] = 0.f;
-    constexpr int Q = VEC ? 16 : 8;  // ranks of a round
-    struct Round { uint4 u[Q]; };
+    constexpr int Q = 16;  // ranks of a round
+    struct Round { Words4 u[Q]; };
     for (int q0 = 0; q0 < rank; q0 += 64) {
       const int n = min(rank - q0, 64), own = q0 + min(lane, n - 1);  // a rank a lane
       const int page = upage[own];
@@ -428,11 +431,11 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
           const uint16_t* up = pv.up + (size_t)__builtin_amdgcn_readlane(page, min(j + i, n - 1)) * N;
-          if (VEC) {
-            o.u[i] = *reinterpret_cast<const uint4*>(up + column(0));
+          if (WIDE) {
+            o.u[i] = *reinterpret_cast<const Words4*>(up + at);
           } else {
-            o.u[i] = make_uint4(up[column(0)] | (uint32_t)up[column(1)] << 16, up[column(2)] | (uint32_t)up[column(3)] << 16,
-                                up[column(4)] | (uint32_t)up[column(5)] << 16, up[column(6)] | (uint32_t)up[column(7)] << 16);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) o.u[i].v[f] = up[min(2 * f, N - 1)] | (uint32_t)up[min(2 * f + 1, N - 1)] << 16;
           }
         }
       };
@@ -441,11 +444,10 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
         for (int i = 0; i < Q; ++i) {
           if (j + i >= n) break;
           const float ti = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(t), j + i));
-          const uint32_t w[4] = {o.u[i].x, o.u[i].y, o.u[i].z, o.u[i].w};
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            low[2 * f] = fmaf(ti, lo_bf(w[f]), low[2 * f]);
-            low[2 * f + 1] = fmaf(ti, hi_bf(w[f]), low[2 * f + 1]);
+            low[2 * f] = fmaf(ti, lo_bf(o.u[i].v[f]), low[2 * f]);
+            low[2 * f + 1] = fmaf(ti, hi_bf(o.u[i].v[f]), low[2 * f + 1]);
           }
         }
       };
@@ -466,14 +468,13 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
     for (int e = 0; e < 8; ++e) sum[e] = __uint_as_float(0x7fc00000u);
   }
   uint16_t* y = Y + (size_t)r * N;
-  if (VEC) {
-    if (b0 + 8 * lane < N)
-      *reinterpret_cast<uint4*>(y + b0 + 8 * lane) = make_uint4(pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3]),
-                                                                pack_bf2(sum[4], sum[5]), pack_bf2(sum[6], sum[7]));
+  if (WIDE && c0 + 8 <= N) {
+    *reinterpret_cast<Words4*>(y + c0) = Words4{
+        {pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3]), pack_bf2(sum[4], sum[5]), pack_bf2(sum[6], sum[7])}};
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (b0 + lane + 64 * e < N) y[b0 + lane + 64 * e] = (uint16_t)f2bf(sum[e]);
+      if (at + e >= c0 && at + e < N) y[at + e] = (uint16_t)f2bf(sum[e]);
   }
 }
 
@@ -586,18 +587,17 @@ hipError_t launch_q4_rows(const Q4View& w, const uint16_t* X, int M, uint16_t* Y
   const RowsArgs a{w, X, M, Y, part, pv ? *pv : PoolView{}, proj, row_key, T};
   const hipError_t e = pv ? launch_rows_form<true>(a, p, stream) : launch_rows_form<false>(a, p, stream);
   if (e != hipSuccess || p.direct) return e;
-  const bool vec = w.N % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
-                   (!pv || reinterpret_cast<uintptr_t>(pv->up) % 16 == 0);
+  const bool wide = w.N >= 8;
   const dim3 g((w.N + kQ4FinishColumns - 1) / kQ4FinishColumns, M), b(kQ4FinishThreads);
   if (pv) {
-    if (vec)
+    if (wide)
       MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
                    row_key, T, p.SK);
     else
       MLORA_LAUNCH("q4_finish", (q4_finish_kernel<false, true>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
                    row_key, T, p.SK);
   } else {
-    if (vec)
+    if (wide)
       MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, false>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
                    row_key, T, p.SK);
     else

@@ -130,7 +130,7 @@ LAYERS = [(1, 256, 64, {0: 8}), (13, 1056, 72, {0: 1, 1: 16, 2: 64}), (32, 4096,
           (200, 1024, 72, {0: 8, 1: 64}), (1100, 128, 72, {0: 8, 1: 40}), (130, 2080, 72, {0: 128, 1: 16}),
           (255, 512, 264, {0: 1, 1: 16, 2: 33}), (257, 512, 264, {0: 8, 1: 16}), (300, 1056, 33, {0: 16, 1: 3}),
           (1000, 160, 72, {0: 8, 1: 40}), (70, 96, 40, {0: 4}), (1100, 160, 72, {0: 8, 1: 40}),
-          (2100, 160, 2050, {0: 8, 1: 40})]
+          (2100, 160, 2050, {0: 8, 1: 40}), (5, 256, 5, {0: 8}), (20, 256, 9, {0: 16}), (70, 1056, 517, {0: 64, 2: 17})]
 
 
 @pytest.mark.parametrize("n,din,dout,ranks", LAYERS)
