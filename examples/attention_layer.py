@@ -2,7 +2,11 @@
 each row's own adapter, the new keys and values into the paged 8-bit cache,
 attention over it, and the output projection.
 
-    python examples/attention_layer.py [--requests 32] [--prompt 300] [--steps 64]
+    python examples/attention_layer.py [--requests 32] [--prompt 300] [--steps 64] [--four-bit]
+
+With --four-bit the projections' weights are in 4 bits, the heads of q and k
+are normed and rotated before the cache takes them, and each request's next
+token is sampled from an output head of 32000 words, in 4 bits as well.
 
 Prompts of different lengths are taken in first, in ragged batches; then every
 request decodes one token a step from a HIP graph that is captured once: the
@@ -62,6 +66,47 @@ class AttentionLayer:
             p.close()
 
 
+class StepLayer(AttentionLayer):
+    """The layer with its weights in 4 bits, norms and a rotation of the heads,
+    and behind it an output head whose logits the next tokens are drawn from."""
+
+    def __init__(self, seed, hidden, heads, kv_heads, dim, ranks, vocab, requests):
+        super().__init__(seed, hidden, heads, kv_heads, dim, ranks)
+        self.W0 = [M.q4_quantize(W) for W in self.W0]
+        rng = np.random.default_rng(seed)
+        part = lambda *shape: torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(torch.bfloat16).cuda()
+        self.head = M.q4_quantize(part(vocab, hidden) * (2.0 / hidden ** 0.5))
+        self.norms = [1 + part(dim) / 8 for _ in range(2)]
+        self.rotary = M.Rotary(dim, base=500000.0)
+        # each request's own temperature and top-p; the first takes the likeliest token
+        self.temperature = torch.linspace(0.0, 1.2, requests, device="cuda")
+        self.top_p = torch.full((requests,), 0.9, device="cuda")
+
+    def scratch(self, cache, batch):
+        requests = len(self.top_p)
+        return ([M.new_q4_work(W, batch.n_rows, p) for W, p in zip(self.W0, self.pools)],
+                M.new_kv_work(cache, batch, self.heads), M.new_q4_work(self.head, requests),
+                M.new_sample_work(requests, self.head.dout))
+
+    def __call__(self, X, row_adapter, cache, layer, batch, scratch, window=0):
+        """As above, with the normed and rotated q and k, and of each request's
+        last row the logits, the random numbers and the tokens."""
+        n, (proj_work, kv_work, head_work, sample_work) = batch.n_rows, scratch
+        seg = M.build_segments(self.pools[0], row_adapter)
+        qkv = M.q4_apply(self.pools[0], 0, X, self.W0[0], seg, work=proj_work[0])
+        q, k, v = qkv.view(n, -1, self.dim).split((self.heads, self.kv_heads, self.kv_heads), dim=1)
+        q, k = M.qk_norm_rotary(q, k, batch, self.rotary, *self.norms)
+        M.kv_append(cache, layer, k, v, batch)
+        att = M.kv_attention(cache, layer, q, batch, window=window, work=kv_work)
+        out = M.q4_apply(self.pools[1], 0, att.view(n, -1), self.W0[1], seg, work=proj_work[1])
+        # (a request without a row in this batch takes another's; its token is not used)
+        last = out.index_select(0, (batch.row_off[1:] - 1).clamp_(min=0))
+        logits = M.q4_gemm(last, self.head, work=head_work)
+        u = torch.rand_like(self.top_p)
+        tokens = M.sample(logits, u, temperature=self.temperature, top_p=self.top_p, work=sample_work)
+        return out, att, qkv, q, k, logits, u, tokens
+
+
 def make_table(lengths, block, n_blocks, rng):
     """Pages for `lengths` tokens of each sequence, in any order; -1 past them."""
     pages = [-(-n // block) for n in lengths]
@@ -85,12 +130,16 @@ def prompt_batches(lens, limit):
 
 
 def run(requests=32, prompt=300, steps=64, hidden=4096, heads=32, kv_heads=8, dim=128, block=16, ranks=None, seed=1,
-        chunk=8192, on_step=None):
+        chunk=8192, on_step=None, vocab=0):
     """Prompts, then `steps` decoded tokens a request; microseconds of a decode
-    step.  on_step(layer, X, ids, cache, batch, results) sees every step."""
+    step.  With `vocab` the layer in 4 bits, with tokens sampled from so many
+    words.  on_step(layer, X, ids, cache, batch, results) sees every step."""
     ranks = ranks or {0: 16, 1: 8, 2: 64}
     rng = np.random.default_rng(seed)
-    layer = AttentionLayer(seed, hidden, heads, kv_heads, dim, ranks)
+    if vocab:
+        layer = StepLayer(seed, hidden, heads, kv_heads, dim, ranks, vocab, requests)
+    else:
+        layer = AttentionLayer(seed, hidden, heads, kv_heads, dim, ranks)
     lens = rng.integers(max(1, prompt // 4), prompt + 1, size=requests)
     adapter = rng.integers(-1, max(ranks) + 1, size=requests).astype(np.int32)
     need = sum(-(-(int(n) + steps) // block) for n in lens)
@@ -146,8 +195,10 @@ def main():
     p.add_argument("--requests", type=int, default=32)
     p.add_argument("--prompt", type=int, default=300, help="longest prompt; the shortest is a quarter of it")
     p.add_argument("--steps", type=int, default=64, help="tokens decoded by each request")
+    p.add_argument("--four-bit", action="store_true",
+                   help="weights in 4 bits, normed and rotated heads, the next token sampled")
     a = p.parse_args()
-    us = run(a.requests, a.prompt, a.steps)
+    us = run(a.requests, a.prompt, a.steps, vocab=32000 if a.four_bit else 0)
     if us is not None:
         print(f"{a.requests} requests, prompts up to {a.prompt} tokens: {us:.1f} us a decode step of one layer, "
               f"{a.requests / us * 1e6:.0f} tokens/s")
