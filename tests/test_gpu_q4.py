@@ -220,3 +220,59 @@ def test_graph_and_streams(M):
             assert torch.equal(Y.view(torch.int16), eager.view(torch.int16)), f"replay {i}"
             assert torch.isfinite(other).all() and torch.isfinite(big).all()
     pool.close()
+
+
+def test_two_graphs_and_an_eager_call_side_by_side(M):
+    """Two captured layers with work buffers of their own, replayed on two
+    streams at once while a third call runs, each as when alone."""
+    torch = torch_cuda()
+    say("4-bit layers side by side")
+    w = synth.custom("q4two", 4, 1056, 136, synth.random_ids(4, 40, [0, 1], 0.25), {0: 33, 1: 8})
+    pool = make_pool(M, w)
+    _, _, w4 = weight(M, np.random.default_rng(2), 136, 1056)
+    X, ids = to_dev_bf16(w.x_bits()), ids_dev(w.row_adapter)
+    seg = M.build_segments(pool, ids)
+    want = M.q4_apply(pool, 0, X, w4, seg)
+    want2 = M.q4_gemm(X, w4)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            work = M.new_q4_work(w4, 40, pool)
+            M.q4_apply(pool, 0, X, w4, seg, work=work)
+            side.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                Y = M.q4_apply(pool, 0, X, w4, seg, work=work)
+        graphs.append((side, g, Y, work))
+    for i in range(4):
+        for side, g, Y, _ in graphs:
+            with torch.cuda.stream(side):
+                Y.zero_()
+                g.replay()
+        Y2 = M.q4_gemm(X, w4)
+        torch.cuda.synchronize()
+        assert all(torch.equal(Y, want) for _, _, Y, _ in graphs) and torch.equal(Y2, want2), f"replay {i}"
+    pool.close()
+
+
+def test_outputs_end_where_they_end(M):
+    """Nothing is written before or behind Y, whatever its alignment."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(8)
+    w = synth.custom("q4ends", 6, 256, 45, synth.random_ids(6, 70, [0], 0.25), {0: 16})
+    pool = make_pool(M, w)
+    _, _, w4 = weight(M, rng, 45, 256)
+    X, seg = to_dev_bf16(w.x_bits()), M.build_segments(pool, ids_dev(w.row_adapter))
+    for n in (1, 33, 70):
+        say(f"guarded outputs, {n} rows")
+        buf = torch.full((3 + n * 45 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        Y = buf[3:3 + n * 45].view(n, 45)
+        M.q4_gemm(X[:n], w4, Y=Y)
+        assert torch.equal(Y, M.q4_gemm(X[:n], w4)) and (buf[:3] == 7).all() and (buf[3 + n * 45:] == 7).all()
+    buf = torch.full((3 + 70 * 45 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = M.q4_apply(pool, 0, X, w4, seg, Y=buf[3:3 + 70 * 45].view(70, 45))
+    again = M.q4_apply(pool, 0, X, w4, seg)
+    assert torch.equal(Y, again) and (buf[:3] == 7).all() and (buf[3 + 70 * 45:] == 7).all()
+    pool.close()

@@ -137,6 +137,52 @@ def test_infinities_and_nan(M, V, f32):
         assert np.array_equal(got, ref), f"{kw} {got} {ref}"
 
 
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V", [16384, 16391, 70000])
+def test_masks_in_large_vocabularies(M, V, f32):
+    """Infinities, NaN, both zeros and masks of the lowest value in rows whose
+    values are counted; unaligned rows; every mix of filters."""
+    say(f"masks {V} f32={f32}")
+    rng = np.random.default_rng(V + 7)
+    n = 12
+    x = rng.normal(size=(n, V)) * 2
+    lowest = -3.3895313892515355e38
+    x[0] = -INF
+    x[1] = NAN
+    x[2, 5:] = -INF
+    x[3, :9] = INF
+    x[4, rng.random(V) < 0.999] = lowest
+    x[5] = lowest
+    x[6, rng.random(V) < 0.9] = -INF
+    x[7] = np.where(rng.random(V) < 0.5, 0.0, -0.0)
+    x[8, rng.random(V) < 0.5] = NAN
+    x[9] = np.where(rng.random(V) < 0.01, -0.0, -2.0)
+    x[10] = -np.abs(x[10]) * 1e-40
+    x[11, 7] = INF
+    u = rng.random(n, dtype=np.float32)
+    for kw in (dict(), dict(temperature=[0.0] * n), dict(temperature=[INF] * n), dict(temperature=[1e-40, 1e30, 1e38] * 4),
+               dict(top_k=[600, 5000, 2, V] * 3), dict(top_p=[0.9, 0.3, 0.9999] * 4),
+               dict(top_k=[700] * n, top_p=[0.9] * n, min_p=[0.01] * n), dict(min_p=[0.5, 1.0, 1e-9] * 4),
+               dict(top_p=[NAN, -1.0, 0.0] * 4, min_p=[NAN, 0.2, 0.0] * 4)):
+        got, ref = run(M, x, u, f32, pad=V % 4 + 1, **kw)
+        assert np.array_equal(got, ref), f"{kw}: rows {np.flatnonzero(got != ref)}"
+
+
+@pytest.mark.parametrize("V", [65535, 65536, 65537, 131072, 200003])
+def test_more_equal_logits_than_16_bits_count(M, V):
+    say(f"equal logits {V}")
+    x = np.full((5, V), 0.25)
+    x[1, 1000] = 3.0
+    x[2, ::2] = -1.0
+    x[3, :3], x[3, -3:] = 8.0, 8.0
+    x[4, V // 2:] = 0.2490234375  # the next value below
+    u = np.array([0.9999, 0.5, 0.75, 0.9, 0.6], np.float32)
+    for kw in (dict(), dict(top_k=[V - 1, V // 2, 66000, 7, 40000]), dict(top_p=[0.99, 0.5, 0.75, 0.3, 0.6]),
+               dict(top_k=[1000] * 5, top_p=[0.999] * 5), dict(min_p=[0.9, 0.01, 0.5, 0.001, 1.0])):
+        got, ref = run(M, x, u, False, **kw)
+        assert np.array_equal(got, ref), f"{kw}: {got} {ref}"
+
+
 def test_random_numbers_at_and_past_the_ends(M):
     say("u outside [0, 1)")
     x = np.log(np.array([[1.0, 4.0, 2.0, 4.0, 0.5]])).repeat(6, 0)
