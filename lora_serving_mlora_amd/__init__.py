@@ -934,10 +934,14 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         out = torch.empty_like(u, dtype=torch.int32)
     else:
         _on_device(out, "out", torch.int32, device, (n,))
-    work = new_sample_work(n, vocab, logits.device) if work is None else _work(work, device)
+    wp = wn = 0
+    if work is not None:
+        wp, wn = _work(work, device).data_ptr(), work.nbytes
+    elif sample_work_bytes(n, vocab):
+        work = new_sample_work(n, vocab, logits.device)
+        wp, wn = work.data_ptr(), work.nbytes
     status = lib().mlora_sample(logits.data_ptr(), logits.dtype is torch.float32, logits.stride(0) if n > 1 else vocab,
-                                n, vocab, u.data_ptr(), *ptr, out.data_ptr(), work.data_ptr(), work.nbytes,
-                                _raw_stream(device))
+                                n, vocab, u.data_ptr(), *ptr, out.data_ptr(), wp, wn, _raw_stream(device))
     if status != OK:
         raise MloraError(status, "mlora_sample")
     return out
