@@ -551,8 +551,8 @@ mlora_status mlora_q4_dequantize(const mlora_q4_weight* w, uint16_t* W, void* st
  *   work: device scratch of mlora_q4_work_bytes(w, pool, n_rows) bytes (pool
  *         NULL for mlora_q4_gemm), 256-byte aligned, contents free; calls
  *         that share it must not overlap.
- * Few rows (256 to 1024 by the shape) multiply the codes as they are; more
- * rows make the weight bf16 in `work` first.  Results are the same bit for bit from call to call. */
+ * Few rows and small products multiply the codes as they are; larger ones
+ * make the weight bf16 in `work` first.  Results are the same bit for bit from call to call. */
 size_t mlora_q4_work_bytes(const mlora_q4_weight* w, const mlora_pool* pool, int32_t n_rows);
 mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t* Y, int32_t n_rows, void* work,
                            size_t work_bytes, void* stream);

@@ -1305,7 +1305,7 @@ mlora_status q4_view(const mlora_q4_weight* w, mlora::Q4View* v) {
   return MLORA_OK;
 }
 bool q4_few(const mlora::Q4View& w, const mlora_pool* p, int n) {
-  return mlora::q4_few_rows(n, w.K, w.N, p != nullptr) && (!p || aligned16(p->d.down_pages));
+  return mlora::q4_few_rows(n, w.K, w.N) && (!p || aligned16(p->d.down_pages));
 }
 // channels of a row of the bf16 weight: the products of many rows want whole
 // steps, the per-row layer takes any (and rounds its result once)

@@ -35,11 +35,11 @@ hipError_t launch_q4_quantize(const uint16_t* W, uint8_t* codes, uint8_t* scales
 hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* W, int64_t n,
                                 hipStream_t stream);
 
-// Products of few rows take the codes as they are, 64 rows to a workgroup;
-// larger ones make the weight bf16 first and take the bf16 products.
+// Products of few rows, and small ones, take the codes as they are, 64 rows to
+// a workgroup; larger ones make the weight bf16 first and take the bf16 products.
 constexpr int kQ4RowBlock = 64, kQ4MinDin = 128, kQ4TSlices = 16;
 inline int q4_row_blocks(int M) { return (M + kQ4RowBlock - 1) / kQ4RowBlock; }
-bool q4_few_rows(int M, int K, int N, bool lora);
+bool q4_few_rows(int M, int K, int N);
 // For the bf16 products of more rows: the weight, and X, in rows of a multiple
 // of 128 channels, zeros past K (the products are slow for other K: 2048 rows,
 // K 4064: 103 us, padded 80; with the low-rank term 117 and 96).

@@ -537,14 +537,17 @@ hipError_t launch_q4_dequantize(const uint8_t* codes, const uint8_t* scales, uin
   return launched();
 }
 
-bool q4_few_rows(int M, int K, int N, bool lora) {
-  // The bf16 products have rates that these do not reach, but the weight has
-  // to be made first (4096 x 4096: 256 rows 18.3 against 30.0 us, with the
-  // low-rank term 27.9 against 32.8; 512 rows 32.6 against 34.5, with it 48.5
-  // against 43.8; 1024 rows 59 against 48), and they are slow where K is not
-  // whole steps or N not whole vectors (1024 rows, K 4064: 63 against 196 us).
+bool q4_few_rows(int M, int K, int N) {
+  // The bf16 products have a rate that these do not reach, but the weight has
+  // to be made first, and a small product does not reach it either (4096
+  // channels, three adapters of rank 16; as they are against bf16 first: 256
+  // rows x 4096 27.5 and 32.8 us, 600 x 4096 60 and 62, 1500 x 2048 66 and 75,
+  // 400 x 11008 96 and 88, 1024 x 4096 88 and 67, 4000 x 1000 92 and 78; 800 x
+  // 1024 of 1024 channels 17 and 33).  Where K is not whole steps or N not
+  // whole vectors they are slower still (1024 x 4096, K 4064: 82 and 234 us).
   if (K < kQ4MinDin) return false;
-  return M <= (K % kStep == 0 && N % 8 == 0 ? (lora ? 256 : 512) : 1024);
+  if (M <= 256 || (long)M * N <= 3l << 20) return true;
+  return (K % kStep != 0 || N % 8 != 0) && M <= 1024;
 }
 
 hipError_t launch_q4_pad(const Q4View& w, const uint16_t* X, int M, uint16_t* Wp, uint16_t* Xp, hipStream_t stream) {

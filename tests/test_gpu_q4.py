@@ -92,7 +92,8 @@ SHAPES = [(1, 32, 1), (1, 4096, 256), (2, 96, 17), (5, 160, 64), (16, 4064, 200)
           (33, 1056, 257), (48, 512, 16), (63, 544, 130), (64, 4096, 128), (64, 11008, 64), (16, 11008, 40),
           (3, 20000, 24), (65, 512, 128), (100, 96, 33), (257, 1024, 264), (1025, 256, 136), (128, 4064, 200),
           (300, 2080, 41), (511, 256, 520), (513, 256, 520), (700, 160, 1032), (1000, 96, 24), (1024, 1056, 17),
-          (1200, 1056, 264), (2100, 96, 2052), (1030, 32, 40)]
+          (1200, 1056, 264), (2100, 96, 2052), (1030, 32, 40), (800, 256, 4104), (1600, 256, 2056),
+          (2100, 256, 2056), (1100, 160, 2880), (4000, 128, 72)]
 
 
 @pytest.mark.parametrize("n,din,dout", SHAPES)
@@ -130,7 +131,9 @@ LAYERS = [(1, 256, 64, {0: 8}), (13, 1056, 72, {0: 1, 1: 16, 2: 64}), (32, 4096,
           (200, 1024, 72, {0: 8, 1: 64}), (1100, 128, 72, {0: 8, 1: 40}), (130, 2080, 72, {0: 128, 1: 16}),
           (255, 512, 264, {0: 1, 1: 16, 2: 33}), (257, 512, 264, {0: 8, 1: 16}), (300, 1056, 33, {0: 16, 1: 3}),
           (1000, 160, 72, {0: 8, 1: 40}), (70, 96, 40, {0: 4}), (1100, 160, 72, {0: 8, 1: 40}),
-          (2100, 160, 2050, {0: 8, 1: 40}), (5, 256, 5, {0: 8}), (20, 256, 9, {0: 16}), (70, 1056, 517, {0: 64, 2: 17})]
+          (2100, 160, 2050, {0: 8, 1: 40}), (5, 256, 5, {0: 8}), (20, 256, 9, {0: 16}), (70, 1056, 517, {0: 64, 2: 17}),
+          (800, 256, 4104, {0: 8, 1: 40}), (1600, 256, 2056, {0: 8, 1: 40}), (2100, 256, 2048, {0: 16, 1: 40}),
+          (1100, 160, 2880, {0: 8, 1: 40}), (3000, 256, 64, {0: 8, 1: 16})]
 
 
 @pytest.mark.parametrize("n,din,dout,ranks", LAYERS)
