@@ -17,7 +17,20 @@ constexpr int kConvThreads = 256;
 // quantiser: a thread takes 8 weights, four threads a group.  The least
 // exponent e with amax <= 6 * 2^e is read off the bits of amax = 1.m * 2^x:
 // 6 = 1.5 * 2^2, so e = x - 2 up to a fraction of one half and x - 1 above.
+// The codes come from the conversion instruction, which rounds to nearest
+// even and ends at 6.  Bound by memory (4096 -> 11008 and read back: 43.4 us at
+// 5.3 TB/s; with the codes counted up by seven comparisons 49.3, bound by those).
 // ---------------------------------------------------------------------------
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// the other value of lanes 1 and 2 apart
+template <int PERM>
+__device__ __forceinline__ uint32_t quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, PERM, 0xf, 0xf, true);
+}
 __global__ __launch_bounds__(kConvThreads) void q4_quantize_kernel(const uint16_t* __restrict__ W,
                                                                    uint8_t* __restrict__ codes,
                                                                    uint8_t* __restrict__ scales, int64_t n8) {
@@ -25,26 +38,22 @@ __global__ __launch_bounds__(kConvThreads) void q4_quantize_kernel(const uint16_
   for (int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x; i < n8; i += stride) {
     const uint4 v = reinterpret_cast<const uint4*>(W)[i];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;
+    uint32_t both = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+    for (int j = 0; j < 4; ++j) both = max_u16x2(both, w[j] & 0x7fff7fffu);
     // n8 is a multiple of 4: the four threads of a group are here together
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+    both = max_u16x2(both, quad<0xb1>(both));  // lanes 1 apart
+    both = max_u16x2(both, quad<0x4e>(both));  // lanes 2 apart
+    const uint32_t top = max(both & 0xffffu, both >> 16);
     uint32_t b = 255, code = 0;
     if (top < 0x7f80u) {
       const int e = (int)(top >> 7) - ((top & 127u) <= 64u ? 2 : 1);
       b = min(max(e, kQ4ExpMin), kQ4ExpMax);
-      const float inv = __uint_as_float((254u - b) << 23);  // 2^(127 - b), a normal number for b <= 252
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t x = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        const float a = bf2f(x & 0x7fffu) * inv;
-        // halfway values go to the even code
-        uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.f);
-        c |= (x >> 15) << 3;
-        code |= c << (4 * j);
-      }
+      const float scale = q4_scale(b);
+      code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2, w[0]), scale, 0);
+      code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2, w[1]), scale, 1);
+      code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2, w[2]), scale, 2);
+      code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2, w[3]), scale, 3);
     }
     reinterpret_cast<uint32_t*>(codes)[i] = code;
     if ((i & 3) == 0) scales[i >> 2] = (uint8_t)b;

@@ -61,6 +61,44 @@ def test_quantizer(M, dout, din):
     assert np.array_equal(dev_to_f64(M.q4_dequantize(q)), S.q4_values(codes, scales))
 
 
+def test_quantizer_of_every_value(M):
+    """Every finite bf16 value as the largest of its group and beside it, in
+    groups whose scale another value sets, the smallest numbers included."""
+    torch = torch_cuda()
+    say("quantise every value")
+    bits = np.arange(1 << 16)
+    bits = bits[(bits & 0x7f80) != 0x7f80].astype(np.uint16)
+    value = lambda b: (b.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    rng = np.random.default_rng(12)
+    x = value(bits)
+    beside = value(rng.choice(bits, (len(x), 15)))
+    near = bf16(x[:, None] * rng.uniform(-1, 1, (len(x), 8)))
+    halves = bf16(np.clip(np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -133)))[:, None] - 2)
+                          * np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]), 0, 3.3e38))
+    for other in (np.zeros((len(x), 31)), np.concatenate([x[:, None] * 0, near, near / 4, near / 64, x[:, None] * 0 + 0.0,
+                                                          near[:, :5]], 1),
+                  np.concatenate([halves, -halves, beside * 0], 1), np.concatenate([beside, beside, x[:, None]], 1)):
+        w = bf16(np.concatenate([x[:, None], other], 1))
+        w = w[np.isfinite(w).all(1)]
+        # the oracle's definition, all groups at once
+        m, ex = np.frexp(np.abs(w).max(1))  # 6 * 2^e is 0.75 * 2^(e + 3)
+        e = np.where(m == 0, -125, np.clip(np.where(m <= 0.75, ex - 3, ex - 2), -125, 125))
+        a = np.minimum(np.abs(w) / np.exp2(e)[:, None], 6.0)
+        d = np.abs(a[..., None] - S.LEVELS)
+        k = d.argmin(-1)
+        tie = np.take_along_axis(d, np.minimum(k + 1, 7)[..., None], -1)[..., 0] == d.min(-1)
+        k += (tie & (k % 2 == 1) & (k < 7)).astype(k.dtype)
+        q = M.q4_quantize(dev(w))
+        assert np.array_equal(q.scales.cpu().numpy()[:, 0], e + 127)
+        got = dev_to_f64(M.q4_dequantize(q))
+        want = np.where(np.signbit(w), -S.LEVELS[k], S.LEVELS[k]) * np.exp2(e)[:, None]
+        bad = np.argwhere(got != want)
+        assert len(bad) == 0, f"{len(bad)}, first {w[tuple(bad[0])]}: {got[tuple(bad[0])]}, not {want[tuple(bad[0])]}"
+        rows = rng.choice(len(w), 40, replace=False)
+        codes, scales = S.q4_quantize(w[rows])
+        assert np.array_equal(S.q4_values(codes, scales), want[rows])
+
+
 def test_quantizer_of_infinities_and_nan(M):
     torch = torch_cuda()
     w = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
