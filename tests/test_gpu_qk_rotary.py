@@ -53,6 +53,8 @@ CASES = [  # new, total, heads, kv_heads, dim, rot, norm, interleaved
     ([2, 2], [100000, 999999], 2, 2, 112, 16, False, False),
     ([1] * 300, [3] * 300, 2, 1, 32, 32, True, False),
     ([1500], [1500], 40, 8, 64, 64, True, False),
+    ([700, 800], [700, 900], 40, 8, 256, 256, True, False),
+    ([3000], [3007], 9, 9, 80, 32, True, True),
     ([5], [2], 2, 1, 48, 40, True, True),  # three rows at negative positions
 ]
 
