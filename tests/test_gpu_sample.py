@@ -138,6 +138,28 @@ def test_infinities_and_nan(M, V, f32):
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V", [129, 700, 1024, 1025, 2352, 5000])
+def test_long_lists(M, V, f32):
+    """Hundreds of tokens in the list: spread out, close together beside a few
+    far above, many of a value; top-k whose list overruns."""
+    say(f"long lists {V} f32={f32}")
+    rng = np.random.default_rng(V + 3)
+    n = 16
+    x = rng.normal(size=(n, V)) * np.repeat([0.5, 2.0, 1e-3, 8.0], 4)[:, None]
+    x[::4, 3] += 12.0
+    x[1::4, V // 2:V // 2 + 5] += 30.0
+    x[2::4] = np.round(x[2::4] * 4) / 4
+    u = rng.random(n, dtype=np.float32)
+    t = rng.choice([0.4, 0.7, 1.0, 1.4], n)
+    for kw in (dict(temperature=t), dict(temperature=t, top_k=rng.integers(200, 513, n)),
+               dict(temperature=t, top_k=rng.integers(300, 900, n), top_p=[0.95] * n),
+               dict(temperature=t, top_p=rng.random(n), min_p=[0.0, 0.01] * 8),
+               dict(temperature=t, top_k=[V - 1, V, V + 1, 512] * 4, min_p=[1e-6] * n), dict(temperature=[1e-3] * n)):
+        got, ref = run(M, x, u, f32, **kw)
+        assert np.array_equal(got, ref), f"{kw}: rows {np.flatnonzero(got != ref)}"
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("V", [16384, 16391, 70000])
 def test_masks_in_large_vocabularies(M, V, f32):
     """Infinities, NaN, both zeros and masks of the lowest value in rows whose
