@@ -385,23 +385,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 }
 
 // Sums the S slices' partial products in order, adds the row's low-rank term
-// (T's slices in order, then the ranks in order) and writes Y: a workgroup 512
-// columns of a row, eight side by side to a thread, loaded at once wherever
-// they begin (rows of an odd N have no alignment; 1024 rows of 4100 columns,
-// 16 ranks: 14 us, a column at a time 48).  The last thread of a row takes the
-// last eight and writes what is its own.  What takes the time is waiting, so a
-// round's pages of Up are on their way while those of the round before are
-// added.  WIDE: N >= 8; else a column at a time.
+// (T's slices in order; the ranks 16 at a time to the waves in turn, each in
+// order, then the waves' sums in order) and writes Y: a workgroup 512 columns of
+// a row, eight side by side to a thread, loaded at once wherever they begin
+// (rows of an odd N have no alignment; 1024 rows of 4100 columns, 16 ranks: 14
+// us, a column at a time 48).  The last thread of a row takes the last eight
+// and writes what is its own.  What takes the time is waiting, so a wave's next
+// pages of Up are on their way while those before are added.  WIDE: N >= 8;
+// else a column at a time.
 struct __attribute__((packed, aligned(2))) Words4 { uint32_t v[4]; };
 struct __attribute__((packed, aligned(4))) Floats8 { float v[8]; };
-constexpr int kQ4FinishThreads = 64, kQ4FinishColumns = 8 * kQ4FinishThreads;
+constexpr int kQ4FinishColumns = 8 * 64, kQ4FinishWaves = 4;
 template <bool WIDE, bool LORA>
-__global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float* __restrict__ part, int S,
+__global__ __launch_bounds__(64 * (LORA ? kQ4FinishWaves : 1)) void q4_finish_kernel(const float* __restrict__ part, int S,
                                                                      uint16_t* __restrict__ Y, int M, int N,
                                                                      PoolView pv, int proj,
                                                                      const int32_t* __restrict__ row_key,
                                                                      const float* __restrict__ T, int SK) {
-  const int lane = threadIdx.x, r = (int)blockIdx.y, b0 = (int)blockIdx.x * kQ4FinishColumns;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int r = (int)blockIdx.y, b0 = (int)blockIdx.x * kQ4FinishColumns;
   const int c0 = b0 + 8 * lane, at = WIDE ? min(c0, N - 8) : 0;  // this thread's columns, and the eight it loads
   const int key = LORA ? scalar(row_key + r) : -1;
   float sum[8];
@@ -410,7 +412,7 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
   const float* p = part + (size_t)r * N;
   const size_t stride = (size_t)M * N;
 #pragma unroll 4
-  for (int s = 0; s < S; ++s, p += stride) {
+  for (int s = 0; s < (wave == 0 ? S : 0); ++s, p += stride) {
     if (WIDE) {
       const Floats8 f = *reinterpret_cast<const Floats8*>(p + at);
 #pragma unroll
@@ -420,13 +422,13 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
       for (int e = 0; e < 8; ++e) sum[e] += p[min(e, N - 1)];
     }
   }
+  float low[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) low[e] = 0.f;
   if (LORA && key >= 0) {
     const int rank = scalar(pv.rank + key);
     const float scale = scalar(pv.scale + key);
     const int32_t* upage = pv.up_page + ((size_t)key * pv.n_proj + proj) * pv.max_rank;
-    float low[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) low[e] = 0.f;
     constexpr int Q = 16;  // ranks of a round
     struct Round { Words4 u[Q]; };
     for (int q0 = 0; q0 < rank; q0 += 64) {
@@ -461,14 +463,27 @@ __global__ __launch_bounds__(kQ4FinishThreads) void q4_finish_kernel(const float
         }
       };
       Round a, b;
-      load(0, a);
-      for (int j = 0; j < n; j += 2 * Q) {
-        if (j + Q < n) load(j + Q, b);
+      const int step = Q * waves;
+      if (Q * wave < n) load(Q * wave, a);
+      for (int j = Q * wave; j < n; j += 2 * step) {
+        if (j + step < n) load(j + step, b);
         add(j, a);
-        if (j + 2 * Q < n) load(j + 2 * Q, a);
-        if (j + Q < n) add(j + Q, b);
+        if (j + 2 * step < n) load(j + 2 * step, a);
+        if (j + step < n) add(j + step, b);
       }
     }
+  }
+  if (LORA) {
+    __shared__ float other[kQ4FinishWaves - 1][8][64];
+    if (wave > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[wave - 1][e][lane] = low[e];
+    }
+    if (waves > 1) __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < waves; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) low[e] += other[w - 1][e][lane];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += low[e];
   }
@@ -600,7 +615,14 @@ hipError_t launch_q4_rows(const Q4View& w, const uint16_t* X, int M, uint16_t* Y
   const hipError_t e = pv ? launch_rows_form<true>(a, p, stream) : launch_rows_form<false>(a, p, stream);
   if (e != hipSuccess || p.direct) return e;
   const bool wide = w.N >= 8;
-  const dim3 g((w.N + kQ4FinishColumns - 1) / kQ4FinishColumns, M), b(kQ4FinishThreads);
+  // several waves a workgroup while that leaves a CU 16 of them (61 rows of 4096
+  // columns, ranks to 64: 6.1 us, one wave 8.7; 406 rows of 15769: 62 and 45)
+  const int tiles = (w.N + kQ4FinishColumns - 1) / kQ4FinishColumns;
+  int waves = pv ? (pv->max_rank + 15) / 16 : 1;
+  const int room = (int)(4096 / ((long)tiles * M));
+  waves = waves > kQ4FinishWaves ? kQ4FinishWaves : waves;
+  waves = waves > room ? (room < 1 ? 1 : room) : waves;
+  const dim3 g(tiles, M), b(64 * waves);
   if (pv) {
     if (wide)
       MLORA_LAUNCH("q4_finish", (q4_finish_kernel<true, true>), g, b, 0, stream, part, p.S, Y, M, w.N, a.pv, proj,
