@@ -128,7 +128,7 @@ constexpr int vmcnt_imm(int v) { return (v & 15) | ((v >> 4) << 14) | (7 << 4) |
 // 16 rows of one adapter by 16 of its ranks, one wave's; the waves take the
 // items in turn.  So rows that share an adapter share what is read of it (61
 // rows of 11008 channels, three adapters of up to 64 ranks: the layer 29.2 us,
-// with each row by itself 38.7).
+// when each row read its own 38.7).
 __device__ __forceinline__ void shrink_items(const PoolView& pv, int proj, const uint16_t* __restrict__ X,
                                              int key, int rank, int worker, int workers, int SK,
                                              float* __restrict__ T, size_t slice) {
