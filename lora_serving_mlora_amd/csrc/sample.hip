@@ -107,7 +107,7 @@ __device__ __forceinline__ void for_row(const T* __restrict__ row, int V, F f) {
 struct Row {
   double mx, scale;  // largest logit; log2(e) / T
   float fit, fit0;   // a logit's place in the histogram: fit0 - fit * logit
-  float least;       // the weight is 0 from here down
+  float least;       // below mx; the weight is 0 from here down
   bool top;          // the largest is +infinity: those stand at 0, all else at -infinity
   // A logit as it is compared: NaN counts as -infinity.
   __device__ __forceinline__ float clean(float x) const {
@@ -118,7 +118,7 @@ struct Row {
 };
 
 // Weight of a logit, in multiples of 2^-42.  ANY: of any clean logit; else of
-// one that is not below r.least.
+// one above r.least.
 template <bool ANY = false>
 __device__ __forceinline__ u64 weight(const Row& r, float x) {
   double d = ((double)x - r.mx) * r.scale;
@@ -157,6 +157,13 @@ __device__ __forceinline__ float from_rising(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 __device__ __forceinline__ float next_up(float x) { return from_rising(rising(x) + 1); }
+__device__ __forceinline__ float next_down(float x) { return from_rising(rising(x) - 1); }
+
+// A logit below the largest from which on, down, every weight is 0: 31 nats
+// down (44.7 powers of two).  The difference is rounded, to `mx` itself where
+// 31 temperatures are less than half its last place, so the float below it is
+// taken: that lies below `mx` and not above the exact difference.
+__device__ __forceinline__ float least_of(float mx, float temp) { return next_down(mx - 31.f * fminf(temp, 1e30f)); }
 
 // place of a token in the order, rising: falling logits, then rising indices
 __device__ __forceinline__ u64 order_key(float x, int i) {
@@ -290,11 +297,13 @@ __device__ __forceinline__ u64 histogram(S& sh, const Row& r, const T* __restric
       const float x = fmaxf(xs[e], r.least);
       const u64 w = weight(r, x);
       const int b = range_of(r, x);
+      // (at r.least, where all lower logits are taken to, w is 0 or, at a
+      // temperature far below the last place of a logit, nothing at all)
       if (x > r.least) {
         atomicAdd(&sh.bins.mass[b], w);
         if (counts) atomicAdd(&sh.bins.count[b], 1u);
+        if (least != 0 && w >= least) strong += w;
       }
-      if (least != 0 && w >= least) strong += w;
       if (e & 1) __builtin_amdgcn_sched_barrier(0);  // keeps the next logits' work out of the registers
     }
   });
@@ -691,7 +700,7 @@ __device__ __forceinline__ bool sample_values(S& sh, const uint16_t* __restrict_
     Row r;
     r.mx = mx;
     r.scale = 1.4426950408889634074 / (double)temp;
-    r.least = mx - 31.f * temp;
+    r.least = least_of(mx, temp);
     r.top = false;
     r.fit = r.fit0 = 0.f;
     const u64 least = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFrac)) : 0ull;
@@ -851,7 +860,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   if (r.top) mx = mn = 0.f;
   r.mx = mx;
   r.scale = 1.4426950408889634074 / (double)temp;
-  r.least = mx - 31.f * fminf(temp, 1e30f);  // 44.7 powers of two down
+  r.least = least_of(mx, temp);
   const float span = fminf(mx - mn, 30.f * temp);
   r.fit = span > 0.f ? fminf((float)kBins / span, 1e36f / fmaxf(fabsf(mx), 1.f)) : 0.f;
   r.fit0 = mx * r.fit;
