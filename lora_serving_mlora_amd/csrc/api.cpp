@@ -872,7 +872,8 @@ namespace {
 // more has its low-rank term added by a separate expand instead of the
 // epilogue (may_overrun).  txw (the widest rank-concatenated batch, Ux
 // living in the upt region) is the largest multiple of 64 up to
-// kMaxConcatRanks that upt_units holds.
+// kMaxConcatRanks that upt_units holds.  terms: numbers that stand for a t
+// (LoraOperands); with two of them all of it is twice as large.
 constexpr size_t kMaxEpilogueBytes = 256u << 20;
 struct EpilogueLayout {
   size_t koff, over, kx, tx, upt, total;
@@ -880,28 +881,28 @@ struct EpilogueLayout {
   int txw;
   bool may_overrun;
 };
-EpilogueLayout epilogue_layout(const mlora_pool* p, int n) {
-  const int wt = mlora::t_rows_width(p->d.max_rank);
+EpilogueLayout epilogue_layout(const mlora_pool* p, int n, int terms) {
+  const int wt = terms * mlora::t_rows_width(p->d.max_rank);
   EpilogueLayout L{};
   L.koff = align256((size_t)n * wt * 2);
   L.over = L.koff + align256((size_t)p->d.max_adapters * 4);
   L.kx = L.over + 4;
-  const long worst = (long)mlora::lora_upt_units(n, p->d.max_adapters, p->d.max_rank);
-  L.txw = (int)std::min<long>(mlora::kMaxConcatRanks, worst / 64 * 64);
+  const long worst = terms * (long)mlora::lora_upt_units(n, p->d.max_adapters, p->d.max_rank);
+  L.txw = (int)std::min<long>(terms * mlora::kMaxConcatRanks, worst / 64 * 64);
   L.tx = L.over + 256;
   L.upt = L.tx + align256((size_t)n * L.txw * 2);
   const size_t row = (size_t)p->d.dout * 2;
-  const long budget = L.upt < kMaxEpilogueBytes ? (long)((kMaxEpilogueBytes - L.upt) / row) / 16 * 16 : 0;
+  const size_t most = terms * kMaxEpilogueBytes;
+  const long budget = L.upt < most ? (long)((most - L.upt) / row) / 16 * 16 : 0;
   L.upt_units = std::min(worst, budget);
   if (L.upt_units < L.txw) L.txw = (int)(L.upt_units / 64 * 64);
   L.may_overrun = L.upt_units < worst;
   L.total = L.upt + align256((size_t)L.upt_units * row);
   return L;
 }
-size_t lora_operands_bytes(const mlora_pool* p, int n) { return epilogue_layout(p, n).total; }
 // The GEMM epilogue needs room for at least one adapter of the largest rank.
-bool big_epilogue_fits(const mlora_pool* p, int n) {
-  return epilogue_layout(p, n).upt_units >= mlora::t_rows_width(p->d.max_rank) &&
+bool big_epilogue_fits(const mlora_pool* p, int n, int terms) {
+  return epilogue_layout(p, n, terms).upt_units >= terms * mlora::t_rows_width(p->d.max_rank) &&
          (size_t)p->d.n_up_pages * p->d.dout < (1u << 31);
 }
 
@@ -935,14 +936,15 @@ namespace {
 // (its base GEMM splits K through them when the buffer holds them, else it
 // takes the one-pass form); SPLIT its shrink slices, plus the epilogue's
 // operands for large batches, and the split-K partials of its base GEMM.
+size_t split_work_bytes(const mlora_pool* p, int n, int terms) {
+  const size_t b = align256((size_t)split_chunks(p, n) * n * p->d.max_rank * sizeof(float));
+  return big_epilogue_fits(p, n, terms) ? b + epilogue_layout(p, n, terms).total : b;
+}
 size_t plan_work_bytes(const mlora_pool* p, int n, int variant) {
   if (n <= 0) return 0;
   const size_t rows = n <= kRowsMax ? rows_work_bytes(p, n) : 0;
   if (variant != MLORA_VARIANT_SPLIT) return rows;
-  const int chunks = std::max(split_chunks(p, n), 1);
-  size_t b = align256((size_t)chunks * n * p->d.max_rank * sizeof(float));
-  if (big_epilogue_fits(p, n)) b += lora_operands_bytes(p, n);
-  return std::max(b, rows);
+  return std::max(split_work_bytes(p, n, 1), rows);
 }
 }  // namespace
 
@@ -969,17 +971,18 @@ namespace {
 // The split plan of a large batch: shrink, the low-rank operands, then one GEMM
 // that adds the low-rank term itself (Y written once).  vb, Xb, W: what the
 // GEMM takes, the pool's view, X and the weight, or with more channels to a
-// row, zeros in X and W.
+// row, zeros in X and W.  terms: bf16 numbers that stand for a t.
 mlora_status apply_big(const mlora_pool* p, int32_t proj, const uint16_t* X, const PoolView& vb, const uint16_t* Xb,
-                       const uint16_t* W, const int32_t* ws, uint16_t* Y, int n, void* work, hipStream_t s) {
+                       const uint16_t* W, const int32_t* ws, uint16_t* Y, int n, void* work, int terms,
+                       hipStream_t s) {
   const mlora_pool_desc& d = p->d;
   const PoolView v = p->view();
   mlora_status st;
   const int chunks = split_chunks(p, n);
   float* T = static_cast<float*>(work);
   char* w = static_cast<char*>(work) + align256((size_t)chunks * n * d.max_rank * sizeof(float));
-  const int wt = mlora::t_rows_width(d.max_rank);
-  const EpilogueLayout L = epilogue_layout(p, n);
+  const int wt = terms * mlora::t_rows_width(d.max_rank);
+  const EpilogueLayout L = epilogue_layout(p, n, terms);
   uint16_t* tb = reinterpret_cast<uint16_t*>(w);
   int32_t* koff = reinterpret_cast<int32_t*>(w + L.koff);
   int32_t* over = reinterpret_cast<int32_t*>(w + L.over);
@@ -989,10 +992,10 @@ mlora_status apply_big(const mlora_pool* p, int32_t proj, const uint16_t* X, con
   st = hip_check(mlora::launch_shrink(v, proj, X, ws, n, T, chunks, chunk_elems_for(d.din, chunks), s), "shrink launch");
   if (st != MLORA_OK) return st;
   st = hip_check(mlora::launch_lora_prep(v, proj, ws, n, T, chunks, tb, wt, koff, upt, L.upt_units, over, tx,
-                                         L.txw, kx, s),
+                                         L.txw, kx, terms, s),
                  "low-rank operand launch");
   if (st != MLORA_OK) return st;
-  const mlora::LoraOperands lo{tb, koff, upt, wt, L.may_overrun ? over : nullptr, tx, L.txw, tx ? kx : nullptr};
+  const mlora::LoraOperands lo{tb, koff, upt, wt, L.may_overrun ? over : nullptr, tx, L.txw, tx ? kx : nullptr, terms};
   st = hip_check(mlora::launch_big_lora(vb, Xb, W, ws, lo, Y, n, s), "GEMM + low-rank term launch");
   if (st != MLORA_OK || !L.may_overrun) return st;
   return hip_check(mlora::launch_expand_over(v, proj, T, chunks, ws, Y, n, over, s), "overrun expand launch");
@@ -1026,8 +1029,8 @@ mlora_status mlora_apply(const mlora_pool* p, int32_t proj, const uint16_t* X, c
     return hip_check(mlora::launch_gemm_lora(v, proj, X, W0, ws, w.T, w.part, Y, n, true, s),
                      "per-row shrink + GEMM + expand launch");
   }
-  if (variant == MLORA_VARIANT_SPLIT && big_epilogue_fits(p, n) && mlora::big_lora_ok(v, X, W0, n))
-    return apply_big(p, proj, X, v, X, W0, ws, Y, n, work, s);
+  if (variant == MLORA_VARIANT_SPLIT && big_epilogue_fits(p, n, 1) && mlora::big_lora_ok(v, X, W0, n))
+    return apply_big(p, proj, X, v, X, W0, ws, Y, n, work, 1, s);
   // the base GEMM: split over K with its partials in `work` (per-row
   // layout) when the batch and the buffer allow, else the plain form
   hipError_t ge = hipErrorNotSupported;
@@ -1307,6 +1310,12 @@ mlora_status q4_view(const mlora_q4_weight* w, mlora::Q4View* v) {
 bool q4_few(const mlora::Q4View& w, const mlora_pool* p, int n) {
   return mlora::q4_few_rows(n, w.K, w.N) && (!p || aligned16(p->d.down_pages));
 }
+// Numbers that stand for a low-rank inner value where many rows take it in
+// bf16: two, which leave the layer's result as it is with fp32 values; one moved
+// it by up to a half of its last place (4096 rows of 4096 -> 11008 channels, ranks 8, 16, 64
+// twice: the error against 64 bits 2.02e-3 of the result, 1.66e-3 with two
+// numbers, as of the last rounding alone).
+constexpr int kQ4Terms = 2;
 // channels of a row of the bf16 weight: the products of many rows want whole
 // steps, the per-row layer takes any (and rounds its result once)
 int q4_channels(const mlora::Q4View& w, int n) { return n > kRowsMax ? mlora::q4_padded(w.K) : w.K; }
@@ -1326,7 +1335,7 @@ size_t q4_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
     return (p ? q4_t_bytes(p, n) : 0) +
            align256(mlora::q4_plan(n, w.K, w.N, p != nullptr).part_floats(n, w.N) * sizeof(float));
   const size_t operands = q4_operand_bytes(w, n);
-  if (p) return operands + mlora_work_bytes(p, n);
+  if (p) return operands + (n > kRowsMax ? split_work_bytes(p, n, kQ4Terms) : mlora_work_bytes(p, n));
   return operands + (n <= kRowsMax ? align256(mlora::gemm_lora_part_floats(n, w.N, w.K) * sizeof(float)) : 0);
 }
 // the bf16 weight in `work`, and X where rows are padded: *X is what goes with it
@@ -1430,11 +1439,12 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
   const uint16_t* W = static_cast<const uint16_t*>(work);
   const size_t operands = q4_operand_bytes(v, n);
   char* rest = static_cast<char*>(work) + operands;
-  if (Xb == X) return mlora_apply(p, proj, X, W, seg_ws, Y, n, rest, work_bytes - operands, MLORA_VARIANT_AUTO, stream);
+  if (n <= kRowsMax) return mlora_apply(p, proj, X, W, seg_ws, Y, n, rest, work_bytes - operands, MLORA_VARIANT_AUTO, stream);
   const int32_t* ws = static_cast<const int32_t*>(seg_ws);
   PoolView vb = p->view();
   vb.din = q4_channels(v, n);
-  if (big_epilogue_fits(p, n) && mlora::big_lora_ok(vb, Xb, W, n)) return apply_big(p, proj, X, vb, Xb, W, ws, Y, n, rest, s);
+  if (big_epilogue_fits(p, n, kQ4Terms) && mlora::big_lora_ok(vb, Xb, W, n))
+    return apply_big(p, proj, X, vb, Xb, W, ws, Y, n, rest, kQ4Terms, s);
   st = hip_check(mlora::launch_base_gemm(Xb, W, Y, n, vb.din, v.N, s), "base GEMM launch");
   if (st != MLORA_OK) return st;
   const int chunks = split_chunks(p, n);

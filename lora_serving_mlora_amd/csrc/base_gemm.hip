@@ -829,6 +829,7 @@ __device__ __forceinline__ void ring_lora_epilogue(int wr, int wc, int M, int N,
       koff = 0;
     } else if (a != kNone) {
       rank = uniform_load(pv.rank, a);
+      if (lo.terms == 2) rank = 2 * ((rank + 15) & ~15);
       koff = uniform_load(lo.koff, a);
     }
   };

@@ -165,6 +165,11 @@ hipError_t launch_shrink_rows(const PoolView& pv, int proj, const uint16_t* X, c
 //        Kx for a row with an invalid id,
 //   Ux   bf16 [dout][txw] in the upt region: Up_a[c][q] at column
 //        koff[a] + q, zeros elsewhere below Kx.
+// terms 2: every t as two bf16 numbers, the nearest one and the nearest to
+// what that leaves, so that 16 bits of it enter the product in place of 8.
+// An adapter then has 2 r_pad ranks, those of the first numbers and those of
+// the second ones, with Up's columns twice; wt, upt_units and txw are twice as
+// large.
 struct LoraOperands {
   const uint16_t* tb;
   const int32_t* koff;
@@ -174,8 +179,9 @@ struct LoraOperands {
   const uint16_t* tx = nullptr;
   int txw = 0;
   const int32_t* kx = nullptr;
+  int terms = 1;
 };
-// the largest extra depth of the rank-concatenated form
+// the largest extra depth of the rank-concatenated form (of either term)
 constexpr int kMaxConcatRanks = 256;
 inline int t_rows_width(int max_rank) { return (max_rank + 15) / 16 * 16; }
 // Rank rows of upt for a batch of n rows at most: every adapter of the
@@ -195,7 +201,7 @@ hipError_t launch_big_lora(const PoolView& pv, const uint16_t* X, const uint16_t
 // order); upt has room for upt_units rank rows.
 hipError_t launch_lora_prep(const PoolView& pv, int proj, const int32_t* ws, int n, const float* Ts, int n_chunks,
                             uint16_t* tb, int wt, int32_t* koff, uint16_t* upt, long upt_units, int32_t* over,
-                            uint16_t* tx, int txw, int32_t* kx, hipStream_t stream);
+                            uint16_t* tx, int txw, int32_t* kx, int terms, hipStream_t stream);
 
 hipError_t launch_shrink(const PoolView& pv, int proj, const uint16_t* X, const int32_t* ws, int n,
                          float* T, int n_chunks, int chunk_elems, hipStream_t stream);

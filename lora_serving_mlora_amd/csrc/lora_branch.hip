@@ -725,6 +725,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void shrink_tiles_kernel(PoolView 
 // the epilogue form a block that would end past upt_units rank rows writes
 // nothing, and the first column block of the last segment (of the first,
 // with no segment) records in *over whether the batch's blocks overran.
+// terms 2: t in two bf16 numbers (LoraOperands), r_pad twice as many ranks.
 // ---------------------------------------------------------------------------
 constexpr int kPrepCols = 64;
 constexpr int kConcatSegs = kMaxConcatRanks / 16;  // segments of a concatenated batch, at most
@@ -749,12 +750,21 @@ __device__ __forceinline__ float sum_slices(const float* __restrict__ p, size_t 
   return v;
 }
 
+// t as bf16, or (second) what its bf16 leaves of it, which is 0 beside an
+// infinity or NaN
+__device__ __forceinline__ uint32_t t_term(float t, bool second) {
+  const uint32_t first = f2bf(t);
+  if (!second) return first;
+  return (first & 0x7f80u) == 0x7f80u ? 0u : f2bf(t - bf2f(first));
+}
+
 __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, const int32_t* __restrict__ ws, int n,
                                                         const float* __restrict__ Ts, int n_chunks,
                                                         uint16_t* __restrict__ tb, int wt, int nt,
                                                         int32_t* __restrict__ koff_out, uint16_t* __restrict__ upt,
                                                         long upt_units, int32_t* __restrict__ over,
-                                                        uint16_t* __restrict__ tx, int txw, int32_t* __restrict__ kx_out) {
+                                                        uint16_t* __restrict__ tx, int txw, int32_t* __restrict__ kx_out,
+                                                        int terms) {
   const int tid = threadIdx.x;
   const int nseg = ws[MLORA_SEG_NSEG];
   const int32_t* seg_adapter = ws + MLORA_SEG_ADAPTER(n);
@@ -770,7 +780,7 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
   int all = 0, before = 0;
   for (int s2 = tid; s2 < nseg; s2 += 256) {
     const int ad = seg_adapter[s2];
-    const int rk = pv.rank[ad], rp = rank_pad16(rk);
+    const int rk = pv.rank[ad], rp = rank_pad16(rk) * terms;
     if (s2 < kConcatSegs) {
       tab_ad[s2] = ad;
       tab_rank[s2] = rk;
@@ -818,8 +828,12 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
               rank = tab_rank[s2];
               sc = tab_scale[s2];
             }
-            run += rank_pad16(tab_rank[s2]);
+            run += rank_pad16(tab_rank[s2]) * terms;
           }
+          // first column of the adapter's numbers that this piece has: the
+          // second ones' behind the first ones'
+          const bool second = terms == 2 && c0 - ko >= rank_pad16(rank);
+          if (second) ko += rank_pad16(rank);
           const float* tp = Ts + (size_t)j * pv.max_rank;
           if (n_chunks <= 8) {
             // all 8 x n_chunks loads first, then the sums in slice order
@@ -838,13 +852,13 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
 #pragma unroll
               for (int ch = 0; ch < 8; ++ch)
                 if (ch < n_chunks) v += x[ch][e];
-              if (q >= 0 && q < rank) h[e] = f2bf(v * sc);
+              if (q >= 0 && q < rank) h[e] = t_term(v * sc, second);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int q = c0 + e - ko;
-              if (q >= 0 && q < rank) h[e] = f2bf(sum_slices(tp + q, cs, n_chunks) * sc);
+              if (q >= 0 && q < rank) h[e] = t_term(sum_slices(tp + q, cs, n_chunks) * sc, second);
             }
           }
         }
@@ -857,12 +871,16 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
     const int32_t* perm = ws + MLORA_SEG_PERM(n);
     const int32_t* row_key = ws + MLORA_SEG_ROWKEY(n);
     for (int idx = blockIdx.x * 256 + tid; idx < n_act * wt; idx += nt * 256) {
-      const int j = idx / wt, q = idx % wt;
+      const int j = idx / wt;
+      int q = idx % wt;
       const int row = perm[j];
       const int key = row_key[row];  // >= 0: sorted positions below n_act are rows on resident adapters
+      const int rank = pv.rank[key];
+      const bool second = terms == 2 && q >= rank_pad16(rank);
+      if (second) q -= rank_pad16(rank);
       float v = 0.f;
-      if (q < pv.rank[key]) v = sum_slices(Ts + (size_t)j * pv.max_rank + q, cs, n_chunks) * pv.scale[key];
-      tb[(size_t)row * wt + q] = (uint16_t)f2bf(v);
+      if (q < rank) v = sum_slices(Ts + (size_t)j * pv.max_rank + q, cs, n_chunks) * pv.scale[key];
+      tb[(size_t)row * wt + idx % wt] = (uint16_t)t_term(v, second);
     }
     return;
   }
@@ -871,7 +889,7 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
   if (sidx >= nseg) return;
   const int a = seg_adapter[sidx];
   const int rank = pv.rank[a], rp = rank_pad16(rank);
-  const bool fits = kx > 0 || koff + rp <= upt_units;
+  const bool fits = kx > 0 || koff + rp * terms <= upt_units;
   if (cc == 0 && tid == 0) {
     koff_out[a] = koff;
     if (sidx == nseg - 1) *over = fits ? 0 : 1;
@@ -901,15 +919,17 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(PoolView pv, int proj, c
   __syncthreads();
   // columns out, 8 ranks per 16-byte store: the block [dout][rp] at
   // koff * dout, or columns koff.. of the txw-wide rows
-  const int stride = kx ? txw : rp;
-  uint16_t* dst = kx ? upt + (size_t)c0 * txw + koff : upt + (size_t)koff * pv.dout + (size_t)c0 * rp;
+  const int stride = kx ? txw : rp * terms;
+  uint16_t* dst = kx ? upt + (size_t)c0 * txw + koff : upt + (size_t)koff * pv.dout + (size_t)c0 * stride;
   for (int idx = tid; idx < ncol * (rp / 8); idx += 256) {
     const int cl = idx / (rp / 8), q0 = (idx % (rp / 8)) * 8;
     uint32_t h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = tile[q0 + e][cl];
-    *reinterpret_cast<uint4*>(dst + (size_t)cl * stride + q0) =
-        make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    const uint4 w = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    uint16_t* o = dst + (size_t)cl * stride + q0;
+    *reinterpret_cast<uint4*>(o) = w;
+    if (terms == 2) *reinterpret_cast<uint4*>(o + rp) = w;
   }
   if (kx && sidx == nseg - 1) {
     // zeros from the last adapter's columns up to Kx
@@ -1010,8 +1030,8 @@ hipError_t launch_fused(const PoolView& pv, int proj, const uint16_t* X, const i
 
 hipError_t launch_lora_prep(const PoolView& pv, int proj, const int32_t* ws, int n, const float* Ts, int n_chunks,
                             uint16_t* tb, int wt, int32_t* koff, uint16_t* upt, long upt_units, int32_t* over,
-                            uint16_t* tx, int txw, int32_t* kx, hipStream_t stream) {
-  if (tx != nullptr && (txw % 64 != 0 || txw > kMaxConcatRanks || (long)txw > upt_units))
+                            uint16_t* tx, int txw, int32_t* kx, int terms, hipStream_t stream) {
+  if (tx != nullptr && (txw % 64 != 0 || txw > kMaxConcatRanks * terms || (long)txw > upt_units))
     return hipErrorInvalidValue;
   const long total = (long)n * wt;
   const int nt = (int)((total + 255) / 256 < 1024 ? (total + 255) / 256 : 1024);
@@ -1019,7 +1039,7 @@ hipError_t launch_lora_prep(const PoolView& pv, int proj, const int32_t* ws, int
   const long blocks = (nt > 0 ? nt : 1) + segs * ((pv.dout + kPrepCols - 1) / kPrepCols);
   if (blocks > 0x7fffffffL) return hipErrorInvalidConfiguration;
   MLORA_LAUNCH("lora_prep", lora_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, pv, proj, ws, n, Ts,
-               n_chunks, tb, wt, nt > 0 ? nt : 1, koff, upt, upt_units, over, tx, txw, kx);
+               n_chunks, tb, wt, nt > 0 ? nt : 1, koff, upt, upt_units, over, tx, txw, kx, terms);
   return launched();
 }
 

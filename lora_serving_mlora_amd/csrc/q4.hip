@@ -227,9 +227,8 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   // the end of a row X reads on (the next row, or zeros past the last) and the
   // last group is read again; both count for nothing below.  A step past this
   // wave's last makes the same loads of empty buffers, so that what is on its
-  // way can be told by its number.  X's buffer begins at the step's channels:
-  // a scalar offset would do the same, but does not count where a load's
-  // address is held against the buffer's end.
+  // way can be told by its number.  (X's buffer begins at the step's channels;
+  // a scalar offset need not count where a load is held against its end.)
   auto fetch = [&](int u, uint8_t* slot, uint32_t& sv) {
     const bool any = u < mine;
     const int k0 = any ? (u0 + u) * kStep : 0;
