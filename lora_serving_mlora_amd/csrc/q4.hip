@@ -227,13 +227,11 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   // the end of a row X reads on (the next row, or zeros past the last) and the
   // last group is read again; both count for nothing below.  A step past this
   // wave's last makes the same loads of empty buffers, so that what is on its
-  // way can be told by its number.  (X's buffer begins at the step's channels;
-  // a scalar offset need not count where a load is held against its end.)
+  // way can be told by its number.
   auto fetch = [&](int u, uint8_t* slot, uint32_t& sv) {
     const bool any = u < mine;
-    const int k0 = any ? (u0 + u) * kStep : 0;
-    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(X) + k0, (short)0,
-                                                                        any ? (M * K - k0) * 2 : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(X), (short)0, any ? M * K * 2 : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rc =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wc), (short)0, any ? cols * (K / 2) : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rs =
@@ -250,7 +248,7 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
     for (int i = 0; i < 4 * MB; ++i) {
       const int row = 4 * i + q, r = min(row, M - 1);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, slot + wave * kSlot + i * 1024, 16,
-                                               r * 2 * K + ((r16 ^ (row & 15)) << 4), 0, 0, 0);
+                                               r * 2 * K + ((r16 ^ (row & 15)) << 4), (u0 + u) * kStep * 2, 0, 0);
     }
     asm volatile("" ::: "memory");
   };
