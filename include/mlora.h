@@ -554,8 +554,11 @@ mlora_status mlora_q4_dequantize(const mlora_q4_weight* w, uint16_t* W, void* st
  * Few rows and small products multiply the codes as they are; larger ones
  * make the weight bf16 in `work` first.  The adapters' inner values s_a Down_a x
  * are fp32 up to 1024 rows; above, where they enter a bf16 product, each is the
- * sum of two bf16 numbers (to 2^-16 of it).  Results are the same bit for bit
- * from call to call. */
+ * sum of two bf16 numbers (to 2^-16 of it).  Y is rounded once, but for batches
+ * of more than 1024 rows whose X or bf16 weight has 2^30 numbers or more, or
+ * whose adapters' ranks, each padded to 16, times 4 dout bytes pass some 500
+ * MiB: there the product is rounded to bf16 before the adapters are added.
+ * Results are the same bit for bit from call to call. */
 size_t mlora_q4_work_bytes(const mlora_q4_weight* w, const mlora_pool* pool, int32_t n_rows);
 mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t* Y, int32_t n_rows, void* work,
                            size_t work_bytes, void* stream);

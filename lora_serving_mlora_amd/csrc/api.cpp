@@ -1443,7 +1443,9 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
   const int32_t* ws = static_cast<const int32_t*>(seg_ws);
   PoolView vb = p->view();
   vb.din = q4_channels(v, n);
-  if (big_epilogue_fits(p, n, kQ4Terms) && mlora::big_lora_ok(vb, Xb, W, n))
+  // Whatever the size: the product alone, with the adapters added to it as
+  // bf16, would be rounded twice.
+  if (big_epilogue_fits(p, n, kQ4Terms) && mlora::big_lora_takes(vb, Xb, W, n))
     return apply_big(p, proj, X, vb, Xb, W, ws, Y, n, rest, kQ4Terms, s);
   st = hip_check(mlora::launch_base_gemm(Xb, W, Y, n, vb.din, v.N, s), "base GEMM launch");
   if (st != MLORA_OK) return st;

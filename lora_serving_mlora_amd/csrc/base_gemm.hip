@@ -1879,11 +1879,14 @@ hipError_t launch_base_split(const uint16_t* X, const uint16_t* W, uint16_t* Y, 
 }
 
 
-bool big_lora_ok(const PoolView& pv, const uint16_t* X, const uint16_t* W, int M) {
+bool big_lora_takes(const PoolView& pv, const uint16_t* X, const uint16_t* W, int M) {
   const int K = pv.din, N = pv.dout;
   const bool vec = (K % 8 == 0) && ((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W)) % 16 == 0);
-  return vec && K % kRingKAlign == 0 && (long)M * N >= 2048L * 2048L && (long)M * K * 2 < (1L << 31) &&
-         (long)N * K * 2 < (1L << 31);
+  return vec && K % kRingKAlign == 0 && (long)M * K * 2 < (1L << 31) && (long)N * K * 2 < (1L << 31);
+}
+
+bool big_lora_ok(const PoolView& pv, const uint16_t* X, const uint16_t* W, int M) {
+  return big_lora_takes(pv, X, W, M) && (long)M * pv.dout >= 2048L * 2048L;
 }
 
 hipError_t launch_big_lora(const PoolView& pv, const uint16_t* X, const uint16_t* W, const int32_t* ws,

@@ -192,7 +192,10 @@ inline size_t lora_upt_units(int n, int max_adapters, int max_rank) {
 
 // Large batches: Y = X W^T plus every row's low-rank term, added inside the
 // large GEMM (extra K tiles over the rank-concatenated operands, or its
-// epilogue; no read-modify-write of Y); invalid rows become NaN.  big_lora_ok: the shapes and pointers this kernel takes.
+// epilogue; no read-modify-write of Y); invalid rows become NaN.
+// big_lora_takes: the shapes and pointers this kernel takes; big_lora_ok: and
+// the product is large enough to be faster so.
+bool big_lora_takes(const PoolView& pv, const uint16_t* X, const uint16_t* W, int M);
 bool big_lora_ok(const PoolView& pv, const uint16_t* X, const uint16_t* W, int M);
 hipError_t launch_big_lora(const PoolView& pv, const uint16_t* X, const uint16_t* W, const int32_t* ws,
                            const LoraOperands& lo, uint16_t* Y, int M, hipStream_t stream);

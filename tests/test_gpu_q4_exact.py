@@ -59,6 +59,9 @@ LAYERS = [  # rows, channels, columns, ranks of the adapters
     # adapters side by side, and with more of them than fit
     (1100, 128, 72, [8, 40]), (1100, 160, 3900, [8, 40]), (2100, 160, 2050, [8, 40]), (2100, 256, 2048, [16, 33, 64]),
     (1500, 256, 2800, [128, 128]), (2048, 512, 2056, [64] * 6), (1600, 320, 2700, [1] * 40), (1300, 256, 3300, [128, 7, 100]),
+    # and small products of that many rows
+    (1100, 160, 2880, [8, 40]), (4000, 1024, 1000, [8, 40]), (1100, 96, 40, [4, 17]), (1025, 32, 5, [3]),
+    (2100, 64, 1500, [64] * 9), (3000, 96, 1, [2, 128]), (1200, 1056, 3071, [16]),
 ]
 
 
