@@ -29,6 +29,7 @@
  *    with the low 16 bits dropped), row-major and densely packed.
  *  - All device work is enqueued on the caller's stream (`stream` is a
  *    hipStream_t; NULL means the default stream) and is asynchronous.
+ *    The device of the stream and the buffers has to be the current one.
  *    Calls on one pool must be ordered by the caller: issue them on one
  *    stream, or synchronise between streams.
  *  - Data-dependent errors (a row id that is not -1 and not a resident

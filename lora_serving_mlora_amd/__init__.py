@@ -12,7 +12,8 @@ Typical use::
     seg = build_segments(pool, row_adapter)                  # device int32 [n]
     Y = apply(pool, proj, X, W0, seg)                        # device bf16
 
-and, for the attention between a layer's projections::
+and, for the attention between a layer's projections (these calls and those
+below want their tensors on the current device)::
 
     cache = KVCache(n_layers, n_blocks, kv_heads, dim, block)          # paged 8-bit keys and values
     batch = KVBatch(table, kv_len, row_off, n_rows, max_new=max_new)   # device int32 tensors
@@ -624,9 +625,19 @@ def _kv_rows(x, name: str, cache: KVCache, batch: KVBatch, heads: int):
     return st
 
 
-def _kv_stream(cache: KVCache) -> int:
+def _raw_stream(device: int) -> int:
+    """The current stream of cuda:`device`, which has to be the current device:
+    a launch goes to that one, and to its default stream where the handle is
+    that of a default stream."""
+    C = _torch()._C
+    if C._cuda_getDevice() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{C._cuda_getDevice()}")
     # the handle alone: building a Stream object costs as much as a small launch
-    return _torch()._C._cuda_getCurrentRawStream(cache.device_index)
+    return C._cuda_getCurrentRawStream(device)
+
+
+def _kv_stream(cache: KVCache) -> int:
+    return _raw_stream(cache.device_index)
 
 
 def kv_append(cache: KVCache, layer: int, k, v, batch: KVBatch) -> None:
@@ -688,11 +699,6 @@ def kv_attention(cache: KVCache, layer: int, q, batch: KVBatch, causal: bool = T
     if status != OK:
         raise MloraError(status, "mlora_kv_attention")
     return out
-
-
-def _raw_stream(device: int) -> int:
-    # the handle alone: building a Stream object costs as much as a small launch
-    return _torch()._C._cuda_getCurrentRawStream(device)
 
 
 def _on_device(t, name: str, dtype, device: int, shape=None):
