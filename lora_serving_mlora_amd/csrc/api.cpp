@@ -1320,8 +1320,8 @@ constexpr int kQ4Terms = 2;
 // steps, the per-row layer takes any (and rounds its result once)
 int q4_channels(const mlora::Q4View& w, int n) { return n > kRowsMax ? mlora::q4_padded(w.K) : w.K; }
 // the low-rank inner products of the form for few rows, every slice's
-size_t q4_t_bytes(const mlora_pool* p, int n) {
-  return align256((size_t)mlora::kQ4TSlices * n * p->d.max_rank * sizeof(float));
+size_t q4_t_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
+  return align256((size_t)mlora::q4_plan(n, w.K, w.N, true).SK * n * p->d.max_rank * sizeof(float));
 }
 size_t q4_operand_bytes(const mlora::Q4View& w, int n) {
   const int Kp = q4_channels(w, n);
@@ -1332,7 +1332,7 @@ size_t q4_operand_bytes(const mlora::Q4View& w, int n) {
 size_t q4_bytes(const mlora::Q4View& w, const mlora_pool* p, int n) {
   if (n <= 0) return 0;
   if (q4_few(w, p, n))
-    return (p ? q4_t_bytes(p, n) : 0) +
+    return (p ? q4_t_bytes(w, p, n) : 0) +
            align256(mlora::q4_plan(n, w.K, w.N, p != nullptr).part_floats(n, w.N) * sizeof(float));
   const size_t operands = q4_operand_bytes(w, n);
   if (p) return operands + (n > kRowsMax ? split_work_bytes(p, n, kQ4Terms) : mlora_work_bytes(p, n));
@@ -1428,7 +1428,7 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
   if (q4_few(v, p, n)) {
     const PoolView pv = p->view();
     float* T = static_cast<float*>(work);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + q4_t_bytes(p, n));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(work) + q4_t_bytes(v, p, n));
     const int32_t* row_key = static_cast<const int32_t*>(seg_ws) + MLORA_SEG_ROWKEY(n);
     return hip_check(mlora::launch_q4_rows(v, X, n, Y, part, &pv, proj, row_key, T, as_stream(stream)),
                      "4-bit product + low-rank term launch");

@@ -57,7 +57,7 @@ struct Q4Plan {
 };
 Q4Plan q4_plan(int M, int K, int N, bool lora);
 // Y = X W^T, with row_key also the low-rank term of each row: T its scratch,
-// kQ4TSlices times [M][max_rank].
+// the plan's SK times [M][max_rank].
 hipError_t launch_q4_rows(const Q4View& w, const uint16_t* X, int M, uint16_t* Y, float* part, const PoolView* pv,
                           int proj, const int32_t* row_key, float* T, hipStream_t stream);
 
