@@ -64,3 +64,42 @@ def test_work_of_the_inner_products(M):
     pool = M.Pool(512, 64, 1, 1, rank, rank)
     assert M.q4_work_bytes(w4, n, pool) <= n * rank * 4 + n * 64 * 4 + 512
     pool.close()
+
+
+@pytest.mark.parametrize("n,din,dout", FORMS)
+def test_outputs_end_where_they_end(M, n, din, dout):
+    """Nothing is written before or behind Y, aligned or not."""
+    torch = torch_cuda()
+    say(f"guarded outputs {n}x{din}x{dout}")
+    rng = np.random.default_rng(n + din)
+    w4 = weight(M, rng, dout, din)
+    x, pool, seg = layer(M, rng, n, din, dout, [17, 8])
+    for call in (lambda Y=None: M.q4_gemm(x, w4, Y=Y), lambda Y=None: M.q4_apply(pool, 0, x, w4, seg, Y=Y)):
+        want = call()
+        assert torch.isfinite(want).all()
+        for at in (3, 8):
+            buf = torch.full((at + n * dout + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+            call(buf[at:at + n * dout].view(n, dout))
+            # (where another form takes outputs without alignment, its sums have an order of their own: a
+            # step of bf16 apart, 2^-7, doubled, and what cancels; here it is the place that is looked at)
+            near = torch.isclose(buf[at:at + n * dout].view(n, dout).float(), want.float(), rtol=2.0 ** -6, atol=0.05)
+            assert near.all() and (buf[:at] == 7).all() and (buf[at + n * dout:] == 7).all()
+    pool.close()
+
+
+@pytest.mark.parametrize("n,din,dout", [(1, 256, 45), (17, 1056, 40), (70, 1056, 40), (300, 2080, 41), (1100, 160, 2880)])
+@pytest.mark.parametrize("odd", [1, 2, 3])
+def test_scales_at_any_address(M, n, din, dout, odd):
+    """Scale bytes that begin at no word's address give the same bits."""
+    torch = torch_cuda()
+    say(f"scales {odd} bytes on, {n}x{din}x{dout}")
+    rng = np.random.default_rng(n)
+    w4 = weight(M, rng, dout, din, odd)
+    again = M.Q4Weight(w4.codes, w4.scales.clone())
+    assert w4.scales.data_ptr() % 4 == odd and again.scales.data_ptr() % 4 == 0
+    x, pool, seg = layer(M, rng, n, din, dout, [17, 8])
+    bits = lambda t: t.view(torch.int16)
+    assert torch.equal(bits(M.q4_dequantize(w4)), bits(M.q4_dequantize(again)))
+    assert torch.equal(bits(M.q4_gemm(x, w4)), bits(M.q4_gemm(x, again)))
+    assert torch.equal(bits(M.q4_apply(pool, 0, x, w4, seg)), bits(M.q4_apply(pool, 0, x, again, seg)))
+    pool.close()
