@@ -192,7 +192,7 @@ __device__ __forceinline__ void shrink_items(const PoolView& pv, int proj, const
   }
 }
 
-// The body of q4_rows_kernel.  x0 .. x3: LDS for a step, a slot of every
+// The body of q4_rows_kernel.  x0 .. x2: LDS for a step, a slot of every
 // wave's (16 * MB rows of 256 bytes of X, 16 * CG of 64 bytes of codes); arrays
 // of their own, so that the compiler knows that reads of one do not wait for
 // what is on its way into another (the first D of them are used).
@@ -201,8 +201,8 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
                                              uint16_t* __restrict__ Y, float* __restrict__ part, const PoolView& pv,
                                              int proj, const int32_t* __restrict__ row_key, float* __restrict__ T,
                                              int SK, uint8_t* __restrict__ x0, uint8_t* __restrict__ x1,
-                                             uint8_t* __restrict__ x2, uint8_t* __restrict__ x3) {
-  static_assert(CG <= 4 && D >= 2 && D <= 4, "the waves' sums fit in a slot; slots are named below");
+                                             uint8_t* __restrict__ x2) {
+  static_assert(CG <= 4 && D >= 2 && D <= 3, "the waves' sums fit in a slot; slots are named below");
   const int K = w.K, N = w.N, G = K / kQ4Group;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -252,7 +252,7 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
     }
     asm volatile("" ::: "memory");
   };
-  auto slot_of = [&](int d) { return d == 0 ? x0 : (d == 1 ? x1 : (d == 2 ? x2 : x3)); };
+  auto slot_of = [&](int d) { return d == 0 ? x0 : (d == 1 ? x1 : x2); };
   // (each row's adapter and rank, for later: loaded here, they are waited for
   // with the first steps)
   const int key = LORA && lane < M ? row_key[m0 + lane] : -1;
@@ -331,9 +331,7 @@ __device__ __forceinline__ void q4_rows_body(const Q4View& w, const uint16_t* __
   }
 #pragma unroll
   for (int d = 0; d < D; ++d) {  // the last steps
-    if (D - 1 - d == 3)
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(3 * kLoads));
-    else if (D - 1 - d == 2)
+    if (D - 1 - d == 2)
       __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * kLoads));
     else if (D - 1 - d == 1)
       __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));
@@ -380,8 +378,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     Q4View w, const uint16_t* __restrict__ X, int M, int S, uint16_t* __restrict__ Y, float* __restrict__ part,
     PoolView pv, int proj, const int32_t* __restrict__ row_key, float* __restrict__ T, int SK) {
   constexpr int kSlot = NW * (MB * 4096 + CG * 1024);
-  __shared__ __attribute__((aligned(16))) uint8_t x0[kSlot], x1[kSlot], x2[D > 2 ? kSlot : 16], x3[D > 3 ? kSlot : 16];
-  q4_rows_body<MB, CG, NW, D, LORA>(w, X, M, S, Y, part, pv, proj, row_key, T, SK, x0, x1, x2, x3);
+  __shared__ __attribute__((aligned(16))) uint8_t x0[kSlot], x1[kSlot], x2[D > 2 ? kSlot : 16];
+  q4_rows_body<MB, CG, NW, D, LORA>(w, X, M, S, Y, part, pv, proj, row_key, T, SK, x0, x1, x2);
 }
 
 // Sums the S slices' partial products in order, adds the row's low-rank term
