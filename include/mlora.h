@@ -623,8 +623,8 @@ mlora_status mlora_qk_norm_rotary(const mlora_kv_batch* batch, int32_t dim, cons
  *   top_p:       device float [n_rows], 1 or more (or NaN): all.  NULL: all
  *   min_p:       device float [n_rows], 0 or less (or NaN): all.  NULL: all
  *   out:         device int32 [n_rows]
- *   work:        device scratch of mlora_sample_work_bytes() bytes, 256-byte
- *                aligned, contents free; calls that share it must not overlap
+ *   work:        reserved: mlora_sample_work_bytes() is 0, the contents are
+ *                not used, and NULL will do; 256-byte aligned where given
  * NaN logits count as -infinity; where the largest is +infinity, the tokens
  * that have it share the weight; a row without any logit above -infinity
  * gives -1.  Sums are exact, so the result does not depend on their order.

@@ -909,13 +909,14 @@ def qk_norm_rotary(q, k, batch: KVBatch, rotary: Rotary, q_weight=None, k_weight
 
 
 def sample_work_bytes(n: int, vocab: int) -> int:
+    """0: sample() needs no work buffer (the argument is reserved)."""
     return int(lib().mlora_sample_work_bytes(n, vocab))
 
 
 def new_sample_work(n: int, vocab: int, device=None):
-    """A work buffer for sample() of n rows of `vocab` logits."""
+    """A work buffer for sample() of n rows of `vocab` logits: an empty one."""
     torch = _torch()
-    return torch.empty(max(sample_work_bytes(n, vocab), 256), dtype=torch.uint8,
+    return torch.empty(sample_work_bytes(n, vocab), dtype=torch.uint8,
                        device=device if device is not None else torch.device("cuda", torch.cuda.current_device()))
 
 
@@ -943,9 +944,6 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
     wp = wn = 0
     if work is not None:
         wp, wn = _work(work, device).data_ptr(), work.nbytes
-    elif sample_work_bytes(n, vocab):
-        work = new_sample_work(n, vocab, logits.device)
-        wp, wn = work.data_ptr(), work.nbytes
     status = lib().mlora_sample(logits.data_ptr(), logits.dtype is torch.float32, logits.stride(0) if n > 1 else vocab,
                                 n, vocab, u.data_ptr(), *ptr, out.data_ptr(), wp, wn, _raw_stream(device))
     if status != OK:

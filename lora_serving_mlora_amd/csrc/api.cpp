@@ -1564,14 +1564,12 @@ mlora_status mlora_qk_norm_rotary(const mlora_kv_batch* b, int32_t dim, const ml
 
 static_assert(mlora::kSampleMaxVocab == MLORA_MAX_VOCAB, "the header states the largest vocabulary");
 
-size_t mlora_sample_work_bytes(int32_t n, int32_t vocab) {
-  if (n < 0 || n > MLORA_MAX_ROWS || vocab < 1 || vocab > MLORA_MAX_VOCAB) return 0;
-  return n == 0 ? 0 : mlora::sample_work_bytes(n, vocab);
-}
+// A row is one workgroup's, which needs no memory but its LDS.
+size_t mlora_sample_work_bytes(int32_t, int32_t) { return 0; }
 
 mlora_status mlora_sample(const void* logits, int32_t is_f32, int64_t row_stride, int32_t n, int32_t vocab,
                           const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
-                          const float* min_p, int32_t* out, void* work, size_t work_bytes, void* stream) {
+                          const float* min_p, int32_t* out, void* work, size_t, void* stream) {
   g_err.clear();
   if (n < 0 || n > MLORA_MAX_ROWS) return fail(MLORA_EINVAL, "n_rows %d outside [0, %d]", n, MLORA_MAX_ROWS);
   if (vocab < 1 || vocab > MLORA_MAX_VOCAB) return fail(MLORA_EINVAL, "vocab %d outside [1, 2^20]", vocab);
@@ -1581,12 +1579,9 @@ mlora_status mlora_sample(const void* logits, int32_t is_f32, int64_t row_stride
   if (!logits || !u || !out) return fail(MLORA_EINVAL, "logits, u and out must not be NULL");
   if (reinterpret_cast<uintptr_t>(logits) % (is_f32 ? 4 : 2) != 0)
     return fail(MLORA_EINVAL, "logits must be aligned to their elements");
-  const size_t need = mlora::sample_work_bytes(n, vocab);
-  if (need > 0 && (!work || work_bytes < need))
-    return fail(MLORA_EINVAL, "work: %zu bytes given, %zu needed", work_bytes, need);
   if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0) return fail(MLORA_EINVAL, "work must be 256-byte aligned");
   const mlora::SampleArgs a{logits, row_stride, n, vocab, is_f32 != 0, u, temperature, top_k, top_p, min_p, out};
-  return hip_check(mlora::launch_sample(a, work, as_stream(stream)), "sampling launch");
+  return hip_check(mlora::launch_sample(a, as_stream(stream)), "sampling launch");
 }
 
 }  // extern "C"

@@ -19,7 +19,6 @@ struct SampleArgs {
   const float* min_p;
   int32_t* out;
 };
-size_t sample_work_bytes(int n, int V);
-hipError_t launch_sample(const SampleArgs& a, void* work, hipStream_t stream);
+hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 
 }  // namespace mlora

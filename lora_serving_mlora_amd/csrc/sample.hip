@@ -1014,9 +1014,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
 
 }  // namespace
 
-size_t sample_work_bytes(int n, int V) { return 0; }
-
-hipError_t launch_sample(const SampleArgs& a, void* work, hipStream_t stream) {
+hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
   if (a.f32)
     MLORA_LAUNCH("sample", sample_kernel<float>, dim3(a.n), dim3(kThreads), 0, stream, a);
   else
