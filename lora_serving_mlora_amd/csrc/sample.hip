@@ -118,7 +118,7 @@ struct Row {
 };
 
 // Weight of a logit, in multiples of 2^-42.  ANY: of any clean logit; else of
-// one above r.least.
+// one that is not below r.least.
 template <bool ANY = false>
 __device__ __forceinline__ u64 weight(const Row& r, float x) {
   double d = ((double)x - r.mx) * r.scale;
@@ -158,6 +158,11 @@ __device__ __forceinline__ float from_rising(uint32_t k) {
 }
 __device__ __forceinline__ float next_up(float x) { return from_rising(rising(x) + 1); }
 __device__ __forceinline__ float next_down(float x) { return from_rising(rising(x) - 1); }
+
+// The temperature, or for one far below a last place of the largest logit the
+// 64th part of that: a logit a place or more down has no weight either way, and
+// the exponents stay within reach of `weight` (-44.7 - 2.2 * 64).
+__device__ __forceinline__ float warm(float mx, float temp) { return fmaxf(temp, (mx - next_down(mx)) * 0.015625f); }
 
 // A logit below the largest from which on, down, every weight is 0: 31 nats
 // down (44.7 powers of two).  The difference is rounded, to `mx` itself where
@@ -297,13 +302,11 @@ __device__ __forceinline__ u64 histogram(S& sh, const Row& r, const T* __restric
       const float x = fmaxf(xs[e], r.least);
       const u64 w = weight(r, x);
       const int b = range_of(r, x);
-      // (at r.least, where all lower logits are taken to, w is 0 or, at a
-      // temperature far below the last place of a logit, nothing at all)
       if (x > r.least) {
         atomicAdd(&sh.bins.mass[b], w);
         if (counts) atomicAdd(&sh.bins.count[b], 1u);
-        if (least != 0 && w >= least) strong += w;
       }
+      if (least != 0 && w >= least) strong += w;
       if (e & 1) __builtin_amdgcn_sched_barrier(0);  // keeps the next logits' work out of the registers
     }
   });
@@ -697,6 +700,7 @@ __device__ __forceinline__ bool sample_values(S& sh, const uint16_t* __restrict_
   int place = -1;
   if (temp > 0.f) {
     if (!(fabsf(mx) <= 1e30f && temp >= 1e-20f && temp <= 1e20f)) return false;
+    temp = warm(mx, temp);
     Row r;
     r.mx = mx;
     r.scale = 1.4426950408889634074 / (double)temp;
@@ -788,7 +792,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   constexpr int E = 16 / sizeof(T);
   const int row_i = blockIdx.x, V = a.V, tid = threadIdx.x;
   const T* row = static_cast<const T*>(a.logits) + row_i * a.stride;
-  const float temp = a.temperature ? a.temperature[row_i] : 1.f;
+  float temp = a.temperature ? a.temperature[row_i] : 1.f;
   const int top_k = a.top_k ? a.top_k[row_i] : 0;
   const float top_p = a.top_p ? a.top_p[row_i] : 1.f;
   const float min_p = a.min_p ? a.min_p[row_i] : 0.f;
@@ -856,7 +860,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
   const bool limit_p = top_p < 1.f;
   // The ranges run over what has a weight, down to 30 nats or the smallest
   // logit.  Numbers past those of any model take the passes of `reach` alone.
-  bool plain = fabsf(mx) <= 1e30f && temp >= 1e-20f && temp <= 1e20f;
+  const bool plain = fabsf(mx) <= 1e30f && temp >= 1e-20f && temp <= 1e20f;
+  if (plain) temp = warm(mx, temp);
   if (r.top) mx = mn = 0.f;
   r.mx = mx;
   r.scale = 1.4426950408889634074 / (double)temp;
