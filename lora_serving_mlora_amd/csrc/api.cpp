@@ -1471,6 +1471,10 @@ HeadSpan head_span(const uint16_t* p, int64_t rs, int64_t hs, int n, int heads, 
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
   return {a, a + 2 * (uintptr_t)((n - 1) * rs + (heads - 1) * hs + dim)};
 }
+// n pieces of dim elements `inner` apart, and m such runs `outer` apart, share none
+bool apart(int n, int64_t inner, int m, int64_t outer, int dim) {
+  return (n == 1 || inner >= dim) && (m == 1 || outer >= (n - 1) * inner + dim);
+}
 bool overlap(const HeadSpan& a, const HeadSpan& b) { return a.first < b.last && b.first < a.last; }
 // Two sets of heads that interleave as slices of the same rows: every row of
 // one lies between the rows of the other.
@@ -1523,9 +1527,9 @@ mlora_status mlora_qk_norm_rotary(const mlora_kv_batch* b, int32_t dim, const ml
       if (x < 0 || x > INT32_MAX) return fail(MLORA_EINVAL, "stride %lld outside [0, 2^31)", (long long)x);
     if (b->n_rows == 0) continue;
     if (!s->x || !s->y) return fail(MLORA_EINVAL, "x and y must not be NULL");
-    // the heads of the output lie apart
-    if ((s->heads > 1 && s->out_head_stride < dim) ||
-        (b->n_rows > 1 && s->out_row_stride < (s->heads - 1) * s->out_head_stride + dim))
+    // the heads of the output lie apart: the heads of a row together, or the rows of a head
+    if (!apart(s->heads, s->out_head_stride, b->n_rows, s->out_row_stride, dim) &&
+        !apart(b->n_rows, s->out_row_stride, s->heads, s->out_head_stride, dim))
       return fail(MLORA_EINVAL, "output heads overlap: strides %lld, %lld", (long long)s->out_row_stride,
                   (long long)s->out_head_stride);
     a.side[i] = {s->x, s->y, s->row_stride, s->head_stride, s->out_row_stride, s->out_head_stride, s->weight, s->heads};
