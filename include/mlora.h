@@ -558,7 +558,10 @@ mlora_status mlora_q4_dequantize(const mlora_q4_weight* w, uint16_t* W, void* st
  * sum of two bf16 numbers (to 2^-16 of it).  Y is rounded once, but for batches
  * of more than 1024 rows whose X or bf16 weight has 2^30 numbers or more, or
  * whose adapters' ranks, each padded to 16, times 4 dout bytes pass some 500
- * MiB: there the product is rounded to bf16 before the adapters are added.
+ * MiB, or while an adapter is resident whose Up holds an infinity or NaN: there
+ * the product is rounded to bf16 before the adapters are added.  Such an
+ * adapter reaches its own rows only, in a plan that was chosen with it resident
+ * (a captured graph keeps the one that it was captured with).
  * Results are the same bit for bit from call to call. */
 size_t mlora_q4_work_bytes(const mlora_q4_weight* w, const mlora_pool* pool, int32_t n_rows);
 mlora_status mlora_q4_gemm(const mlora_q4_weight* w, const uint16_t* X, uint16_t* Y, int32_t n_rows, void* work,

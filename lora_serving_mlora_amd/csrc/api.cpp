@@ -198,6 +198,10 @@ struct mlora_pool {
   std::vector<float> scale;
   std::vector<RangeAlloc::Runs> druns, uruns;
   int32_t n_resident = 0;
+  // resident adapters whose Up holds an infinity or NaN: products that take
+  // all of a batch's adapters side by side would carry it to every row
+  std::vector<uint8_t> broken;
+  std::atomic<int32_t> n_broken{0};
   void* stage[2] = {nullptr, nullptr};
   hipEvent_t ev[2] = {nullptr, nullptr};
   bool pending[2] = {false, false};
@@ -434,6 +438,7 @@ mlora_status mlora_pool_create(const mlora_pool_desc* desc, void* stream, mlora_
   p->rank.assign(d.max_adapters, 0);
   p->scale.assign(d.max_adapters, 0.f);
   p->druns.resize(d.max_adapters);
+  p->broken.assign(d.max_adapters, 0);
   p->uruns.resize(d.max_adapters);
   p->ready.assign(d.max_adapters, nullptr);
   auto cleanup = [&](mlora_status st) {
@@ -557,7 +562,9 @@ mlora_status mlora_pool_load(mlora_pool* p, int32_t id, int32_t rank, float scal
     bool upr;   // Up row (column q of Up for projection p), else Down row
   };
   std::vector<Fill> fills;
+  std::atomic<bool> broken{false};
   auto fill_range = [&](size_t b, size_t e) {
+    uint32_t top = 0;  // the largest exponent of Up
     for (size_t k = b; k < e; ++k) {
       const Fill& f = fills[k];
       if (!f.upr) {
@@ -565,9 +572,13 @@ mlora_status mlora_pool_load(mlora_pool* p, int32_t id, int32_t rank, float scal
       } else {
         uint16_t* row = reinterpret_cast<uint16_t*>(f.h);
         const uint16_t* src = up + (size_t)(f.i / rank) * d.dout * rank + f.i % rank;
-        for (int32_t c = 0; c < d.dout; ++c) row[c] = src[(size_t)c * rank];
+        for (int32_t c = 0; c < d.dout; ++c) {
+          row[c] = src[(size_t)c * rank];
+          top = std::max<uint32_t>(top, row[c] & 0x7f80u);
+        }
       }
     }
+    if (top == 0x7f80u) broken = true;
   };
   sg.on_flush([&]() {
     const size_t n = fills.size();
@@ -627,6 +638,8 @@ mlora_status mlora_pool_load(mlora_pool* p, int32_t id, int32_t rank, float scal
   p->druns[id] = dr;
   p->uruns[id] = ur;
   ++p->n_resident;
+  p->broken[id] = broken ? 1 : 0;
+  p->n_broken += p->broken[id];
   return MLORA_OK;
 }
 
@@ -665,6 +678,7 @@ mlora_status mlora_pool_unload(mlora_pool* p, int32_t id, void* stream) {
   p->rank[id] = 0;
   p->scale[id] = 0.f;
   --p->n_resident;
+  p->n_broken -= p->broken[id];
   return MLORA_OK;
 }
 
@@ -1444,8 +1458,9 @@ mlora_status mlora_q4_apply(const mlora_pool* p, int32_t proj, const uint16_t* X
   PoolView vb = p->view();
   vb.din = q4_channels(v, n);
   // Whatever the size: the product alone, with the adapters added to it as
-  // bf16, would be rounded twice.
-  if (big_epilogue_fits(p, n, kQ4Terms) && mlora::big_lora_takes(vb, Xb, W, n))
+  // bf16, would be rounded twice.  (That keeps an infinity of one adapter's Up
+  // to its own rows, though.)
+  if (p->n_broken == 0 && big_epilogue_fits(p, n, kQ4Terms) && mlora::big_lora_takes(vb, Xb, W, n))
     return apply_big(p, proj, X, vb, Xb, W, ws, Y, n, rest, kQ4Terms, s);
   st = hip_check(mlora::launch_base_gemm(Xb, W, Y, n, vb.din, v.N, s), "base GEMM launch");
   if (st != MLORA_OK) return st;
