@@ -564,7 +564,7 @@ mlora_status mlora_pool_load(mlora_pool* p, int32_t id, int32_t rank, float scal
   std::vector<Fill> fills;
   std::atomic<bool> broken{false};
   auto fill_range = [&](size_t b, size_t e) {
-    uint32_t top = 0;  // the largest exponent of Up
+    int16_t top = 0;  // the largest exponent of Up
     for (size_t k = b; k < e; ++k) {
       const Fill& f = fills[k];
       if (!f.upr) {
@@ -572,13 +572,12 @@ mlora_status mlora_pool_load(mlora_pool* p, int32_t id, int32_t rank, float scal
       } else {
         uint16_t* row = reinterpret_cast<uint16_t*>(f.h);
         const uint16_t* src = up + (size_t)(f.i / rank) * d.dout * rank + f.i % rank;
-        for (int32_t c = 0; c < d.dout; ++c) {
-          row[c] = src[(size_t)c * rank];
-          top = std::max<uint32_t>(top, row[c] & 0x7f80u);
-        }
+        for (int32_t c = 0; c < d.dout; ++c) row[c] = src[(size_t)c * rank];
+        // (a loop of its own, which takes eight at a time)
+        for (int32_t c = 0; c < d.dout; ++c) top = std::max<int16_t>(top, (int16_t)(row[c] & 0x7f80));
       }
     }
-    if (top == 0x7f80u) broken = true;
+    if (top == 0x7f80) broken = true;
   };
   sg.on_flush([&]() {
     const size_t n = fills.size();
