@@ -1324,10 +1324,9 @@ bool q4_few(const mlora::Q4View& w, const mlora_pool* p, int n) {
   return mlora::q4_few_rows(n, w.K, w.N) && (!p || aligned16(p->d.down_pages));
 }
 // Numbers that stand for a low-rank inner value where many rows take it in
-// bf16: two, which leave the layer's result as it is with fp32 values; one moved
-// it by up to a half of its last place (4096 rows of 4096 -> 11008 channels, ranks 8, 16, 64
-// twice: the error against 64 bits 2.02e-3 of the result, 1.66e-3 with two
-// numbers, as of the last rounding alone).
+// bf16: two, which leave the result as fp32 values do (4096 rows of 4096 ->
+// 11008 channels, ranks 8, 16, 64 twice: 1.66e-3 of it from 64 bits, as the last
+// rounding alone, and 361 us; with one number 2.02e-3 and 346 us).
 constexpr int kQ4Terms = 2;
 // channels of a row of the bf16 weight: the products of many rows want whole
 // steps, the per-row layer takes any (and rounds its result once)

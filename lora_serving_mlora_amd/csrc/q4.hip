@@ -101,8 +101,9 @@ __global__ __launch_bounds__(kConvThreads) void q4_pad_kernel(Q4View w, const ui
 // of them need the same codes or the same part of X, and there is no barrier
 // before the shares are summed through LDS in order.
 // Codes and X come through LDS all the same, a wave's own: whole row pieces (64
-// bytes of codes, 256 of X) whose 16-byte chunks are XOR-ed with the row, so
-// that the 16 rows of an operand hit different banks.  (Operands loaded from
+// bytes of codes, 256 of X) whose 16-byte chunks are XOR-ed with the row, since
+// the 16 rows of an operand would all hit the same banks otherwise; conflicts
+// still take 38 to 44 % of the cycles in which LDS is read.  (Operands loaded from
 // memory as they are have a row to a lane, which the address unit takes four
 // times as long for: 61 rows of 11008 channels 23.5 us, X alone through LDS
 // 18.8.)
@@ -563,10 +564,11 @@ bool q4_few_rows(int M, int K, int N) {
   // The bf16 products have a rate that these do not reach, but the weight has
   // to be made first, and a small product does not reach it either (4096
   // channels, three adapters of rank 16; as they are against bf16 first: 256
-  // rows x 4096 27.5 and 32.8 us, 600 x 4096 60 and 62, 1500 x 2048 66 and 75,
-  // 400 x 11008 96 and 88, 1024 x 4096 88 and 67, 4000 x 1000 92 and 78; 800 x
-  // 1024 of 1024 channels 17 and 33).  Where K is not whole steps or N not
-  // whole vectors they are slower still (1024 x 4096, K 4064: 82 and 234 us).
+  // rows x 4096 27.3 and 38.5 us, 600 x 4096 61 and 68, 1500 x 2048 66 and 63,
+  // without adapters 46 and 58, 400 x 11008 96 and 88, 1024 x 4096 88 and 67,
+  // 4000 x 1000 92 and 75; 800 x 1024 of 1024 channels 17 and 30).  Where K is
+  // not whole steps or N not whole vectors they are slower still (1024 x 4096,
+  // K 4064: 83 and 238 us).
   if (K < kQ4MinDin) return false;
   if (M <= 256 || (long)M * N <= 3l << 20) return true;
   return (K % kStep != 0 || N % 8 != 0) && M <= 1024;
